@@ -289,6 +289,89 @@ int moe_shared_expert_forward(const uint16_t* x, int T, int H, int I, const uint
                               const uint16_t* w_down, float limit, void* ws, size_t ws_bytes, uint16_t* shared_out,
                               void* stream);
 
+/* ---------------------------------------------------------------- FP8 experts */
+/*
+ * Block-scaled FP8 (W8A8): E4M3 codes with one FP32 scale for each 128 columns of an activation
+ * row and for each 128 x 128 block of a weight (groups start at column and row 0; the last ones may
+ * be shorter).  A value is code * scale.  The quantisers make the operands of the products, and the
+ * gate/up product makes the operands of the down product.
+ *
+ * Codes are uint8 E4M3 ("FN": no infinities, 0x7F / 0xFF are NaN), 16-byte aligned, rows `ld` bytes
+ * apart, ld % 16 == 0 and ld >= K.  K, N and R may be any number (the bytes between K and ld are
+ * not read).  Activation scales of (row r, group g) lie at s[r * s_row + g * s_grp] (float elements):
+ * any layout; group-major (s_row = 1) is the one whose reads coalesce in the products.  Weight
+ * scales are [count][ceil(N / 128)][ceil(K / 128)], contiguous.
+ */
+typedef struct {
+  const uint8_t* q;      /* device E4M3 [rows, ld] */
+  int64_t ld;
+  const float* s;        /* device FP32 scales */
+  int64_t s_row, s_grp;
+  int rows;
+} moe_fp8_rows;
+
+typedef struct {
+  const uint8_t* q;      /* device E4M3 [count][N, ld], experts expert_stride bytes apart (% 16 == 0) */
+  int64_t ld, expert_stride;
+  const float* s;        /* device FP32 [count][ceil(N/128)][ceil(K/128)] */
+  int first, count;      /* this weight holds the experts first .. first + count - 1 of a call's E */
+  int N, K;
+} moe_fp8_weight;
+
+#define MOE_FP8_MAX_EXPERTS 512
+
+/*
+ * Rows to codes and scales: for each group of 128 columns of a row, in FP32,
+ *   a = max(max |x|, 2^-100),  s = a / 448,  q = e4m3(x * (448 / a))  (round to nearest even).
+ * A group of zeros gives codes 0; a group holding an infinity or a NaN gives s = NaN and NaN codes.
+ *   x     device BF16 or FP32 (x_dtype) [R, ld_x], ld_x >= K; any alignment of its element type
+ *         (rows on 16-byte boundaries are read with wide loads)
+ *   q, s  device outputs, laid out as above
+ * R = 0 does nothing.
+ */
+int moe_fp8_quantize_rows(const void* x, int x_dtype, int64_t ld_x, int R, int K, uint8_t* q, int64_t ld_q, float* s,
+                          int64_t s_row, int64_t s_grp, void* stream);
+/* The same over 128 x 128 blocks of a weight w [N, ld_w]: s [ceil(N/128)][ceil(K/128)]. */
+int moe_fp8_quantize_blocks(const void* w, int w_dtype, int64_t ld_w, int N, int K, uint8_t* q, int64_t ld_q, float* s,
+                            void* stream);
+
+/*
+ * Dense product: C[r, n] = sum_k A[r, k] W[n, k] over the dequantised values, as
+ *   sum over groups g of sa[r, g] * sw[n/128, g] * (sum over k in g of the codes' products),
+ * the inner sums by FP8 tensor-core MMAs with FP32 accumulation, the outer in FP32; C is BF16
+ * (rounded to nearest even) or FP32 [A->rows, ldc], ldc >= N, ldc % 8 == 0, 16-byte aligned.
+ * W->first = 0, W->count = 1.
+ */
+int moe_fp8_gemm(const moe_fp8_rows* A, const moe_fp8_weight* W, void* C, int64_t ldc, int c_dtype, void* stream);
+
+/*
+ * The same for all experts in one launch: sorted rows p in [expert_offsets[e], expert_offsets[e+1])
+ * of C take expert e's weight and row gather_ids[p] of A (row p when gather_ids is NULL, then
+ * A->rows >= R).
+ *   expert_offsets device int32 [E+1], non-decreasing from 0, expert_offsets[E] <= R (else
+ *              MOE_DEVERR_BAD_OFFSETS and nothing is written); rows past expert_offsets[E] are not
+ *              touched
+ *   gather_ids device int32 [R] or NULL; an index outside [0, A->rows) reads row 0
+ *              (MOE_DEVERR_BAD_GATHER)
+ * Rows of experts that W does not hold (expert parallelism) are written as zeros.
+ * Requirements: 1 <= E <= MOE_FP8_MAX_EXPERTS, 0 <= first, 1 <= count, first + count <= E; R = 0 does
+ * nothing.  The launch reads expert_offsets on the device: no host round trip, capturable.
+ */
+int moe_fp8_grouped_gemm(const moe_fp8_rows* A, const int32_t* gather_ids, const moe_fp8_weight* W,
+                         const int32_t* expert_offsets, int E, int R, void* C, int64_t ldc, int c_dtype, void* stream);
+
+/*
+ * The gate/up product with the clamped SwiGLU and the row quantiser in its epilogue: W has N = 2 I
+ * rows (0..I-1 gate, I..2I-1 up), I % 128 == 0, and
+ *   act[p, j] = silu(min(g, L)) * clamp(u, -L, L)  of the FP32 sums g = C[p, j], u = C[p, I + j]
+ * is quantised per row and 128 columns as by moe_fp8_quantize_rows (its FP32 values, no BF16
+ * rounding between): act device E4M3 [R, ld_act], act_s its scales -- the A of the down product.
+ * A NaN sum gives a NaN act.  Rows of experts W does not hold are quantised zeros.
+ */
+int moe_fp8_grouped_gemm_swiglu(const moe_fp8_rows* A, const int32_t* gather_ids, const moe_fp8_weight* W,
+                                const int32_t* expert_offsets, int E, int R, float limit, uint8_t* act, int64_t ld_act,
+                                float* act_s, int64_t act_s_row, int64_t act_s_grp, void* stream);
+
 /* ---------------------------------------------------------------- fused forward */
 typedef struct {
   int hidden;             /* H */

@@ -29,6 +29,8 @@ __all__ = [
     "MOE_DTYPE_BF16", "MOE_DTYPE_F32", "MOE_FWD_NUM_EVENTS", "DEVERR",
     "moe_debug_set_gemm_kernel", "moe_debug_set_wait_limit_ns", "MOE_GEMM_KERNEL_AUTO", "MOE_GEMM_KERNEL_SINGLE",
     "MOE_GEMM_KERNEL_PAIR", "gemm_kernel", "moe_debug_grouped_gemm_after",
+    "moe_fp8_quantize_rows", "moe_fp8_quantize_blocks", "moe_fp8_gemm", "moe_fp8_grouped_gemm",
+    "moe_fp8_grouped_gemm_swiglu", "MOE_FP8_BLOCK", "MOE_FP8_MAX_EXPERTS",
 ]
 
 HEADER = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include", "moe_prefill.h")
@@ -44,6 +46,8 @@ MOE_SORT_NOALLOC_MAX_INTS = 65536  # int32 entries of the library's fixed sort s
 MOE_GEMM_KERNEL_AUTO = 0  # moe_debug_set_gemm_kernel: CTA-pair kernel where its shapes allow
 MOE_GEMM_KERNEL_SINGLE = 1  # the single-CTA kernel
 MOE_GEMM_KERNEL_PAIR = 2  # the CTA-pair kernel only (other shapes are refused)
+MOE_FP8_BLOCK = 128  # elements per scale of the FP8 formats (rows: 128 columns, weights: 128 x 128)
+MOE_FP8_MAX_EXPERTS = 512
 STATUS = {0: "MOE_OK", 1: "MOE_ERR_INVALID_ARG", 2: "MOE_ERR_UNSUPPORTED_SHAPE", 3: "MOE_ERR_WORKSPACE_TOO_SMALL",
           4: "MOE_ERR_CUDA", 5: "MOE_ERR_DEVICE", 6: "MOE_ERR_NOT_BUILT_FOR_DEVICE", 7: "MOE_ERR_SCRATCH_LIMIT"}
 DEVERR = {0: "none", 1: "bad expert id", 2: "bad expert offsets", 3: "pipeline wait timeout", 4: "NaN logit",
@@ -76,6 +80,16 @@ _I64 = ctypes.c_int64
 _F = ctypes.c_float
 _SZ = ctypes.c_size_t
 
+
+class Fp8Rows(ctypes.Structure):
+    _fields_ = [("q", _P), ("ld", _I64), ("s", _P), ("s_row", _I64), ("s_grp", _I64), ("rows", _I)]
+
+
+class Fp8Weight(ctypes.Structure):
+    _fields_ = [("q", _P), ("ld", _I64), ("expert_stride", _I64), ("s", _P), ("first", _I), ("count", _I), ("N", _I),
+                ("K", _I)]
+
+
 _SIGS = {
     "moe_version": (ctypes.c_char_p, []),
     "moe_status_string": (ctypes.c_char_p, [_I]),
@@ -101,6 +115,13 @@ _SIGS = {
                                  ctypes.POINTER(_P), _P]),
     "moe_shared_expert_workspace_bytes": (_SZ, [_I, _I, _I]),
     "moe_shared_expert_forward": (_I, [_P, _I, _I, _I, _P, _P, _P, _F, _P, _SZ, _P, _P]),
+    "moe_fp8_quantize_rows": (_I, [_P, _I, _I64, _I, _I, _P, _I64, _P, _I64, _I64, _P]),
+    "moe_fp8_quantize_blocks": (_I, [_P, _I, _I64, _I, _I, _P, _I64, _P, _P]),
+    "moe_fp8_gemm": (_I, [ctypes.POINTER(Fp8Rows), ctypes.POINTER(Fp8Weight), _P, _I64, _I, _P]),
+    "moe_fp8_grouped_gemm": (_I, [ctypes.POINTER(Fp8Rows), _P, ctypes.POINTER(Fp8Weight), _P, _I, _I, _P, _I64, _I,
+                                  _P]),
+    "moe_fp8_grouped_gemm_swiglu": (_I, [ctypes.POINTER(Fp8Rows), _P, ctypes.POINTER(Fp8Weight), _P, _I, _I, _F, _P,
+                                         _I64, _P, _I64, _I64, _P]),
     "moe_get_device_error": (_I, [_P, ctypes.POINTER(_I)]),
     "moe_debug_set_gemm_kernel": (_I, [_I]),
     "moe_debug_set_wait_limit_ns": (ctypes.c_ulonglong, [ctypes.c_ulonglong]),
@@ -429,6 +450,185 @@ def moe_shared_expert_forward(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch
     _check(lib().moe_shared_expert_forward(_ptr(x), T, H, I, _ptr(w_gate), _ptr(w_up), _ptr(w_down), limit, _ptr(ws),
                                            ws.numel(), _ptr(out), _stream(stream)), "moe_shared_expert_forward")
     return out
+
+
+# ------------------------------------------------------------------------------------------ FP8
+
+
+def _fp8_codes(rows: int, cols: int, device) -> torch.Tensor:
+    """Uninitialised E4M3 [rows, cols] whose rows are whole 16-byte pieces apart (a view when cols is
+    not a multiple of 16)."""
+    ld = (cols + 15) // 16 * 16
+    t = torch.empty(rows, ld, dtype=torch.float8_e4m3fn, device=device)
+    return t if ld == cols else t[:, :cols]
+
+
+def _fp8_row_scales(rows: int, cols: int, device) -> torch.Tensor:
+    """Uninitialised FP32 [rows, ceil(cols/128)] stored group by group."""
+    return torch.empty((cols + 127) // 128, rows, dtype=torch.float32, device=device).t()
+
+
+def _need_codes(t: torch.Tensor, name: str):
+    if not t.is_cuda or t.dtype != torch.float8_e4m3fn or t.stride(-1) != 1 and t.shape[-1] != 1:
+        raise ValueError(f"{name}: need a CUDA {torch.float8_e4m3fn} tensor with unit column stride, got {t.dtype} on "
+                         f"{t.device}, strides {tuple(t.stride())}")
+
+
+def _fp8_dtype(t: torch.Tensor, name: str) -> int:
+    if t.dim() != 2 or not t.is_cuda or t.dtype not in (torch.bfloat16, torch.float32) or (
+            t.stride(1) != 1 and t.shape[1] != 1):
+        raise ValueError(f"{name}: need a CUDA BF16 or FP32 matrix with unit column stride, got {t.dtype} on {t.device}")
+    return MOE_DTYPE_BF16 if t.dtype == torch.bfloat16 else MOE_DTYPE_F32
+
+
+def _ld(t: torch.Tensor) -> int:
+    """Row stride; of a single row (whose stride torch leaves arbitrary) whole 16-byte pieces."""
+    return t.stride(-2) if t.shape[-2] > 1 else max(t.stride(-2), (t.shape[-1] + 15) // 16 * 16)
+
+
+def moe_fp8_quantize_rows(x: torch.Tensor, out: Optional[torch.Tensor] = None, scales: Optional[torch.Tensor] = None,
+                          stream=None):
+    """Rows [R, K] (BF16 or FP32, any row stride) -> (E4M3 [R, K], FP32 [R, ceil(K/128)])."""
+    dt = _fp8_dtype(x, "x")
+    R, K = x.shape
+    if out is None:
+        out = _fp8_codes(R, K, x.device)
+    else:
+        _need_codes(out, "out")
+    if scales is None:
+        scales = _fp8_row_scales(R, K, x.device)
+    elif scales.dtype != torch.float32 or not scales.is_cuda:
+        raise ValueError("scales: CUDA FP32")
+    if out.shape != x.shape or scales.shape != (R, (K + 127) // 128):
+        raise ValueError("out, scales: shapes of the codes and of their scales")
+    if R:
+        _check(lib().moe_fp8_quantize_rows(x.data_ptr(), dt, x.stride(0) if R > 1 else max(x.stride(0), K), R, K, out.data_ptr(), _ld(out),
+                                           scales.data_ptr(), scales.stride(0), scales.stride(1), _stream(stream)),
+               "moe_fp8_quantize_rows")
+    return out, scales
+
+
+def moe_fp8_quantize_blocks(w: torch.Tensor, out: Optional[torch.Tensor] = None, scales: Optional[torch.Tensor] = None,
+                            stream=None):
+    """Weight [N, K] (BF16 or FP32) -> (E4M3 [N, K], FP32 [ceil(N/128), ceil(K/128)])."""
+    dt = _fp8_dtype(w, "w")
+    N, K = w.shape
+    if out is None:
+        out = _fp8_codes(N, K, w.device)
+    else:
+        _need_codes(out, "out")
+    if scales is None:
+        scales = torch.empty((N + 127) // 128, (K + 127) // 128, dtype=torch.float32, device=w.device)
+    else:
+        _need(scales, torch.float32, "scales")
+    if out.shape != w.shape or scales.shape != ((N + 127) // 128, (K + 127) // 128):
+        raise ValueError("out, scales: shapes of the codes and of their scales")
+    _check(lib().moe_fp8_quantize_blocks(w.data_ptr(), dt, w.stride(0) if N > 1 else max(w.stride(0), K), N, K, out.data_ptr(), _ld(out),
+                                         scales.data_ptr(), _stream(stream)), "moe_fp8_quantize_blocks")
+    return out, scales
+
+
+def _fp8_operands(A, a_scales, W, w_scales, first: int):
+    """C views of activation rows [rows, K] and of a weight [N, K] or [experts, N, K]."""
+    _need_codes(A, "A")
+    _need_codes(W, "W")
+    count = W.shape[0] if W.dim() == 3 else 1
+    N, K = W.shape[-2:]
+    rows = A.shape[0]
+    if A.dim() != 2 or A.shape[1] != K:
+        raise ValueError(f"A: need [rows, {K}], got {tuple(A.shape)}")
+    if a_scales.dtype != torch.float32 or not a_scales.is_cuda or a_scales.shape != (rows, (K + 127) // 128):
+        raise ValueError(f"a_scales: need a CUDA FP32 tensor of shape {(rows, (K + 127) // 128)}")
+    _need(w_scales, torch.float32, "w_scales")
+    if w_scales.shape != W.shape[:-2] + ((N + 127) // 128, (K + 127) // 128):
+        raise ValueError(f"w_scales: need {tuple(W.shape[:-2]) + ((N + 127) // 128, (K + 127) // 128)}")
+    a = Fp8Rows(A.data_ptr(), _ld(A), a_scales.data_ptr(), a_scales.stride(0), a_scales.stride(1), rows)
+    w = Fp8Weight(W.data_ptr(), _ld(W), W.stride(0) if count > 1 else 0, w_scales.data_ptr(), first, count, N, K)
+    return a, w
+
+
+def _fp8_out(out, R: int, N: int, c_dtype, device):
+    """(C [R, N], its row stride): rows a multiple of 8 elements apart."""
+    if out is None:
+        ld = (N + 7) // 8 * 8
+        out = torch.empty(R, ld, dtype=c_dtype, device=device)
+        return (out if ld == N else out[:, :N]), ld
+    if not out.is_cuda or out.dtype != c_dtype or out.dim() != 2 or out.shape[0] < R or out.shape[1] != N or (
+            out.stride(1) != 1 and N != 1):
+        raise ValueError(f"out: need a CUDA {c_dtype} [{R}, {N}] tensor with unit column stride")
+    return out, out.stride(0) if out.shape[0] > 1 else max(out.stride(0), (N + 7) // 8 * 8)
+
+
+def _fp8_c_dtype(c_dtype) -> int:
+    if c_dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError("c_dtype: torch.bfloat16 or torch.float32")
+    return MOE_DTYPE_F32 if c_dtype == torch.float32 else MOE_DTYPE_BF16
+
+
+def moe_fp8_gemm(A: torch.Tensor, a_scales: torch.Tensor, W: torch.Tensor, w_scales: torch.Tensor,
+                 out: Optional[torch.Tensor] = None, c_dtype: torch.dtype = torch.bfloat16, stream=None) -> torch.Tensor:
+    """Quantised rows A [R, K] times a quantised weight W [N, K] transposed: BF16 or FP32 [R, N]."""
+    a, w = _fp8_operands(A, a_scales, W, w_scales, 0)
+    if W.dim() != 2:
+        raise ValueError("W: need [N, K]")
+    code = _fp8_c_dtype(c_dtype)
+    out, ld = _fp8_out(out, a.rows, w.N, c_dtype, A.device)
+    if a.rows:
+        _check(lib().moe_fp8_gemm(ctypes.byref(a), ctypes.byref(w), out.data_ptr(), ld, code, _stream(stream)),
+               "moe_fp8_gemm")
+    return out
+
+
+def _fp8_grouped(A, a_scales, W, w_scales, expert_offsets, R: int, gather_ids, first: int):
+    if W.dim() != 3:
+        raise ValueError("W: need [experts, N, K]")
+    a, w = _fp8_operands(A, a_scales, W, w_scales, first)
+    _need(expert_offsets, torch.int32, "expert_offsets")
+    if gather_ids is not None:
+        _need(gather_ids, torch.int32, "gather_ids")
+        if gather_ids.numel() < R:
+            raise ValueError("gather_ids: need R entries")
+    return a, w, expert_offsets.numel() - 1
+
+
+def moe_fp8_grouped_gemm(A: torch.Tensor, a_scales: torch.Tensor, W: torch.Tensor, w_scales: torch.Tensor,
+                         expert_offsets: torch.Tensor, R: int, gather_ids: Optional[torch.Tensor] = None,
+                         first: int = 0, out: Optional[torch.Tensor] = None, c_dtype: torch.dtype = torch.bfloat16,
+                         stream=None) -> torch.Tensor:
+    """Expert-sorted rows times their expert's weight, W [experts, N, K]: BF16 or FP32 [R, N].  W holds
+    the experts from ``first`` on; the others' rows are zeros."""
+    a, w, E = _fp8_grouped(A, a_scales, W, w_scales, expert_offsets, R, gather_ids, first)
+    code = _fp8_c_dtype(c_dtype)
+    out, ld = _fp8_out(out, R, w.N, c_dtype, A.device)
+    if R:
+        _check(lib().moe_fp8_grouped_gemm(ctypes.byref(a), _ptr(gather_ids), ctypes.byref(w), expert_offsets.data_ptr(),
+                                          E, R, out.data_ptr(), ld, code, _stream(stream)), "moe_fp8_grouped_gemm")
+    return out
+
+
+def moe_fp8_grouped_gemm_swiglu(A: torch.Tensor, a_scales: torch.Tensor, W: torch.Tensor, w_scales: torch.Tensor,
+                                expert_offsets: torch.Tensor, R: int, limit: float = 7.0,
+                                gather_ids: Optional[torch.Tensor] = None, first: int = 0,
+                                out: Optional[torch.Tensor] = None, scales: Optional[torch.Tensor] = None, stream=None):
+    """Gate/up product over W [experts, 2I, K], clamped SwiGLU, and the row quantiser on its result:
+    (E4M3 [R, I], FP32 [R, I/128]), the operands of the down product."""
+    a, w, E = _fp8_grouped(A, a_scales, W, w_scales, expert_offsets, R, gather_ids, first)
+    inter = w.N // 2
+    if out is None:
+        out = _fp8_codes(R, inter, A.device)
+    else:
+        _need_codes(out, "out")
+    if scales is None:
+        scales = _fp8_row_scales(R, inter, A.device)
+    if out.shape != (R, inter) or scales.shape != (R, (inter + 127) // 128) or (
+            scales.dtype != torch.float32 or not scales.is_cuda):
+        raise ValueError("out, scales: shapes of the activation's codes and of their scales")
+    if R:
+        _check(lib().moe_fp8_grouped_gemm_swiglu(ctypes.byref(a), _ptr(gather_ids), ctypes.byref(w),
+                                                 expert_offsets.data_ptr(), E, R, float(limit), out.data_ptr(),
+                                                 _ld(out), scales.data_ptr(), scales.stride(0), scales.stride(1),
+                                                 _stream(stream)), "moe_fp8_grouped_gemm_swiglu")
+    return out, scales
 
 
 def moe_get_device_error(stream=None) -> int:

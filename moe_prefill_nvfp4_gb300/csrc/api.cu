@@ -45,28 +45,6 @@ int current_device() {
   return d;
 }
 
-// Once per device: the compute capability check, the SM count and the error word address.
-int ensure_device() {
-  const int d = current_device();
-  if (d < 0) return MOE_ERR_CUDA;
-  if (g_arch_ok[d].load(std::memory_order_acquire) == 1) return MOE_OK;
-  std::lock_guard<std::mutex> lk(g_mu);
-  if (g_arch_ok[d].load(std::memory_order_relaxed) == 0) {
-    cudaDeviceProp p;
-    if (cudaGetDeviceProperties(&p, d) != cudaSuccess) return MOE_ERR_CUDA;
-    if (!(p.major == 10 && p.minor == 3)) {
-      g_arch_ok[d].store(-1, std::memory_order_release);
-    } else {
-      void* addr = nullptr;
-      if (cudaGetSymbolAddress(&addr, g_device_error) != cudaSuccess) return MOE_ERR_CUDA;
-      g_err_addr[d] = static_cast<int*>(addr);
-      g_sm_count[d] = p.multiProcessorCount;
-      g_arch_ok[d].store(1, std::memory_order_release);
-    }
-  }
-  return g_arch_ok[d].load(std::memory_order_relaxed) == 1 ? MOE_OK : MOE_ERR_NOT_BUILT_FOR_DEVICE;
-}
-
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // Where p points, for the current device: kMemDevice (device or managed memory), kMemHost (host
@@ -99,6 +77,27 @@ MemKind memory_kind(const void* p) {
 cudaStream_t as_stream(void* s) { return static_cast<cudaStream_t>(s); }
 
 }  // namespace
+
+int ensure_device() {
+  const int d = current_device();
+  if (d < 0) return MOE_ERR_CUDA;
+  if (g_arch_ok[d].load(std::memory_order_acquire) == 1) return MOE_OK;
+  std::lock_guard<std::mutex> lk(g_mu);
+  if (g_arch_ok[d].load(std::memory_order_relaxed) == 0) {
+    cudaDeviceProp p;
+    if (cudaGetDeviceProperties(&p, d) != cudaSuccess) return MOE_ERR_CUDA;
+    if (!(p.major == 10 && p.minor == 3)) {
+      g_arch_ok[d].store(-1, std::memory_order_release);
+    } else {
+      void* addr = nullptr;
+      if (cudaGetSymbolAddress(&addr, g_device_error) != cudaSuccess) return MOE_ERR_CUDA;
+      g_err_addr[d] = static_cast<int*>(addr);
+      g_sm_count[d] = p.multiProcessorCount;
+      g_arch_ok[d].store(1, std::memory_order_release);
+    }
+  }
+  return g_arch_ok[d].load(std::memory_order_relaxed) == 1 ? MOE_OK : MOE_ERR_NOT_BUILT_FOR_DEVICE;
+}
 
 int device_sm_count() {
   const int d = current_device();

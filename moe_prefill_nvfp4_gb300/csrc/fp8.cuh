@@ -1,0 +1,48 @@
+// fp8.cuh -- device helpers shared by the FP8 (E4M3, 128-element scales) kernels.
+#pragma once
+
+#include "common.cuh"
+
+namespace moe {
+
+constexpr uint32_t kFp8AmaxFloorBits = 0x0D800000u;  // 2^-100
+
+// Scale and its reciprocal of a group whose largest magnitude has the bits amax_bits (inf and NaN
+// compare above every number): a = max(amax, 2^-100), scale = a / 448, inv = 448 / a; both NaN
+// for a group with a value that is not finite.
+MOE_DEV void fp8_scale(uint32_t amax_bits, float& scale, float& inv) {
+  const bool finite = amax_bits < 0x7F800000u;
+  const float a = __uint_as_float(finite ? max(amax_bits, kFp8AmaxFloorBits) : 0x7FC00000u);
+  scale = __fdiv_rn(a, 448.0f);
+  inv = __fdiv_rn(448.0f, a);
+}
+
+// Four floats to E4M3 codes, round to nearest even, a in the low byte.
+MOE_DEV uint32_t pack_e4m3x4(float a, float b, float c, float d) {
+  uint32_t out;
+  asm("{\n .reg .b16 lo, hi;\n cvt.rn.satfinite.e4m3x2.f32 lo, %2, %1;\n cvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\n"
+      " mov.b32 %0, {lo, hi};\n}"
+      : "=r"(out)
+      : "f"(a), "f"(b), "f"(c), "f"(d));
+  return out;
+}
+
+// silu(min(g, L)) * clamp(u, -L, L) of FP32 sums, NaN kept (fminf and fmaxf would drop it).  The
+// exponential and the division are the hardware approximations (a few FP32 ulp); for g -> -inf the
+// denominator overflows and the quotient is -0, the limit of silu.
+MOE_DEV float swiglu_keep_nan(float g, float u, float L) {
+  const float gm = g > L ? L : g;
+  const float uc = u > L ? L : (u < -L ? -L : u);
+  return __fdividef(gm, 1.0f + __expf(-gm)) * uc;
+}
+
+// Load from the shared memory of CTA `rank` of the cluster, at the offset of local_addr in ours.
+MOE_DEV float ld_shared_cluster_f32(uint32_t local_addr, uint32_t rank) {
+  uint32_t ra;
+  float v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(ra) : "r"(local_addr), "r"(rank));
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(ra) : "memory");
+  return v;
+}
+
+}  // namespace moe

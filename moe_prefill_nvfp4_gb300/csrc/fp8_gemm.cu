@@ -1,0 +1,986 @@
+// fp8_gemm.cu -- block-scaled FP8 (E4M3) products on the 5th-generation tensor cores, dense and
+// grouped by expert:
+//
+//   C[p, n] = sum_g sa[row(p), g] * sw_e[n / 128, g] * P_g,   P_g = sum_{k in block g} A[row(p), k] W_e[n, k]
+//
+// A is E4M3 with one FP32 scale per row and 128 columns, W_e E4M3 with one per 128 x 128 block.
+// The scales change every 128 k, so a k block is the unit of the accumulation: four
+// tcgen05.mma.kind::f8f6f4 (k 32 each) make P_g in tensor memory, the epilogue warps read it and
+// add sa * sw * P_g to FP32 registers while the MMAs of the next block run into the other half of
+// tensor memory.  Sums stay in FP32 throughout; one rounding makes the BF16 output.
+//
+// Two kernels:
+//   wide  token rows are the MMA's M operand (128 per tile, a TMEM lane and an epilogue thread to a
+//         row: its sa is one register), weight rows the N operand (NB blocks of 128, sw uniform
+//         over a block).  Persistent CTAs over all experts' tiles.
+//   few   weight rows are the M operand (two blocks of 128 per tile), up to NT token rows the N
+//         operand: a tile of the wide kernel would be mostly empty rows.  The k blocks of a tile are
+//         split over a cluster whose partial sums meet in shared memory.
+//
+// gate/up form: the tile's two blocks are a gate block and the matching up block, and the tile's
+// output is a 128-column group of act = silu(min(g, L)) * clamp(u, -L, L), quantised in the
+// epilogue (the group's scale needs only this tile), so no intermediate goes to memory.
+//
+// Operands are staged by TMA in the canonical 128-byte-swizzled K-major layout (one swizzle row is
+// one 128-k block).  Out-of-range k, weight rows and tokens are zero-filled by the TMA or hold
+// other rows' data that only reaches accumulator rows nobody stores.  Every wait is bounded
+// (MOE_DEVERR_TIMEOUT; the CTA then drains its copies and MMAs, frees TMEM and returns).
+
+#include <algorithm>
+#include <atomic>
+
+#include "fp8.cuh"
+#include "internal.h"
+
+namespace moe {
+namespace f8 {
+
+constexpr int BK = 128;               // k per stage = one scale block = one 128-byte swizzle row
+constexpr int BLK = 128 * BK;         // 128 rows of a stage: 16 KB
+constexpr int MAX_E = MOE_FP8_MAX_EXPERTS;
+
+// kind::f8f6f4: D FP32 (bits 4-5 = 1), A and B E4M3 (0), both K-major, N>>3 at 17, M>>4 at 24
+__host__ __device__ constexpr uint32_t make_idesc_e4m3(int M, int N) {
+  return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+// One k block: four k32 MMAs, both descriptors advancing 32 bytes inside the swizzle row; the
+// first overwrites D.
+MOE_DEV void mma4_e4m3_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc) {
+  asm volatile(
+      "{\n .reg .pred p, q;\n .reg .b64 a1, a2, a3, b1, b2, b3;\n"
+      " setp.ne.b32 p, 0, 0;\n setp.eq.b32 q, 0, 0;\n"
+      " add.s64 a1, %1, 2;\n add.s64 a2, %1, 4;\n add.s64 a3, %1, 6;\n"
+      " add.s64 b1, %2, 2;\n add.s64 b2, %2, 4;\n add.s64 b3, %2, 6;\n"
+      " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n"
+      " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a1, b1, %3, q;\n"
+      " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a2, b2, %3, q;\n"
+      " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a3, b3, %3, q;\n}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc)
+      : "memory");
+}
+
+MOE_DEV void tma_load_3d(uint32_t dst, const void* tmap, int x, int y, int z, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+          dst),
+      "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
+
+// Waits for this thread's TMEM loads; naming the registers keeps their uses behind the wait.
+template <int N>
+MOE_DEV void tmem_wait_ld_regs(uint32_t (&r)[N]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
+}
+
+MOE_DEV void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+
+// Two FP32 sums in one 64-bit register pair: acc += {v0, v1} * {f, f}
+MOE_DEV uint64_t pack_f32x2(float lo, float hi) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+  return d;
+}
+MOE_DEV void unpack_f32x2(uint64_t d, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(d));
+}
+MOE_DEV void fma_f32x2(uint64_t& acc, uint32_t v0, uint32_t v1, uint64_t f) {
+  asm("{\n .reg .b64 d;\n mov.b64 d, {%1, %2};\n fma.rn.f32x2 %0, d, %3, %0;\n}" : "+l"(acc) : "r"(v0), "r"(v1), "l"(f));
+}
+
+template <uint32_t N>
+MOE_DEV void reg_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <uint32_t N>
+MOE_DEV void reg_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+MOE_DEV bool wait_bounded(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* err, uint64_t limit) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = globaltimer_ns();
+  for (;;) {
+    if (mbar_try_wait_sleep(bar, parity, kSleepHintNs)) return true;
+    if (*abort_flag) return false;
+    if (globaltimer_ns() - t0 > limit) {
+      *abort_flag = 1;
+      set_error(err, MOE_DEVERR_TIMEOUT);
+      return false;
+    }
+  }
+}
+
+MOE_DEV bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* err, uint64_t limit) {
+  bool ok = true;
+  if (lane_id() == 0) ok = wait_bounded(bar, parity, abort_flag, err, limit);
+  return __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+}
+
+// named_bar_sync that tells every thread whether any of them had pred set.
+MOE_DEV bool named_bar_any(uint32_t id, uint32_t nthreads, bool pred) {
+  uint32_t any;
+  asm volatile("{\n .reg .pred p, q;\n setp.ne.u32 p, %3, 0;\n bar.red.or.pred q, %1, %2, p;\n selp.u32 %0, 1, 0, q;\n}"
+               : "=r"(any)
+               : "r"(id), "r"(nthreads), "r"(pred ? 1u : 0u)
+               : "memory");
+  return any != 0;
+}
+
+// Token row of sorted row p (checked: an index outside [0, a_rows) reads row 0 and is recorded).
+MOE_DEV int source_row(const Fp8GemmArgs& a, int p) {
+  if (a.gather == nullptr) return p;
+  const int r = __ldg(a.gather + p);
+  if ((unsigned)r < (unsigned)a.a_rows) return r;
+  set_error(a.err, MOE_DEVERR_BAD_GATHER);
+  return 0;
+}
+
+// ------------------------------------------------------------------------------------------------
+// Tiles.  Expert e (of this call's e_first .. e_first + e_count) owns tiles tbase[e] .. tbase[e+1]):
+// ceil(rows / BT) token tiles x NG weight tiles, weight tiles fastest so that CTAs running together
+// share token rows and the expert's weights in L2.
+
+// By one warp: the prefix sum of the experts' tile counts, the total in s_tbase[E].  Offsets that are
+// not a non-decreasing sequence from 0 to at most R are recorded and make the total -1 (no tile is
+// run, no row written).
+MOE_DEV void build_tiles(const Fp8GemmArgs& a, const int* s_offs, int* s_tbase, int BT, int NG) {
+  const int lane = lane_id();
+  const int per = (a.E + 31) / 32;
+  const int e0 = min(a.E, lane * per), e1 = min(a.E, e0 + per);
+  int sum = 0;
+  bool bad = false;
+  for (int e = e0; e < e1; ++e) {
+    const int m = s_offs[e + 1] - s_offs[e];
+    if (m < 0) bad = true;
+    if (m > 0 && (unsigned)(e - a.e_first) < (unsigned)a.e_count) sum += NG * ((m + BT - 1) / BT);
+  }
+  if (lane == 0 && (s_offs[0] != 0 || s_offs[a.E] > a.R)) bad = true;
+  bad = __any_sync(0xffffffffu, bad);
+  if (bad && lane == 0) set_error(a.err, MOE_DEVERR_BAD_OFFSETS);
+  int incl = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += v;
+  }
+  int run = incl - sum;
+  for (int e = e0; e < e1; ++e) {
+    s_tbase[e] = bad ? 0 : run;
+    const int m = s_offs[e + 1] - s_offs[e];
+    if (m > 0 && (unsigned)(e - a.e_first) < (unsigned)a.e_count) run += NG * ((m + BT - 1) / BT);
+  }
+  if (lane == 31) s_tbase[a.E] = bad ? -1 : incl;
+}
+
+struct Tile {
+  int e;    // expert within W
+  int p0;   // first sorted row
+  int cnt;  // token rows
+  int ng;   // weight tile
+};
+
+MOE_DEV Tile decode_tile(int g, const Fp8GemmArgs& a, const int* s_offs, const int* s_tbase, int BT, int NG) {
+  int lo = 0, hi = a.E - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (s_tbase[mid] <= g) lo = mid; else hi = mid - 1;
+  }
+  const int local = g - s_tbase[lo];
+  const int tt = local / NG;
+  Tile t;
+  t.e = lo - a.e_first;
+  t.ng = local - tt * NG;
+  t.p0 = s_offs[lo] + tt * BT;
+  t.cnt = min(BT, s_offs[lo + 1] - t.p0);
+  return t;
+}
+
+// First weight row of block h of weight tile ng, and the scale row of that block.
+template <int NB>
+MOE_DEV int block_row(const Fp8GemmArgs& a, int ng, int h) {
+  return a.half ? h * a.half + ng * 128 : (ng * NB + h) * 128;
+}
+
+// Rows of experts outside W (expert parallelism: other ranks' experts) read as zeros: sorted rows
+// [0, offs[e_first]) and [offs[e_first + e_count], offs[E]).  `tid` of `nthreads` threads of the grid.
+MOE_DEV void zero_absent(const Fp8GemmArgs& a, const int* s_offs, int64_t tid, int64_t nthreads) {
+  const int lo = s_offs[a.e_first], hi = s_offs[a.e_first + a.e_count];
+  const int64_t rows = (int64_t)lo + (s_offs[a.E] - hi);
+  if (rows <= 0) return;
+  const int cols = a.half ? a.half : a.N;
+  for (int64_t i = tid; i < rows * cols; i += nthreads) {
+    const int64_t r = i / cols;
+    const int c = (int)(i - r * cols);
+    const int64_t p = r < lo ? r : hi + (r - lo);
+    if (a.half) {
+      a.q[p * a.ld_q + c] = 0;
+      if ((c & 127) == 0) {
+        float s, inv;
+        fp8_scale(0, s, inv);
+        a.s[p * a.s_row + (c >> 7) * a.s_grp] = s;
+      }
+    } else if (a.c_dtype == MOE_DTYPE_BF16) {
+      static_cast<uint16_t*>(a.C)[p * a.ldc + c] = 0;
+    } else {
+      static_cast<float*>(a.C)[p * a.ldc + c] = 0.f;
+    }
+  }
+}
+
+// Stores 64 bytes of each of the warp's 32 rows (w: this lane's row, columns n0 .. of T) through the
+// warp's staging rows: 16-byte chunk c of row r lies at c ^ ((r >> 1) & 3), free of bank conflicts both
+// ways, and leaves in 16-byte stores with 4 lanes to a row.  Rows from nrow and columns from N on are
+// left out; `out` is row 0, column 0.
+template <typename T>
+MOE_DEV void store_rows(uint8_t* stg, const uint32_t (&w)[16], T* out, int64_t ld, int nrow, int n0, int N) {
+  constexpr int PER = 16 / sizeof(T);
+  const int lane = lane_id();
+#pragma unroll
+  for (int c = 0; c < 4; ++c)
+    *reinterpret_cast<uint4*>(stg + lane * 64 + ((c ^ ((lane >> 1) & 3)) * 16)) =
+        make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+  __syncwarp();
+  const int c = lane & 3, col = n0 + c * PER;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = i * 8 + (lane >> 2);
+    if (r < nrow && col < N) {
+      const T* src = reinterpret_cast<const T*>(stg + r * 64 + ((c ^ ((r >> 1) & 3)) * 16));
+      T* dst = out + r * ld + col;
+      if (col + PER <= N) {
+        *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<const uint4*>(src);
+      } else {
+        for (int j = 0; col + j < N; ++j) dst[j] = src[j];
+      }
+    }
+  }
+  __syncwarp();
+}
+
+// ------------------------------------------------------------------------------------------------
+// wide kernel
+
+template <int NB_>
+struct WideCfg {
+  static constexpr int NB = NB_;           // weight blocks of 128 per tile
+  static constexpr int BN = NB * 128;
+  static constexpr int THREADS = 384;      // warpgroup 0: producer, MMA; warpgroups 1, 2: epilogue
+  static constexpr int STAGE = BLK + NB * BLK;
+  static constexpr int NS = NB == 2 ? 4 : 6;
+  static constexpr int TMEM_COLS = 2 * BN;
+  static constexpr int EPI_WARP = 32 * 64;  // 32 rows x 64 bytes
+  static constexpr int OFF_EPI = NS * STAGE;
+  static constexpr int OFF_AMAX = OFF_EPI + 8 * EPI_WARP;      // uint32 [2][128]
+  static constexpr int OFF_OFFS = OFF_AMAX + 2 * 128 * 4;
+  static constexpr int OFF_TBASE = OFF_OFFS + (MAX_E + 1) * 4;
+  static constexpr int OFF_BAR = (OFF_TBASE + (MAX_E + 1) * 4 + 7) & ~7;
+  // full[NS] empty[NS] d_full[2] d_empty[2] drain
+  static constexpr int NBAR = 2 * NS + 5;
+  static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
+  static constexpr int BYTES = OFF_MISC + 16;
+  static constexpr int SMEM = BYTES + 1024;
+  // registers: the launch has 384 x 168; 128 x 56 + 256 x 224 is the same number
+  static constexpr int REG_LOW = 56, REG_HIGH = 224;
+  static_assert(128 * REG_LOW + 256 * REG_HIGH <= THREADS * 168, "register split");
+  static_assert(SMEM > 232448 / 2 && SMEM <= 232448, "one CTA per SM (it takes all of TMEM)");
+};
+
+// Warp roles: 0 TMA producer, 1 MMA issuer and TMEM owner, 4-11 epilogue (two warpgroups; warp w
+// reads TMEM lanes 32 (w % 4).., warpgroup g the columns 64 g .. 64 g + 63 of each weight block, so
+// that in the gate/up form a thread holds a gate column and its up column).
+template <class C, bool GATHER>
+__global__ void __launch_bounds__(C::THREADS, 1)
+    wide_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap wmap,
+                const __grid_constant__ Fp8GemmArgs args) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sbase = smem_u32(smem);
+  constexpr int NS = C::NS, NB = C::NB;
+  int* s_offs = reinterpret_cast<int*>(smem + C::OFF_OFFS);
+  int* s_tbase = reinterpret_cast<int*>(smem + C::OFF_TBASE);
+  const uint32_t bar0 = sbase + C::OFF_BAR;
+  auto full = [&](int s) { return bar0 + 8u * s; };
+  auto empty = [&](int s) { return bar0 + 8u * (NS + s); };
+  auto d_full = [&](int d) { return bar0 + 8u * (2 * NS + d); };
+  auto d_empty = [&](int d) { return bar0 + 8u * (2 * NS + 2 + d); };
+  const uint32_t drain_bar = bar0 + 8u * (2 * NS + 4);
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
+  volatile int* s_abort = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint64_t limit = args.wait_ns;
+  int* err = args.err;
+
+  if (tid == 0) {
+    for (int s = 0; s < NS; ++s) {
+      mbar_init(full(s), 1);
+      mbar_init(empty(s), 1);
+    }
+    for (int d = 0; d < 2; ++d) {
+      mbar_init(d_full(d), 1);
+      mbar_init(d_empty(d), 8);  // the epilogue warps
+    }
+    mbar_init(drain_bar, 1);
+    *s_abort = 0;
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(s_tmem), C::TMEM_COLS);
+    tmem_relinquish();
+  }
+  griddep_wait();
+  griddep_launch_dependents();
+  const int NG = args.half ? args.half / 128 : (args.N + C::BN - 1) / C::BN;
+  if (args.offsets == nullptr) {  // dense: one group of R rows
+    if (tid == 0) {
+      s_offs[0] = 0;
+      s_offs[1] = args.R;
+    }
+  } else {
+    for (int i = tid; i <= args.E; i += C::THREADS) s_offs[i] = args.offsets[i];
+  }
+  __syncthreads();
+  if (warp == 0) build_tiles(args, s_offs, s_tbase, 128, NG);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *s_tmem;
+  const int KB = (args.K + BK - 1) / BK;
+  const int total = s_tbase[args.E];
+
+  if (warp < 4) {
+    reg_dec<C::REG_LOW>();
+    if (warp == 0) {
+      // ---------------------------------------------------------------- TMA producer (whole warp)
+      if (lane == 0) {
+        prefetch_tmap(&amap);
+        prefetch_tmap(&wmap);
+      }
+      int i = 0;
+      bool ok = true;
+      for (int g = blockIdx.x; ok && g < total; g += gridDim.x) {
+        const Tile t = decode_tile(g, args, s_offs, s_tbase, 128, NG);
+        int r[4] = {0, 0, 0, 0};
+        const int nrow4 = (t.cnt + 3) >> 2;  // gathered rows come in fours
+        if (GATHER && lane < nrow4) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) r[j] = source_row(args, t.p0 + min(4 * lane + j, t.cnt - 1));
+        }
+        const uint32_t bytes = NB * BLK + (GATHER ? nrow4 * 4 * BK : BLK);
+        for (int kb = 0; kb < KB; ++kb, ++i) {
+          const int s = i % NS;
+          if (!warp_wait(empty(s), ((i / NS) & 1) ^ 1, s_abort, err, limit)) {
+            ok = false;
+            break;
+          }
+          const uint32_t st = sbase + s * C::STAGE;
+          if (lane == 0) {
+            mbar_arrive_expect_tx(full(s), bytes);
+            if (!GATHER) tma_load_2d(st, &amap, kb * BK, t.p0, full(s));
+#pragma unroll
+            for (int h = 0; h < NB; ++h)
+              tma_load_3d(st + BLK + h * BLK, &wmap, kb * BK, block_row<NB>(args, t.ng, h), t.e, full(s));
+          }
+          if (GATHER) {
+            __syncwarp();
+            if (lane < nrow4) tma_gather4(st + lane * 4 * BK, &amap, kb * BK, r[0], r[1], r[2], r[3], full(s));
+          }
+        }
+      }
+      if (!ok && lane == 0)  // every copy issued lands before the CTA leaves
+        for (int j = max(0, i - NS); j < i; ++j) mbar_wait_drain(full(j % NS), (j / NS) & 1);
+    } else if (warp == 1) {
+      // ---------------------------------------------------------------- MMA issuer
+      constexpr uint32_t idesc = make_idesc_e4m3(128, C::BN);
+      int i = 0;
+      bool ok = true;
+      for (int g = blockIdx.x; ok && g < total; g += gridDim.x) {
+        for (int kb = 0; kb < KB; ++kb, ++i) {
+          const int s = i % NS, db = i & 1;
+          if (!warp_wait(d_empty(db), ((i >> 1) & 1) ^ 1, s_abort, err, limit) ||
+              !warp_wait(full(s), (i / NS) & 1, s_abort, err, limit)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t st = sbase + s * C::STAGE;
+          if (elect_one()) {
+            mma4_e4m3_ss(tmem_base + (uint32_t)(db * C::BN), make_sdesc_sw128(st), make_sdesc_sw128(st + BLK), idesc);
+            mma_commit(empty(s));
+            mma_commit(d_full(db));
+          }
+          __syncwarp();
+        }
+      }
+      if (!ok) {  // every issued MMA completes before TMEM is freed
+        if (elect_one()) {
+          mma_commit(drain_bar);
+          mbar_wait_drain(drain_bar, 0);
+        }
+        __syncwarp();
+      }
+    }
+  } else {
+    // ------------------------------------------------------------------ epilogue
+    reg_inc<C::REG_HIGH>();
+    const int wg = (warp - 4) >> 2;
+    const int q = warp & 3;
+    uint8_t* stg = smem + C::OFF_EPI + (warp - 4) * C::EPI_WARP;
+    uint32_t* s_amax = reinterpret_cast<uint32_t*>(smem + C::OFF_AMAX);
+    const uint32_t lane_base = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(wg * 64);
+    const int row = q * 32 + lane;  // of the tile
+    if (total >= 0) zero_absent(args, s_offs, (int64_t)blockIdx.x * 256 + (tid - 128), (int64_t)gridDim.x * 256);
+    int i = 0;
+    bool ok = true;
+    for (int g = blockIdx.x; ok && g < total; g += gridDim.x) {
+      const Tile t = decode_tile(g, args, s_offs, s_tbase, 128, NG);
+      const float* sa = args.sa + (int64_t)source_row(args, t.p0 + min(row, t.cnt - 1)) * args.sa_row;
+      const float* sw[NB];
+#pragma unroll
+      for (int h = 0; h < NB; ++h)  // (a block past N: any scale, its columns are not stored)
+        sw[h] = args.sw + ((int64_t)t.e * args.nblk + min(block_row<NB>(args, t.ng, h) >> 7, args.nblk - 1)) * KB;
+      uint64_t acc[NB][32];
+#pragma unroll
+      for (int h = 0; h < NB; ++h)
+#pragma unroll
+        for (int j = 0; j < 32; ++j) acc[h][j] = 0;
+      // scales two k blocks ahead
+      float pa[2], pw[2][NB];
+#pragma unroll
+      for (int d = 0; d < 2; ++d) {
+        const int k = min(d, KB - 1);
+        pa[d] = __ldg(sa + k * args.sa_grp);
+#pragma unroll
+        for (int h = 0; h < NB; ++h) pw[d][h] = __ldg(sw[h] + k);
+      }
+      for (int kb = 0; kb < KB; ++kb, ++i) {
+        const int db = i & 1;
+        uint64_t f[NB];
+#pragma unroll
+        for (int h = 0; h < NB; ++h) {
+          const float v = pa[0] * pw[0][h];
+          f[h] = pack_f32x2(v, v);
+          pw[0][h] = pw[1][h];
+          pw[1][h] = __ldg(sw[h] + min(kb + 2, KB - 1));
+        }
+        pa[0] = pa[1];
+        pa[1] = __ldg(sa + min(kb + 2, KB - 1) * args.sa_grp);
+        if (!warp_wait(d_full(db), (i >> 1) & 1, s_abort, err, limit)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t base = lane_base + (uint32_t)(db * C::BN);
+        uint32_t v[2][32];
+        tmem_ld_32x32b_x32(base, v[0]);
+#pragma unroll
+        for (int c = 0; c < 2 * NB; ++c) {  // 32 columns of block c / 2
+          tmem_wait_ld_regs(v[c & 1]);
+          if (c + 1 < 2 * NB) {
+            tmem_ld_32x32b_x32(base + (uint32_t)(((c + 1) >> 1) * 128 + ((c + 1) & 1) * 32), v[(c + 1) & 1]);
+          } else {  // the accumulator may be overwritten
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(d_empty(db));
+          }
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            fma_f32x2(acc[c >> 1][(c & 1) * 16 + j], v[c & 1][2 * j], v[c & 1][2 * j + 1], f[c >> 1]);
+        }
+      }
+      const bool gate_up = NB == 2 && args.half != 0;
+      // (the gate/up form's warps exchange maxima below: all of them leave the loop at the same tile)
+      if (gate_up ? named_bar_any(1, 256, !ok) : !ok) {
+        ok = false;
+        break;
+      }
+      const bool live = row < t.cnt;
+      if (gate_up) {
+        // gate (block 0) and up (block 1) columns 64 wg .. of the act group
+        uint32_t m = 0;
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+          float g0, g1, u0, u1;
+          unpack_f32x2(acc[0][j], g0, g1);
+          unpack_f32x2(acc[NB - 1][j], u0, u1);
+          g0 = swiglu_keep_nan(g0, u0, args.limit);
+          g1 = swiglu_keep_nan(g1, u1, args.limit);
+          m = max(m, max(__float_as_uint(g0) & 0x7FFFFFFFu, __float_as_uint(g1) & 0x7FFFFFFFu));
+          acc[0][j] = pack_f32x2(g0, g1);
+        }
+        s_amax[wg * 128 + row] = m;
+        named_bar_sync(1, 256);
+        m = max(m, s_amax[(wg ^ 1) * 128 + row]);  // (the next tile's write comes after its first barrier)
+        float scale, inv;
+        fp8_scale(m, scale, inv);
+        uint8_t* dst = args.q + (int64_t)(t.p0 + row) * args.ld_q + t.ng * 128 + wg * 64;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t w[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            float a0, a1, a2, a3;
+            unpack_f32x2(acc[0][c * 8 + 2 * j], a0, a1);
+            unpack_f32x2(acc[0][c * 8 + 2 * j + 1], a2, a3);
+            w[j] = pack_e4m3x4(a0 * inv, a1 * inv, a2 * inv, a3 * inv);
+          }
+          if (live) *reinterpret_cast<uint4*>(dst + c * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        if (live && wg == 0) args.s[(int64_t)(t.p0 + row) * args.s_row + t.ng * args.s_grp] = scale;
+      } else {
+        const int nrow = min(32, t.cnt - q * 32);
+        const int64_t p0 = t.p0 + q * 32;
+#pragma unroll
+        for (int h = 0; h < NB; ++h) {
+          const int n0 = block_row<NB>(args, t.ng, h) + wg * 64;
+          uint32_t w[16];
+          if (args.c_dtype == MOE_DTYPE_F32) {
+#pragma unroll
+            for (int ps = 0; ps < 4; ++ps) {
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
+                float a0, a1;
+                unpack_f32x2(acc[h][ps * 8 + j], a0, a1);
+                w[2 * j] = __float_as_uint(a0);
+                w[2 * j + 1] = __float_as_uint(a1);
+              }
+              store_rows(stg, w, static_cast<uint32_t*>(args.C) + p0 * args.ldc, args.ldc, nrow, n0 + ps * 16, args.N);
+            }
+          } else {
+#pragma unroll
+            for (int ps = 0; ps < 2; ++ps) {
+#pragma unroll
+              for (int j = 0; j < 16; ++j) {
+                float a0, a1;
+                unpack_f32x2(acc[h][ps * 16 + j], a0, a1);
+                w[j] = pack_bf16x2(a0, a1);
+              }
+              store_rows(stg, w, static_cast<uint16_t*>(args.C) + p0 * args.ldc, args.ldc, nrow, n0 + ps * 32, args.N);
+            }
+          }
+        }
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem_base, C::TMEM_COLS);
+  }
+}
+
+// ------------------------------------------------------------------------------------------------
+// few-row kernel
+
+template <int NT_, int NS_, int PER_SM_>
+struct FewCfg {
+  static constexpr int NT = NT_;            // token rows per tile
+  static constexpr int NS = NS_;
+  static constexpr int PER_SM = PER_SM_;    // CTAs per SM
+  static constexpr int THREADS = 192;
+  static constexpr int STAGE = 2 * BLK + NT * BK;
+  static constexpr int TMEM_COLS = 4 * NT;  // two buffers x two blocks
+  static constexpr int PART = NT * 256 * 4; // partial sums [NT][256], over the drained stages
+  static constexpr int OFF_SCALE = NS * STAGE;                      // float [4 warps][2][2][NT]
+  static constexpr int OFF_AMAX = OFF_SCALE + 4 * 4 * NT * 4;       // uint32 [NT][4]
+  static constexpr int OFF_BAR = OFF_AMAX + NT * 4 * 4;
+  static constexpr int OFF_OFFS = 0;  // the tile tables, over the stages (read before the first load)
+  static constexpr int OFF_TBASE = (MAX_E + 1) * 4;
+  static constexpr int NBAR = 2 * NS + 5;
+  static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
+  static constexpr int BYTES = OFF_MISC + 16;
+  static constexpr int SMEM = BYTES + 1024;
+  static_assert(NT % 16 == 0 && STAGE % 1024 == 0 && PART <= NS * STAGE, "tile");
+  static_assert(PER_SM * (SMEM + 1024) <= 228 * 1024 && PER_SM * TMEM_COLS <= 512, "CTAs per SM");
+};
+
+// Warp roles: 0 TMA producer, 1 MMA issuer and TMEM owner, 2-5 epilogue (TMEM lanes 32 (w % 4)..).
+// One tile per cluster; CTA `rank` of the cluster takes k blocks KB rank / S .. KB (rank + 1) / S.
+template <class C, bool GATHER>
+__global__ void __launch_bounds__(C::THREADS, C::PER_SM)
+    few_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap wmap,
+               const __grid_constant__ Fp8GemmArgs args) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sbase = smem_u32(smem);
+  constexpr int NS = C::NS, NT = C::NT;
+  int* s_offs = reinterpret_cast<int*>(smem + C::OFF_OFFS);
+  int* s_tbase = reinterpret_cast<int*>(smem + C::OFF_TBASE);
+  const uint32_t bar0 = sbase + C::OFF_BAR;
+  auto full = [&](int s) { return bar0 + 8u * s; };
+  auto empty = [&](int s) { return bar0 + 8u * (NS + s); };
+  auto d_full = [&](int d) { return bar0 + 8u * (2 * NS + d); };
+  auto d_empty = [&](int d) { return bar0 + 8u * (2 * NS + 2 + d); };
+  const uint32_t drain_bar = bar0 + 8u * (2 * NS + 4);
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
+  volatile int* s_abort = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint64_t limit = args.wait_ns;
+  int* err = args.err;
+  const int S = (int)cluster_nctarank(), rank = (int)cluster_ctarank();
+
+  if (tid == 0) {
+    for (int s = 0; s < NS; ++s) {
+      mbar_init(full(s), 1);
+      mbar_init(empty(s), 1);
+    }
+    for (int d = 0; d < 2; ++d) {
+      mbar_init(d_full(d), 1);
+      mbar_init(d_empty(d), 4);
+    }
+    mbar_init(drain_bar, 1);
+    *s_abort = 0;
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(s_tmem), C::TMEM_COLS);
+    tmem_relinquish();
+  }
+  griddep_wait();
+  griddep_launch_dependents();
+  const int NG = args.half ? args.half / 128 : (args.N + 255) / 256;
+  if (args.offsets == nullptr) {
+    if (tid == 0) {
+      s_offs[0] = 0;
+      s_offs[1] = args.R;
+    }
+  } else {
+    for (int i = tid; i <= args.E; i += C::THREADS) s_offs[i] = args.offsets[i];
+  }
+  __syncthreads();
+  if (warp == 0) build_tiles(args, s_offs, s_tbase, NT, NG);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *s_tmem;
+  const int KB = (args.K + BK - 1) / BK;
+  const int total = s_tbase[args.E];
+  const int g = (int)cluster_id_x();
+  const int kb0 = (int)((int64_t)KB * rank / S), kb1 = (int)((int64_t)KB * (rank + 1) / S);
+  // (a cluster beyond the last tile has nothing to do; the tile index is uniform over a cluster)
+  const bool work = g < total;
+  Tile t = {0, 0, 0, 0};
+  if (work) t = decode_tile(g, args, s_offs, s_tbase, NT, NG);
+
+  if (total >= 0) zero_absent(args, s_offs, (int64_t)blockIdx.x * C::THREADS + tid, (int64_t)gridDim.x * C::THREADS);
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  __syncthreads();  // the tables have been read: the stages may be loaded
+
+  float* part = reinterpret_cast<float*>(smem);  // [NT][256], after the last MMA has read the stages
+  bool ok = true;
+  if (work && warp == 0) {
+    // ------------------------------------------------------------------ TMA producer (whole warp)
+    int r[4] = {0, 0, 0, 0};
+    const int nrow4 = (t.cnt + 3) >> 2;
+    if (GATHER && lane < nrow4) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) r[j] = source_row(args, t.p0 + min(4 * lane + j, t.cnt - 1));
+    }
+    const uint32_t bytes = 2 * BLK + (GATHER ? nrow4 * 4 : NT) * BK;
+    int i = 0;
+    for (int kb = kb0; kb < kb1; ++kb, ++i) {
+      const int s = i % NS;
+      if (!warp_wait(empty(s), ((i / NS) & 1) ^ 1, s_abort, err, limit)) {
+        ok = false;
+        break;
+      }
+      const uint32_t st = sbase + s * C::STAGE;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(full(s), bytes);
+        tma_load_3d(st, &wmap, kb * BK, block_row<2>(args, t.ng, 0), t.e, full(s));
+        tma_load_3d(st + BLK, &wmap, kb * BK, block_row<2>(args, t.ng, 1), t.e, full(s));
+        if (!GATHER) tma_load_2d(st + 2 * BLK, &amap, kb * BK, t.p0, full(s));
+      }
+      if (GATHER) {
+        __syncwarp();
+        if (lane < nrow4) tma_gather4(st + 2 * BLK + lane * 4 * BK, &amap, kb * BK, r[0], r[1], r[2], r[3], full(s));
+      }
+    }
+    if (!ok && lane == 0)
+      for (int j = max(0, i - NS); j < i; ++j) mbar_wait_drain(full(j % NS), (j / NS) & 1);
+  } else if (work && warp == 1) {
+    // ------------------------------------------------------------------ MMA issuer
+    constexpr uint32_t idesc = make_idesc_e4m3(128, NT);
+    int i = 0;
+    for (int kb = kb0; kb < kb1; ++kb, ++i) {
+      const int s = i % NS, db = i & 1;
+      if (!warp_wait(d_empty(db), ((i >> 1) & 1) ^ 1, s_abort, err, limit) ||
+          !warp_wait(full(s), (i / NS) & 1, s_abort, err, limit)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      const uint32_t st = sbase + s * C::STAGE;
+      if (elect_one()) {
+        const uint64_t tok = make_sdesc_sw128(st + 2 * BLK);
+        mma4_e4m3_ss(tmem_base + (uint32_t)(db * 2 * NT), make_sdesc_sw128(st), tok, idesc);
+        mma4_e4m3_ss(tmem_base + (uint32_t)(db * 2 * NT + NT), make_sdesc_sw128(st + BLK), tok, idesc);
+        mma_commit(empty(s));
+        mma_commit(d_full(db));
+      }
+      __syncwarp();
+    }
+    if (!ok) {
+      if (elect_one()) {
+        mma_commit(drain_bar);
+        mbar_wait_drain(drain_bar, 0);
+      }
+      __syncwarp();
+    }
+  } else if (work) {
+    // ------------------------------------------------------------------ accumulation
+    const int q = warp & 3;
+    const uint32_t lane_base = tmem_base + ((uint32_t)(q * 32) << 16);
+    // this warp's products sa * sw of the k block for both weight blocks: [2 buffers][2][NT]
+    float* s_f = reinterpret_cast<float*>(smem + C::OFF_SCALE) + (warp - 2) * 4 * NT;
+    constexpr int PT = (NT + 31) / 32;  // tokens whose scales this lane holds
+    const float* sa[PT];
+#pragma unroll
+    for (int j = 0; j < PT; ++j)
+      sa[j] = args.sa + (int64_t)source_row(args, t.p0 + min(lane + 32 * j, t.cnt - 1)) * args.sa_row;
+    const float* sw0 = args.sw + ((int64_t)t.e * args.nblk + (block_row<2>(args, t.ng, 0) >> 7)) * KB;
+    const float* sw1 =
+        args.sw + ((int64_t)t.e * args.nblk + min(block_row<2>(args, t.ng, 1) >> 7, args.nblk - 1)) * KB;
+    uint64_t acc[2][NT / 2];
+#pragma unroll
+    for (int j = 0; j < NT / 2; ++j) acc[0][j] = acc[1][j] = 0;
+    float pa[2][PT], pw[2][2];
+#pragma unroll
+    for (int d = 0; d < 2; ++d) {
+      const int k = min(kb0 + d, KB - 1);
+#pragma unroll
+      for (int j = 0; j < PT; ++j) pa[d][j] = __ldg(sa[j] + k * args.sa_grp);
+      pw[d][0] = __ldg(sw0 + k);
+      pw[d][1] = __ldg(sw1 + k);
+    }
+    int i = 0;
+    for (int kb = kb0; kb < kb1; ++kb, ++i) {
+      const int db = i & 1;
+      float* f = s_f + db * 2 * NT;
+#pragma unroll
+      for (int j = 0; j < PT; ++j) {
+        if (lane + 32 * j < NT) {
+          f[lane + 32 * j] = pa[0][j] * pw[0][0];
+          f[NT + lane + 32 * j] = pa[0][j] * pw[0][1];
+        }
+        pa[0][j] = pa[1][j];
+        pa[1][j] = __ldg(sa[j] + min(kb + 2, KB - 1) * args.sa_grp);
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        pw[0][h] = pw[1][h];
+        pw[1][h] = __ldg((h ? sw1 : sw0) + min(kb + 2, KB - 1));
+      }
+      __syncwarp();
+      if (!warp_wait(d_full(db), (i >> 1) & 1, s_abort, err, limit)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      const uint32_t base = lane_base + (uint32_t)(db * 2 * NT);
+#pragma unroll
+      for (int c = 0; c < 2 * NT / 16; ++c) {  // 16 columns: tokens 16 (c % (NT / 16)).. of block c / (NT / 16)
+        uint32_t v[16];
+        tmem_ld_32x32b_x16(base + c * 16, v);
+        tmem_wait_ld_regs(v);
+        if (c + 1 == 2 * NT / 16) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(d_empty(db));
+        }
+        const ulonglong2* fc = reinterpret_cast<const ulonglong2*>(f + c * 16);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const ulonglong2 ff = fc[j];
+          uint64_t* a = &acc[c / (NT / 16)][(c % (NT / 16)) * 8 + 2 * j];
+          fma_f32x2(a[0], v[4 * j], v[4 * j + 1], ff.x);
+          fma_f32x2(a[1], v[4 * j + 2], v[4 * j + 3], ff.y);
+        }
+      }
+    }
+    // Partial sums to shared memory: the last accumulator is complete, so every stage has been
+    // read and no copy is in flight.  (All four warps pass the last d_full before any writes.)
+    named_bar_sync(1, 128);
+    if (ok) {
+#pragma unroll
+      for (int j = 0; j < NT / 2; ++j)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float a0, a1;
+          unpack_f32x2(acc[h][j], a0, a1);
+          part[(2 * j) * 256 + h * 128 + q * 32 + lane] = a0;
+          part[(2 * j + 1) * 256 + h * 128 + q * 32 + lane] = a1;
+        }
+    }
+  }
+
+  if (S > 1) {
+    __syncwarp();
+    cluster_sync_all();
+  } else {
+    __syncthreads();
+  }
+  if (work && warp >= 2 && *s_abort == 0) {
+    // ------------------------------------------------------------------ join and store
+    // token n belongs to rank n % S, which adds the S partial sums in rank order
+    const int q = warp & 3;
+    const int j = q * 32 + lane;  // weight row of each block
+    uint32_t* s_amax = reinterpret_cast<uint32_t*>(smem + C::OFF_AMAX);
+    for (int n = rank; n < t.cnt; n += S) {
+      float v0 = 0.f, v1 = 0.f;
+      for (int c = 0; c < S; ++c) {
+        const uint32_t at = sbase + (uint32_t)(n * 256 + j) * 4u;
+        v0 += ld_shared_cluster_f32(at, (uint32_t)c);
+        v1 += ld_shared_cluster_f32(at + 512u, (uint32_t)c);
+      }
+      const int64_t p = t.p0 + n;
+      if (args.half) {
+        const float act = swiglu_keep_nan(v0, v1, args.limit);
+        part[n * 256 + j] = act;  // only this thread reads this element of this CTA's token n
+        const uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(act) & 0x7FFFFFFFu);
+        if (lane == 0) s_amax[n * 4 + q] = m;
+      } else {
+        const int n0 = block_row<2>(args, t.ng, 0) + j, n1 = n0 + 128;
+        if (args.c_dtype == MOE_DTYPE_BF16) {
+          __nv_bfloat16* c = static_cast<__nv_bfloat16*>(args.C) + p * args.ldc;
+          if (n0 < args.N) c[n0] = __float2bfloat16_rn(v0);
+          if (n1 < args.N) c[n1] = __float2bfloat16_rn(v1);
+        } else {
+          float* c = static_cast<float*>(args.C) + p * args.ldc;
+          if (n0 < args.N) c[n0] = v0;
+          if (n1 < args.N) c[n1] = v1;
+        }
+      }
+    }
+    if (args.half) {
+      named_bar_sync(1, 128);
+      for (int n = rank; n < t.cnt; n += S) {
+        const uint4 m4 = *reinterpret_cast<const uint4*>(s_amax + n * 4);
+        float scale, inv;
+        fp8_scale(max(max(m4.x, m4.y), max(m4.z, m4.w)), scale, inv);
+        const int64_t p = t.p0 + n;
+        const uint32_t code = pack_e4m3x4(part[n * 256 + j] * inv, 0.f, 0.f, 0.f);
+        args.q[p * args.ld_q + t.ng * 128 + j] = (uint8_t)code;
+        if (j == 0) args.s[p * args.s_row + t.ng * args.s_grp] = scale;
+      }
+    }
+  }
+  tc_fence_before();
+  if (S > 1) {  // the other CTAs have read this one's partial sums
+    __syncwarp();
+    cluster_sync_all();
+  } else {
+    __syncthreads();
+  }
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem_base, C::TMEM_COLS);
+  }
+}
+
+// ------------------------------------------------------------------------------------------------
+// launches
+
+template <class K>
+int configure(K kernel, int smem, std::atomic<int>* configured) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return MOE_ERR_CUDA;
+  if (!configured[dev].load(std::memory_order_acquire)) {
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+      return MOE_ERR_CUDA;
+    configured[dev].store(1, std::memory_order_release);
+  }
+  return MOE_OK;
+}
+
+int a_map(CUtensorMap* m, const Fp8Gemm& d, int box_rows) {
+  const cuuint64_t dims[2] = {(cuuint64_t)d.args.K, (cuuint64_t)d.args.a_rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)d.lda};
+  const cuuint32_t box[2] = {(cuuint32_t)BK, (cuuint32_t)box_rows};
+  const cuuint32_t estr[2] = {1, 1};
+  return encode_tmap(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(d.A), dims, strides, box, estr,
+                     CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+int w_map(CUtensorMap* m, const Fp8Gemm& d) {
+  const cuuint64_t dims[3] = {(cuuint64_t)d.args.K, (cuuint64_t)d.args.N, (cuuint64_t)d.args.e_count};
+  const cuuint64_t strides[2] = {(cuuint64_t)d.ldw, (cuuint64_t)d.w_expert};
+  const cuuint32_t box[3] = {(cuuint32_t)BK, 128, 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return encode_tmap(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<uint8_t*>(d.W), dims, strides, box, estr,
+                     CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+template <class C, bool GATHER>
+int launch_wide(const Fp8Gemm& d, int64_t tiles, cudaStream_t st) {
+  CUtensorMap am, wm;
+  int rc = a_map(&am, d, GATHER ? 1 : 128);
+  if (rc == MOE_OK) rc = w_map(&wm, d);
+  if (rc != MOE_OK) return rc;
+  static std::atomic<int> configured[64];
+  if ((rc = configure(wide_kernel<C, GATHER>, C::SMEM, configured)) != MOE_OK) return rc;
+  const int grid = (int)std::min<int64_t>(tiles, device_sm_count());
+  return launch_pdl(wide_kernel<C, GATHER>, dim3(grid), dim3(C::THREADS), C::SMEM, st, am, wm, d.args);
+}
+
+template <class C, bool GATHER>
+int launch_few(const Fp8Gemm& d, int64_t tiles, cudaStream_t st) {
+  CUtensorMap am, wm;
+  int rc = a_map(&am, d, GATHER ? 1 : C::NT);
+  if (rc == MOE_OK) rc = w_map(&wm, d);
+  if (rc != MOE_OK) return rc;
+  static std::atomic<int> configured[64];
+  if ((rc = configure(few_kernel<C, GATHER>, C::SMEM, configured)) != MOE_OK) return rc;
+  // split k while the tiles leave CTA slots free and every CTA keeps two k blocks
+  const int slots = device_sm_count() * C::PER_SM;
+  const int KB = (d.args.K + BK - 1) / BK;
+  int S = 1;
+  while (S < 8 && tiles * 2 * S <= slots && KB >= 4 * S) S *= 2;
+  return launch_pdl_cluster(few_kernel<C, GATHER>, dim3((unsigned)(tiles * S)), dim3(C::THREADS), C::SMEM, st, S, am,
+                            wm, d.args);
+}
+
+// Upper bound of the number of token tiles of BT rows: experts with rows plus their full tiles.
+int64_t token_tiles(const Fp8Gemm& d, int BT) {
+  const Fp8GemmArgs& a = d.args;
+  if (a.offsets == nullptr) return (a.R + BT - 1) / BT;
+  return std::min<int64_t>(a.R, std::min<int64_t>(a.R, a.e_count) + a.R / BT);
+}
+
+template <bool GATHER>
+int launch(const Fp8Gemm& d, cudaStream_t st) {
+  const Fp8GemmArgs& a = d.args;
+  const int groups = a.offsets == nullptr ? 1 : std::min(a.E, a.R);
+  const double rows = (double)a.R / groups;  // per expert
+  const int64_t ng2 = a.half ? a.half / 128 : (a.N + 255) / 256;
+  if (rows <= 12) return launch_few<FewCfg<16, 3, 2>, GATHER>(d, token_tiles(d, 16) * ng2, st);
+  if (rows <= 40) return launch_few<FewCfg<32, 3, 2>, GATHER>(d, token_tiles(d, 32) * ng2, st);
+  const int64_t tt = token_tiles(d, 128);
+  if (!a.half && tt * ng2 < device_sm_count())
+    return launch_wide<WideCfg<1>, GATHER>(d, tt * ((a.N + 127) / 128), st);
+  return launch_wide<WideCfg<2>, GATHER>(d, tt * ng2, st);
+}
+
+}  // namespace f8
+
+int fp8_gemm_launch(const Fp8Gemm& d, cudaStream_t st) {
+  if (device_sm_count() <= 0) return MOE_ERR_CUDA;
+  return d.args.gather != nullptr ? f8::launch<true>(d, st) : f8::launch<false>(d, st);
+}
+
+}  // namespace moe

@@ -1,0 +1,259 @@
+// fp8_quant.cu -- quantisation to E4M3 with one FP32 scale per 128 elements of a row (activations)
+// or per 128 x 128 block (weights): the operands of the FP8 products.
+//
+//   a = max(max |x| over the group, 2^-100),  s = a / 448,  q = e4m3(x * (448 / a))
+//
+// in FP32 with correctly rounded division and multiplication; q rounds to nearest even (x * 448/a
+// is at most 448 (1 + 2^-23), which rounds to 448, so nothing saturates).  The floor of a keeps
+// 448 / a and s normal FP32 numbers; a group of zeros gives q = 0.  A group with an infinity or a
+// NaN gives s = NaN and codes NaN: whatever reads it is NaN, no finite value stands for it.
+//
+// Bound by memory: each element is read once (held in registers between the maximum and the
+// rounding), its code is written once.
+
+#include <algorithm>
+
+#include "fp8.cuh"
+#include "internal.h"
+
+namespace moe {
+namespace fq {
+
+constexpr int G = 128;
+
+// Bits of |x| compare like the magnitudes, with inf above every number and NaN above inf, so an
+// unsigned maximum keeps what is not finite.
+MOE_DEV uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
+
+template <typename T>
+MOE_DEV float load1(const T* p);
+template <>
+MOE_DEV float load1<uint16_t>(const uint16_t* p) {
+  return __uint_as_float((uint32_t)__ldg(p) << 16);
+}
+template <>
+MOE_DEV float load1<float>(const float* p) {
+  return __ldg(p);
+}
+
+// 16 consecutive elements, 16-byte aligned
+MOE_DEV void load16(const uint16_t* p, float (&v)[16]) {
+  const uint4 a = __ldg(reinterpret_cast<const uint4*>(p));
+  const uint4 b = __ldg(reinterpret_cast<const uint4*>(p) + 1);
+  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    v[2 * i] = bf16_lo(w[i]);
+    v[2 * i + 1] = bf16_hi(w[i]);
+  }
+}
+MOE_DEV void load16(const float* p, float (&v)[16]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float4 a = __ldg(reinterpret_cast<const float4*>(p) + i);
+    v[4 * i] = a.x;
+    v[4 * i + 1] = a.y;
+    v[4 * i + 2] = a.z;
+    v[4 * i + 3] = a.w;
+  }
+}
+
+// Rows, 16 elements to a lane and 8 lanes to a group: a warp takes four consecutive groups of one
+// row.  For 16-byte aligned rows (VEC); K need not be a multiple of 16 (the last lane's elements
+// are then loaded one by one).
+template <typename T>
+__global__ void __launch_bounds__(256) rows_vec_kernel(const T* __restrict__ x, int64_t ld_x, int R, int K, uint8_t* q,
+                                                       int64_t ld_q, float* s, int64_t s_row, int64_t s_grp) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int lane = threadIdx.x & 31;
+  const int sub = lane & 7;
+  const int ngrp = (K + G - 1) / G;
+  const int per_row = (ngrp + 3) / 4;
+  const int64_t items = (int64_t)R * per_row;
+  const int64_t step = (int64_t)gridDim.x * (blockDim.x >> 5);
+  for (int64_t it = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); it < items; it += step) {
+    const int64_t row = it / per_row;
+    const int grp = (int)(it - row * per_row) * 4 + (lane >> 3);
+    const int k0 = grp * G + sub * 16;
+    const int n = max(0, min(16, K - k0));
+    float v[16];
+    if (n == 16) {
+      load16(x + row * ld_x + k0, v);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) v[i] = i < n ? load1(x + row * ld_x + k0 + i) : 0.f;
+    }
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) m = max(m, abs_bits(v[i]));
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+    float scale, inv;
+    fp8_scale(m, scale, inv);
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      w[i] = pack_e4m3x4(v[4 * i] * inv, v[4 * i + 1] * inv, v[4 * i + 2] * inv, v[4 * i + 3] * inv);
+    uint8_t* dst = q + row * ld_q + k0;
+    if (n == 16) {
+      *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (i < n) dst[i] = (uint8_t)(w[i >> 2] >> (8 * (i & 3)));
+    }
+    if (sub == 0 && grp < ngrp) s[row * s_row + grp * s_grp] = scale;
+  }
+}
+
+// Rows of any alignment, 4 consecutive elements to a lane and a warp to a group; U groups in flight
+// per warp.  Codes are stored as words (q is 16-byte aligned with ld_q a multiple of 16).
+template <typename T, int U>
+__global__ void __launch_bounds__(256) rows_any_kernel(const T* __restrict__ x, int64_t ld_x, int R, int K, uint8_t* q,
+                                                       int64_t ld_q, float* s, int64_t s_row, int64_t s_grp) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int lane = threadIdx.x & 31;
+  const int ngrp = (K + G - 1) / G;
+  const int per_row = (ngrp + U - 1) / U;
+  const int64_t items = (int64_t)R * per_row;
+  const int64_t step = (int64_t)gridDim.x * (blockDim.x >> 5);
+  for (int64_t it = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); it < items; it += step) {
+    const int64_t row = it / per_row;
+    const int g0 = (int)(it - row * per_row) * U;
+    const T* src = x + row * ld_x;
+    float v[U][4];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int k = (g0 + u) * G + lane * 4 + i;
+        v[u][i] = k < K ? load1(src + k) : 0.f;
+      }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (g0 + u >= ngrp) break;
+      uint32_t m = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) m = max(m, abs_bits(v[u][i]));
+      m = __reduce_max_sync(0xffffffffu, m);
+      float scale, inv;
+      fp8_scale(m, scale, inv);
+      const uint32_t w = pack_e4m3x4(v[u][0] * inv, v[u][1] * inv, v[u][2] * inv, v[u][3] * inv);
+      const int k0 = (g0 + u) * G + lane * 4;
+      uint8_t* dst = q + row * ld_q + k0;
+      if (k0 + 4 <= K) {
+        *reinterpret_cast<uint32_t*>(dst) = w;
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (k0 + i < K) dst[i] = (uint8_t)(w >> (8 * i));
+      }
+      if (lane == 0) s[row * s_row + (g0 + u) * s_grp] = scale;
+    }
+  }
+}
+
+// Weights: a CTA of 256 threads per 128 x 128 block, 64 elements to a thread (lane: 4 consecutive
+// columns; warp w: rows w, w + 8, ...).  VEC: 4-element loads (rows 4-element aligned).
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(256) blocks_kernel(const T* __restrict__ w, int64_t ld_w, int N, int K, uint8_t* q,
+                                                     int64_t ld_q, float* s) {
+  __shared__ uint32_t s_max[8];
+  griddep_wait();
+  griddep_launch_dependents();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int k0 = blockIdx.x * G + lane * 4;
+  const int n0 = blockIdx.y * G + warp;
+  float v[16][4];
+  uint32_t m = 0;
+#pragma unroll
+  for (int r = 0; r < 16; ++r) {
+    const int n = n0 + 8 * r;
+    const T* src = w + (int64_t)n * ld_w + k0;
+    if (VEC && n < N && k0 + 4 <= K) {
+      if constexpr (sizeof(T) == 2) {
+        const uint2 a = __ldg(reinterpret_cast<const uint2*>(src));
+        v[r][0] = bf16_lo(a.x);
+        v[r][1] = bf16_hi(a.x);
+        v[r][2] = bf16_lo(a.y);
+        v[r][3] = bf16_hi(a.y);
+      } else {
+        const float4 a = __ldg(reinterpret_cast<const float4*>(src));
+        v[r][0] = a.x;
+        v[r][1] = a.y;
+        v[r][2] = a.z;
+        v[r][3] = a.w;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[r][i] = n < N && k0 + i < K ? load1(src + i) : 0.f;
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < 16; ++r)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m = max(m, abs_bits(v[r][i]));
+  m = __reduce_max_sync(0xffffffffu, m);
+  if (lane == 0) s_max[warp] = m;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = max(m, s_max[i]);
+  float scale, inv;
+  fp8_scale(m, scale, inv);
+#pragma unroll
+  for (int r = 0; r < 16; ++r) {
+    const int n = n0 + 8 * r;
+    if (n >= N) break;
+    const uint32_t c = pack_e4m3x4(v[r][0] * inv, v[r][1] * inv, v[r][2] * inv, v[r][3] * inv);
+    uint8_t* dst = q + (int64_t)n * ld_q + k0;
+    if (k0 + 4 <= K) {
+      *reinterpret_cast<uint32_t*>(dst) = c;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (k0 + i < K) dst[i] = (uint8_t)(c >> (8 * i));
+    }
+  }
+  if (threadIdx.x == 0) s[(int64_t)blockIdx.y * gridDim.x + blockIdx.x] = scale;
+}
+
+template <typename T>
+int rows(const T* x, int64_t ld_x, int R, int K, uint8_t* q, int64_t ld_q, float* s, int64_t s_row, int64_t s_grp,
+         cudaStream_t st) {
+  const int nsm = device_sm_count();
+  if (nsm <= 0) return MOE_ERR_CUDA;
+  const int ngrp = (K + G - 1) / G;
+  const bool vec = reinterpret_cast<uintptr_t>(x) % 16 == 0 && (ld_x * (int64_t)sizeof(T)) % 16 == 0;
+  constexpr int U = 4;
+  const int64_t warps = (int64_t)R * ((ngrp + 3) / 4);  // both kernels give a warp four groups
+  const int grid = (int)std::min<int64_t>((warps + 7) / 8, (int64_t)nsm * 8);
+  return vec ? launch_pdl(rows_vec_kernel<T>, dim3(grid), dim3(256), 0, st, x, ld_x, R, K, q, ld_q, s, s_row, s_grp)
+             : launch_pdl(rows_any_kernel<T, U>, dim3(grid), dim3(256), 0, st, x, ld_x, R, K, q, ld_q, s, s_row, s_grp);
+}
+
+template <typename T>
+int blocks(const T* w, int64_t ld_w, int N, int K, uint8_t* q, int64_t ld_q, float* s, cudaStream_t st) {
+  const dim3 grid((K + G - 1) / G, (N + G - 1) / G);
+  const bool vec = reinterpret_cast<uintptr_t>(w) % (4 * sizeof(T)) == 0 && ld_w % 4 == 0;
+  return vec ? launch_pdl(blocks_kernel<T, true>, grid, dim3(256), 0, st, w, ld_w, N, K, q, ld_q, s)
+             : launch_pdl(blocks_kernel<T, false>, grid, dim3(256), 0, st, w, ld_w, N, K, q, ld_q, s);
+}
+
+}  // namespace fq
+
+int fp8_quantize_rows_launch(const void* x, int x_dtype, int64_t ld_x, int R, int K, uint8_t* q, int64_t ld_q, float* s,
+                             int64_t s_row, int64_t s_grp, cudaStream_t st) {
+  return x_dtype == MOE_DTYPE_BF16
+             ? fq::rows(static_cast<const uint16_t*>(x), ld_x, R, K, q, ld_q, s, s_row, s_grp, st)
+             : fq::rows(static_cast<const float*>(x), ld_x, R, K, q, ld_q, s, s_row, s_grp, st);
+}
+
+int fp8_quantize_blocks_launch(const void* w, int w_dtype, int64_t ld_w, int N, int K, uint8_t* q, int64_t ld_q,
+                               float* s, cudaStream_t st) {
+  return w_dtype == MOE_DTYPE_BF16 ? fq::blocks(static_cast<const uint16_t*>(w), ld_w, N, K, q, ld_q, s, st)
+                                   : fq::blocks(static_cast<const float*>(w), ld_w, N, K, q, ld_q, s, st);
+}
+
+}  // namespace moe

@@ -58,6 +58,8 @@ struct GemmArgs {
 int encode_tmap(CUtensorMap* map, CUtensorMapDataType dtype, int rank, void* base, const cuuint64_t* dims,
                 const cuuint64_t* strides_bytes, const cuuint32_t* box, const cuuint32_t* elem_strides,
                 CUtensorMapSwizzle swizzle);
+// Once per device: the compute capability check, the SM count and the error word address.
+int ensure_device();
 int device_sm_count();
 int* device_error_word();  // device address of the current device's error word
 
@@ -153,6 +155,41 @@ struct DenseGemm {
 int dense_gemm_launch(const DenseGemm& d, cudaStream_t stream);
 // token-tile width the launch takes for T tokens over weight_tiles tiles of 128 weight rows
 int dense_gemm_token_tile(int T, int weight_tiles, int nsm);
+
+// FP8 quantisation (fp8_quant.cu); x and w of MOE_DTYPE_BF16 or MOE_DTYPE_F32, arguments checked
+int fp8_quantize_rows_launch(const void* x, int x_dtype, int64_t ld_x, int R, int K, uint8_t* q, int64_t ld_q, float* s,
+                             int64_t s_row, int64_t s_grp, cudaStream_t st);
+int fp8_quantize_blocks_launch(const void* w, int w_dtype, int64_t ld_w, int N, int K, uint8_t* q, int64_t ld_q,
+                               float* s, cudaStream_t st);
+
+// FP8 products (fp8_gemm.cu)
+struct Fp8GemmArgs {
+  const float* sa;         // activation scales: (row, group) at row * sa_row + group * sa_grp
+  int64_t sa_row, sa_grp;
+  const float* sw;         // weight scales [e_count][nblk][ceil(K / 128)]
+  const int32_t* gather;   // device [R] or NULL (sorted row p is row p of A)
+  const int32_t* offsets;  // device [E + 1]; NULL: one group of R rows (E = 1)
+  void* C;                 // [R, ldc] of c_dtype (plain form)
+  int64_t ldc;
+  uint8_t* q;              // gate/up form: codes [R, ld_q] and scales of act
+  int64_t ld_q;
+  float* s;
+  int64_t s_row, s_grp;
+  uint64_t wait_ns;        // bound of every pipeline wait
+  int* err;                // device error word
+  int E, e_first, e_count; // experts of offsets; those W holds
+  int N, K, R, a_rows, nblk, c_dtype;
+  int half;                // 0, or I of the gate/up form (N = 2 I, a multiple of 128)
+  float limit;
+};
+struct Fp8Gemm {
+  const uint8_t* A;
+  int64_t lda;
+  const uint8_t* W;
+  int64_t ldw, w_expert;
+  Fp8GemmArgs args;
+};
+int fp8_gemm_launch(const Fp8Gemm& d, cudaStream_t st);
 
 // shared expert (shared_expert.cu): workspace = gate|up [T, 2I] BF16 and act [T, I] BF16, each
 // 256-byte aligned; returns the total bytes
