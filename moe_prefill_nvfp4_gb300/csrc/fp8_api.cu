@@ -34,12 +34,12 @@ int check(const moe_fp8_rows* A, const moe_fp8_weight* W, int R, int E) {
 Fp8Gemm make(const moe_fp8_rows* A, const int32_t* gather_ids, const moe_fp8_weight* W, const int32_t* offsets, int E,
              int R) {
   Fp8Gemm d = {};
-  d.A = A->q;
-  d.lda = A->ld;
   d.W = W->q;
   d.ldw = W->ld;
   d.w_expert = W->count > 1 ? W->expert_stride : (W->ld * (int64_t)W->N);
   Fp8GemmArgs& a = d.args;
+  a.A = A->q;
+  a.lda = A->ld;
   a.sa = A->s;
   a.sa_row = A->s_row;
   a.sa_grp = A->s_grp;

@@ -122,10 +122,26 @@ MOE_DEV bool wait_bounded(uint32_t bar, uint32_t parity, volatile int* abort_fla
   }
 }
 
+// By a whole warp, every lane polling (a poll by one lane and a shuffle took longer).
 MOE_DEV bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* err, uint64_t limit) {
-  bool ok = true;
-  if (lane_id() == 0) ok = wait_bounded(bar, parity, abort_flag, err, limit);
-  return __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+  return __all_sync(0xffffffffu, wait_bounded(bar, parity, abort_flag, err, limit));
+}
+
+// Orders generic-proxy accesses of shared memory before later asynchronous ones (TMA, MMA).
+MOE_DEV void fence_proxy_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// Asynchronous 16-byte copy to shared memory, the first `bytes` of it from global memory, zeros after.
+MOE_DEV void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+MOE_DEV void cp_async4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+MOE_DEV void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Waits until at most N of this thread's committed groups of copies are still on their way.
+template <int N>
+MOE_DEV void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 // named_bar_sync that tells every thread whether any of them had pred set.
@@ -276,14 +292,17 @@ template <int NB_>
 struct WideCfg {
   static constexpr int NB = NB_;           // weight blocks of 128 per tile
   static constexpr int BN = NB * 128;
-  static constexpr int THREADS = 384;      // warpgroup 0: producer, MMA; warpgroups 1, 2: epilogue
+  static constexpr int THREADS = 384;      // warpgroup 0: producer, MMA, scales; 1 and 2: epilogue
   static constexpr int STAGE = BLK + NB * BLK;
   static constexpr int NS = NB == 2 ? 4 : 6;
   static constexpr int TMEM_COLS = 2 * BN;
   static constexpr int EPI_WARP = 32 * 64;  // 32 rows x 64 bytes
   static constexpr int OFF_EPI = NS * STAGE;
   static constexpr int OFF_AMAX = OFF_EPI + 8 * EPI_WARP;      // uint32 [2][128]
-  static constexpr int OFF_OFFS = OFF_AMAX + 2 * 128 * 4;
+  static constexpr int NF = 4;              // k blocks whose scales are held
+  static constexpr int F_SLOT = 128 + 4;    // sa of the rows, then sw of the blocks
+  static constexpr int OFF_F = OFF_AMAX + 2 * 128 * 4;         // float [NF][F_SLOT]
+  static constexpr int OFF_OFFS = OFF_F + NF * F_SLOT * 4;
   static constexpr int OFF_TBASE = OFF_OFFS + (MAX_E + 1) * 4;
   static constexpr int OFF_BAR = (OFF_TBASE + (MAX_E + 1) * 4 + 7) & ~7;
   // full[NS] empty[NS] d_full[2] d_empty[2] drain
@@ -291,13 +310,15 @@ struct WideCfg {
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
   static constexpr int BYTES = OFF_MISC + 16;
   static constexpr int SMEM = BYTES + 1024;
-  // registers: the launch has 384 x 168; 128 x 56 + 256 x 224 is the same number
-  static constexpr int REG_LOW = 56, REG_HIGH = 224;
+  // registers: the launch has 384 x 168; 128 x 72 + 256 x 216 is the same number
+  static constexpr int REG_LOW = 72, REG_HIGH = 216;
   static_assert(128 * REG_LOW + 256 * REG_HIGH <= THREADS * 168, "register split");
   static_assert(SMEM > 232448 / 2 && SMEM <= 232448, "one CTA per SM (it takes all of TMEM)");
 };
 
-// Warp roles: 0 TMA producer, 1 MMA issuer and TMEM owner, 4-11 epilogue (two warpgroups; warp w
+// Warp roles: 0 (and 3, gathering) operand producers, 1 MMA issuer and TMEM owner, 2 the scales of each
+// k block into shared memory (asynchronously and blocks ahead, across tiles too: epilogue threads that
+// loaded their own scales waited for L2 in every block), 4-11 epilogue (two warpgroups; warp w
 // reads TMEM lanes 32 (w % 4).., warpgroup g the columns 64 g .. 64 g + 63 of each weight block, so
 // that in the gate/up form a thread holds a gate column and its up column).
 template <class C, bool GATHER>
@@ -318,6 +339,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   const uint32_t drain_bar = bar0 + 8u * (2 * NS + 4);
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
   volatile int* s_abort = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
+  float* s_f = reinterpret_cast<float*>(smem + C::OFF_F);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint64_t limit = args.wait_ns;
@@ -325,11 +347,11 @@ __global__ void __launch_bounds__(C::THREADS, 1)
 
   if (tid == 0) {
     for (int s = 0; s < NS; ++s) {
-      mbar_init(full(s), 1);
+      mbar_init(full(s), GATHER ? 3 : 1);  // TMA, the two gathering warps
       mbar_init(empty(s), 1);
     }
     for (int d = 0; d < 2; ++d) {
-      mbar_init(d_full(d), 1);
+      mbar_init(d_full(d), 2);   // MMA commit, scales
       mbar_init(d_empty(d), 8);  // the epilogue warps
     }
     mbar_init(drain_bar, 1);
@@ -362,23 +384,32 @@ __global__ void __launch_bounds__(C::THREADS, 1)
 
   if (warp < 4) {
     reg_dec<C::REG_LOW>();
-    if (warp == 0) {
-      // ---------------------------------------------------------------- TMA producer (whole warp)
-      if (lane == 0) {
+    if (warp == 0 || (GATHER && warp == 3)) {
+      // ---------------------------------------------------------------- operand producers
+      // TMA (one lane of warp 0): the weight blocks, and the token rows where they are contiguous.
+      // Gathered token rows: warps 0 and 3 copy 64 rows each with 16-byte cp.async into the swizzled
+      // layout (chunk c of row r at c ^ (r % 8)), 4 rows to an instruction; rows past the tile's are
+      // left as they are (their accumulator rows are not stored).
+      if (warp == 0 && lane == 0) {
         prefetch_tmap(&amap);
         prefetch_tmap(&wmap);
       }
+      const int r0 = (warp ? 64 : 0) + (lane >> 3);  // this lane's first row, then every fourth
+      const int chunk = lane & 7;
+      auto hand_over = [&](uint32_t bar) {
+        fence_proxy_async_shared();  // written by the generic proxy, read by the MMA
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar);
+      };
       int i = 0;
       bool ok = true;
       for (int g = blockIdx.x; ok && g < total; g += gridDim.x) {
         const Tile t = decode_tile(g, args, s_offs, s_tbase, 128, NG);
-        int r[4] = {0, 0, 0, 0};
-        const int nrow4 = (t.cnt + 3) >> 2;  // gathered rows come in fours
-        if (GATHER && lane < nrow4) {
+        int src[16];
+        if (GATHER) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) r[j] = source_row(args, t.p0 + min(4 * lane + j, t.cnt - 1));
+          for (int j = 0; j < 16; ++j) src[j] = r0 + 4 * j < t.cnt ? source_row(args, t.p0 + r0 + 4 * j) : -1;
         }
-        const uint32_t bytes = NB * BLK + (GATHER ? nrow4 * 4 * BK : BLK);
         for (int kb = 0; kb < KB; ++kb, ++i) {
           const int s = i % NS;
           if (!warp_wait(empty(s), ((i / NS) & 1) ^ 1, s_abort, err, limit)) {
@@ -386,8 +417,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             break;
           }
           const uint32_t st = sbase + s * C::STAGE;
-          if (lane == 0) {
-            mbar_arrive_expect_tx(full(s), bytes);
+          if (warp == 0 && lane == 0) {
+            mbar_arrive_expect_tx(full(s), (GATHER ? 0 : BLK) + NB * BLK);
             if (!GATHER) tma_load_2d(st, &amap, kb * BK, t.p0, full(s));
 #pragma unroll
             for (int h = 0; h < NB; ++h)
@@ -395,11 +426,28 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           }
           if (GATHER) {
             __syncwarp();
-            if (lane < nrow4) tma_gather4(st + lane * 4 * BK, &amap, kb * BK, r[0], r[1], r[2], r[3], full(s));
+            const int k = kb * BK + chunk * 16;
+            const uint32_t bytes = (uint32_t)max(0, min(16, args.K - k));
+            const uint8_t* col = args.A + (bytes ? k : 0);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              const int r = r0 + 4 * j;
+              if (src[j] >= 0)
+                cp_async16(st + r * BK + ((chunk ^ (r & 7)) << 4), col + src[j] * args.lda, bytes);
+            }
+            cp_async_commit();
+            if (i > 0) {  // the stage before has landed
+              cp_async_wait<1>();
+              hand_over(full((i - 1) % NS));
+            }
           }
         }
       }
-      if (!ok && lane == 0)  // every copy issued lands before the CTA leaves
+      if (GATHER) {
+        cp_async_wait<0>();
+        if (ok && i > 0) hand_over(full((i - 1) % NS));
+      }
+      if (!ok && warp == 0 && lane == 0)  // every copy issued lands before the CTA leaves
         for (int j = max(0, i - NS); j < i; ++j) mbar_wait_drain(full(j % NS), (j / NS) & 1);
     } else if (warp == 1) {
       // ---------------------------------------------------------------- MMA issuer
@@ -431,6 +479,49 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         }
         __syncwarp();
       }
+    } else if (warp == 2) {
+      // ---------------------------------------------------------------- scales of every k block
+      // Block i's copies are issued two blocks ahead, into the slot that block i - 4 left; once the
+      // accumulator buffer of block i is free its arrival joins the MMA's commit.
+      const float* sa[4];
+      const float* sw = nullptr;
+      int g = blockIdx.x, kb = 0, n = 0;  // the next block to copy
+      auto copy_next = [&]() {
+        if (g < total) {
+          if (kb == 0) {
+            const Tile t = decode_tile(g, args, s_offs, s_tbase, 128, NG);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              sa[j] = args.sa + (int64_t)source_row(args, t.p0 + min(32 * j + lane, t.cnt - 1)) * args.sa_row;
+            // lane h < NB: block h's (past N: any scale, the block's columns are not stored)
+            const int blk = min(block_row<NB>(args, t.ng, min(lane, NB - 1)) >> 7, args.nblk - 1);
+            sw = args.sw + ((int64_t)t.e * args.nblk + blk) * KB;
+          }
+          const uint32_t dst = sbase + C::OFF_F + (uint32_t)((n % C::NF) * C::F_SLOT + lane) * 4u;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            cp_async4(dst + 128u * j, sa[j]);
+            sa[j] += args.sa_grp;
+          }
+          if (lane < NB) cp_async4(dst + 512u, sw + kb);
+          if (++kb == KB) {
+            kb = 0;
+            g += gridDim.x;
+          }
+          ++n;
+        }
+        cp_async_commit();  // (an empty group past the last block)
+      };
+      copy_next();
+      copy_next();
+      for (int i = 0; i < n; ++i) {
+        if (!warp_wait(d_empty(i & 1), ((i >> 1) & 1) ^ 1, s_abort, err, limit)) break;
+        cp_async_wait<1>();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(d_full(i & 1));
+        copy_next();
+      }
+      cp_async_wait<0>();
     }
   } else {
     // ------------------------------------------------------------------ epilogue
@@ -446,58 +537,49 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     bool ok = true;
     for (int g = blockIdx.x; ok && g < total; g += gridDim.x) {
       const Tile t = decode_tile(g, args, s_offs, s_tbase, 128, NG);
-      const float* sa = args.sa + (int64_t)source_row(args, t.p0 + min(row, t.cnt - 1)) * args.sa_row;
-      const float* sw[NB];
-#pragma unroll
-      for (int h = 0; h < NB; ++h)  // (a block past N: any scale, its columns are not stored)
-        sw[h] = args.sw + ((int64_t)t.e * args.nblk + min(block_row<NB>(args, t.ng, h) >> 7, args.nblk - 1)) * KB;
       uint64_t acc[NB][32];
 #pragma unroll
       for (int h = 0; h < NB; ++h)
 #pragma unroll
         for (int j = 0; j < 32; ++j) acc[h][j] = 0;
-      // scales two k blocks ahead
-      float pa[2], pw[2][NB];
-#pragma unroll
-      for (int d = 0; d < 2; ++d) {
-        const int k = min(d, KB - 1);
-        pa[d] = __ldg(sa + k * args.sa_grp);
-#pragma unroll
-        for (int h = 0; h < NB; ++h) pw[d][h] = __ldg(sw[h] + k);
-      }
       for (int kb = 0; kb < KB; ++kb, ++i) {
         const int db = i & 1;
-        uint64_t f[NB];
-#pragma unroll
-        for (int h = 0; h < NB; ++h) {
-          const float v = pa[0] * pw[0][h];
-          f[h] = pack_f32x2(v, v);
-          pw[0][h] = pw[1][h];
-          pw[1][h] = __ldg(sw[h] + min(kb + 2, KB - 1));
-        }
-        pa[0] = pa[1];
-        pa[1] = __ldg(sa + min(kb + 2, KB - 1) * args.sa_grp);
         if (!warp_wait(d_full(db), (i >> 1) & 1, s_abort, err, limit)) {
           ok = false;
           break;
         }
         tc_fence_after();
         const uint32_t base = lane_base + (uint32_t)(db * C::BN);
-        uint32_t v[2][32];
-        tmem_ld_32x32b_x32(base, v[0]);
+        uint64_t f[NB];
 #pragma unroll
-        for (int c = 0; c < 2 * NB; ++c) {  // 32 columns of block c / 2
-          tmem_wait_ld_regs(v[c & 1]);
-          if (c + 1 < 2 * NB) {
-            tmem_ld_32x32b_x32(base + (uint32_t)(((c + 1) >> 1) * 128 + ((c + 1) & 1) * 32), v[(c + 1) & 1]);
-          } else {  // the accumulator may be overwritten
+        for (int h = 0; h < NB; ++h) {
+          const float* slot = s_f + (i % C::NF) * C::F_SLOT;
+          const float v = slot[row] * slot[128 + h];
+          f[h] = pack_f32x2(v, v);
+        }
+        // 16 columns at a time through two register buffers (column j of this warp's 64 NB is column
+        // j % 64 of block j / 64); the accumulator is given back once its last columns are in registers
+        uint32_t v[2][16];
+        auto load = [&](int c) {
+          tmem_ld_32x32b_x16(base + (uint32_t)((c >> 2) * 128 + (c & 3) * 16), v[c & 1]);
+        };
+        load(0);
+        load(1);
+#pragma unroll
+        for (int c = 0; c < 4 * NB; c += 2) {
+          tmem_wait_ld_regs(v[0]);
+          tmem_wait_ld_regs(v[1]);
+          if (c == 4 * NB - 2) {
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(d_empty(db));
           }
 #pragma unroll
-          for (int j = 0; j < 16; ++j)
-            fma_f32x2(acc[c >> 1][(c & 1) * 16 + j], v[c & 1][2 * j], v[c & 1][2 * j + 1], f[c >> 1]);
+          for (int d = c; d < c + 2; ++d) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) fma_f32x2(acc[d >> 2][(d & 3) * 8 + j], v[d & 1][2 * j], v[d & 1][2 * j + 1], f[d >> 2]);
+            if (d + 2 < 4 * NB) load(d + 2);
+          }
         }
       }
       const bool gate_up = NB == 2 && args.half != 0;
@@ -678,7 +760,7 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
   if (work) t = decode_tile(g, args, s_offs, s_tbase, NT, NG);
 
   if (total >= 0) zero_absent(args, s_offs, (int64_t)blockIdx.x * C::THREADS + tid, (int64_t)gridDim.x * C::THREADS);
-  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  fence_proxy_async_shared();
   __syncthreads();  // the tables have been read: the stages may be loaded
 
   float* part = reinterpret_cast<float*>(smem);  // [NT][256], after the last MMA has read the stages
@@ -910,10 +992,10 @@ int configure(K kernel, int smem, std::atomic<int>* configured) {
 
 int a_map(CUtensorMap* m, const Fp8Gemm& d, int box_rows) {
   const cuuint64_t dims[2] = {(cuuint64_t)d.args.K, (cuuint64_t)d.args.a_rows};
-  const cuuint64_t strides[1] = {(cuuint64_t)d.lda};
+  const cuuint64_t strides[1] = {(cuuint64_t)d.args.lda};
   const cuuint32_t box[2] = {(cuuint32_t)BK, (cuuint32_t)box_rows};
   const cuuint32_t estr[2] = {1, 1};
-  return encode_tmap(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(d.A), dims, strides, box, estr,
+  return encode_tmap(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(d.args.A), dims, strides, box, estr,
                      CU_TENSOR_MAP_SWIZZLE_128B);
 }
 

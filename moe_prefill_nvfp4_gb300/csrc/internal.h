@@ -164,6 +164,8 @@ int fp8_quantize_blocks_launch(const void* w, int w_dtype, int64_t ld_w, int N, 
 
 // FP8 products (fp8_gemm.cu)
 struct Fp8GemmArgs {
+  const uint8_t* A;        // activation codes, rows lda bytes apart
+  int64_t lda;
   const float* sa;         // activation scales: (row, group) at row * sa_row + group * sa_grp
   int64_t sa_row, sa_grp;
   const float* sw;         // weight scales [e_count][nblk][ceil(K / 128)]
@@ -183,8 +185,6 @@ struct Fp8GemmArgs {
   float limit;
 };
 struct Fp8Gemm {
-  const uint8_t* A;
-  int64_t lda;
   const uint8_t* W;
   int64_t ldw, w_expert;
   Fp8GemmArgs args;
