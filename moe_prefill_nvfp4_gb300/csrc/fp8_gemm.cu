@@ -137,6 +137,10 @@ MOE_DEV void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
 MOE_DEV void cp_async4(uint32_t dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
+// One of the barrier's expected arrivals, made when this thread's copies so far have landed.
+MOE_DEV void cp_async_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
 MOE_DEV void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 // Waits until at most N of this thread's committed groups of copies are still on their way.
 template <int N>
@@ -288,11 +292,13 @@ MOE_DEV void store_rows(uint8_t* stg, const uint32_t (&w)[16], T* out, int64_t l
 // ------------------------------------------------------------------------------------------------
 // wide kernel
 
-template <int NB_>
+template <int NB_, bool GATHER_>
 struct WideCfg {
   static constexpr int NB = NB_;           // weight blocks of 128 per tile
+  static constexpr bool GATHER = GATHER_;  // token rows through gather ids
   static constexpr int BN = NB * 128;
-  static constexpr int THREADS = 384;      // warpgroup 0: producer, MMA, scales; 1 and 2: epilogue
+  // warpgroup 0: TMA, MMA, scales; 1 and 2: epilogue; 3: gathering
+  static constexpr int THREADS = GATHER ? 512 : 384;
   static constexpr int STAGE = BLK + NB * BLK;
   static constexpr int NS = NB == 2 ? 4 : 6;
   static constexpr int TMEM_COLS = 2 * BN;
@@ -310,18 +316,21 @@ struct WideCfg {
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
   static constexpr int BYTES = OFF_MISC + 16;
   static constexpr int SMEM = BYTES + 1024;
-  // registers: the launch has 384 x 168; 128 x 72 + 256 x 216 is the same number
-  static constexpr int REG_LOW = 72, REG_HIGH = 216;
-  static_assert(128 * REG_LOW + 256 * REG_HIGH <= THREADS * 168, "register split");
+  // registers: the launch has 384 x 168 or 512 x 128, the warpgroups share the same number
+  static constexpr int REG_LAUNCH = GATHER ? 128 : 168;
+  static constexpr int REG_LOW = NB == 1 ? REG_LAUNCH - 32 : GATHER ? 56 : 72;
+  static constexpr int REG_HIGH = NB == 1 ? REG_LAUNCH + (GATHER ? 32 : 16) : GATHER ? 200 : 216;
+  static_assert((THREADS - 256) * REG_LOW + 256 * REG_HIGH <= THREADS * REG_LAUNCH, "register split");
   static_assert(SMEM > 232448 / 2 && SMEM <= 232448, "one CTA per SM (it takes all of TMEM)");
 };
 
-// Warp roles: 0 (and 3, gathering) operand producers, 1 MMA issuer and TMEM owner, 2 the scales of each
+// Warp roles: 0 TMA producer, 1 MMA issuer and TMEM owner, 2 the scales of each
 // k block into shared memory (asynchronously and blocks ahead, across tiles too: epilogue threads that
-// loaded their own scales waited for L2 in every block), 4-11 epilogue (two warpgroups; warp w
+// loaded their own scales waited for L2 in every block), 4-11 epilogue, 12-15 gathered
+// token rows.  (Epilogue: two warpgroups; warp w
 // reads TMEM lanes 32 (w % 4).., warpgroup g the columns 64 g .. 64 g + 63 of each weight block, so
 // that in the gate/up form a thread holds a gate column and its up column).
-template <class C, bool GATHER>
+template <class C>
 __global__ void __launch_bounds__(C::THREADS, 1)
     wide_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap wmap,
                 const __grid_constant__ Fp8GemmArgs args) {
@@ -329,6 +338,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem);
   constexpr int NS = C::NS, NB = C::NB;
+  constexpr bool GATHER = C::GATHER;
   int* s_offs = reinterpret_cast<int*>(smem + C::OFF_OFFS);
   int* s_tbase = reinterpret_cast<int*>(smem + C::OFF_TBASE);
   const uint32_t bar0 = sbase + C::OFF_BAR;
@@ -347,7 +357,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
 
   if (tid == 0) {
     for (int s = 0; s < NS; ++s) {
-      mbar_init(full(s), GATHER ? 3 : 1);  // TMA, the two gathering warps
+      mbar_init(full(s), GATHER ? 1 + 128 : 1);  // TMA; every gathering thread
       mbar_init(empty(s), 1);
     }
     for (int d = 0; d < 2; ++d) {
@@ -384,71 +394,32 @@ __global__ void __launch_bounds__(C::THREADS, 1)
 
   if (warp < 4) {
     reg_dec<C::REG_LOW>();
-    if (warp == 0 || (GATHER && warp == 3)) {
-      // ---------------------------------------------------------------- operand producers
-      // TMA (one lane of warp 0): the weight blocks, and the token rows where they are contiguous.
-      // Gathered token rows: warps 0 and 3 copy 64 rows each with 16-byte cp.async into the swizzled
-      // layout (chunk c of row r at c ^ (r % 8)), 4 rows to an instruction; rows past the tile's are
-      // left as they are (their accumulator rows are not stored).
-      if (warp == 0 && lane == 0) {
+    if (warp == 0) {
+      // ---------------------------------------------------------------- TMA producer
+      if (lane == 0) {
         prefetch_tmap(&amap);
         prefetch_tmap(&wmap);
-      }
-      const int r0 = (warp ? 64 : 0) + (lane >> 3);  // this lane's first row, then every fourth
-      const int chunk = lane & 7;
-      auto hand_over = [&](uint32_t bar) {
-        fence_proxy_async_shared();  // written by the generic proxy, read by the MMA
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar);
-      };
-      int i = 0;
-      bool ok = true;
-      for (int g = blockIdx.x; ok && g < total; g += gridDim.x) {
-        const Tile t = decode_tile(g, args, s_offs, s_tbase, 128, NG);
-        int src[16];
-        if (GATHER) {
-#pragma unroll
-          for (int j = 0; j < 16; ++j) src[j] = r0 + 4 * j < t.cnt ? source_row(args, t.p0 + r0 + 4 * j) : -1;
-        }
-        for (int kb = 0; kb < KB; ++kb, ++i) {
-          const int s = i % NS;
-          if (!warp_wait(empty(s), ((i / NS) & 1) ^ 1, s_abort, err, limit)) {
-            ok = false;
-            break;
-          }
-          const uint32_t st = sbase + s * C::STAGE;
-          if (warp == 0 && lane == 0) {
+        int i = 0;
+        bool ok = true;
+        for (int g = blockIdx.x; ok && g < total; g += gridDim.x) {
+          const Tile t = decode_tile(g, args, s_offs, s_tbase, 128, NG);
+          for (int kb = 0; kb < KB; ++kb, ++i) {
+            const int s = i % NS;
+            if (!wait_bounded(empty(s), ((i / NS) & 1) ^ 1, s_abort, err, limit)) {
+              ok = false;
+              break;
+            }
+            const uint32_t st = sbase + s * C::STAGE;
             mbar_arrive_expect_tx(full(s), (GATHER ? 0 : BLK) + NB * BLK);
             if (!GATHER) tma_load_2d(st, &amap, kb * BK, t.p0, full(s));
 #pragma unroll
             for (int h = 0; h < NB; ++h)
               tma_load_3d(st + BLK + h * BLK, &wmap, kb * BK, block_row<NB>(args, t.ng, h), t.e, full(s));
           }
-          if (GATHER) {
-            __syncwarp();
-            const int k = kb * BK + chunk * 16;
-            const uint32_t bytes = (uint32_t)max(0, min(16, args.K - k));
-            const uint8_t* col = args.A + (bytes ? k : 0);
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              const int r = r0 + 4 * j;
-              if (src[j] >= 0)
-                cp_async16(st + r * BK + ((chunk ^ (r & 7)) << 4), col + src[j] * args.lda, bytes);
-            }
-            cp_async_commit();
-            if (i > 0) {  // the stage before has landed
-              cp_async_wait<1>();
-              hand_over(full((i - 1) % NS));
-            }
-          }
         }
+        if (!ok)  // every copy issued lands before the CTA leaves
+          for (int j = max(0, i - NS); j < i; ++j) mbar_wait_drain(full(j % NS), (j / NS) & 1);
       }
-      if (GATHER) {
-        cp_async_wait<0>();
-        if (ok && i > 0) hand_over(full((i - 1) % NS));
-      }
-      if (!ok && warp == 0 && lane == 0)  // every copy issued lands before the CTA leaves
-        for (int j = max(0, i - NS); j < i; ++j) mbar_wait_drain(full(j % NS), (j / NS) & 1);
     } else if (warp == 1) {
       // ---------------------------------------------------------------- MMA issuer
       constexpr uint32_t idesc = make_idesc_e4m3(128, C::BN);
@@ -463,6 +434,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             break;
           }
           tc_fence_after();
+          if (GATHER) fence_proxy_async_shared();  // the gathered rows came through the generic proxy
           const uint32_t st = sbase + s * C::STAGE;
           if (elect_one()) {
             mma4_e4m3_ss(tmem_base + (uint32_t)(db * C::BN), make_sdesc_sw128(st), make_sdesc_sw128(st + BLK), idesc);
@@ -523,6 +495,44 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       }
       cp_async_wait<0>();
     }
+  } else if (GATHER && warp >= 12) {
+    // ------------------------------------------------------------------ gathered token rows
+    // 16-byte cp.async into the swizzled layout (chunk c of row r at c ^ (r % 8)): 8 lanes to a row of
+    // the k block, 4 rows to an instruction, every fourth group of 4 rows to a warp.  (TMA gather4
+    // moved ~12 bytes per cycle and SM where a tile takes ~20.)  Rows past the tile's repeat its last.
+    reg_dec<C::REG_LOW>();
+    const int r0 = (warp - 12) * 4 + (lane >> 3);  // rows r0 + 16 j: the same chunk place in all of them
+    const int chunk = lane & 7;
+    const uint32_t dst = sbase + (uint32_t)(r0 * BK + ((chunk ^ (r0 & 7)) << 4));
+    int i = 0;
+    bool ok = true;
+    for (int g = blockIdx.x; ok && g < total; g += gridDim.x) {
+      const Tile t = decode_tile(g, args, s_offs, s_tbase, 128, NG);
+      const uint8_t* src[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        src[j] = args.A + source_row(args, t.p0 + min(r0 + 16 * j, t.cnt - 1)) * args.lda + chunk * 16;
+      for (int kb = 0; kb < KB; ++kb, ++i) {
+        const int s = i % NS;
+        if (!warp_wait(empty(s), ((i / NS) & 1) ^ 1, s_abort, err, limit)) {
+          ok = false;
+          break;
+        }
+        const int left = args.K - kb * BK - chunk * 16;
+        if (left >= 16) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) cp_async16(dst + s * C::STAGE + j * 16 * BK, src[j], 16);
+        } else {  // past K: zeros (an address inside the row, of which nothing or the rest is read)
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            cp_async16(dst + s * C::STAGE + j * 16 * BK, left > 0 ? src[j] : args.A, (uint32_t)max(left, 0));
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) src[j] += BK;
+        cp_async_arrive(full(s));
+      }
+    }
+    cp_async_wait<0>();
   } else {
     // ------------------------------------------------------------------ epilogue
     reg_inc<C::REG_HIGH>();
@@ -1008,16 +1018,16 @@ int w_map(CUtensorMap* m, const Fp8Gemm& d) {
                      CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-template <class C, bool GATHER>
+template <class C>
 int launch_wide(const Fp8Gemm& d, int64_t tiles, cudaStream_t st) {
   CUtensorMap am, wm;
-  int rc = a_map(&am, d, GATHER ? 1 : 128);
+  int rc = a_map(&am, d, 128);
   if (rc == MOE_OK) rc = w_map(&wm, d);
   if (rc != MOE_OK) return rc;
   static std::atomic<int> configured[64];
-  if ((rc = configure(wide_kernel<C, GATHER>, C::SMEM, configured)) != MOE_OK) return rc;
+  if ((rc = configure(wide_kernel<C>, C::SMEM, configured)) != MOE_OK) return rc;
   const int grid = (int)std::min<int64_t>(tiles, device_sm_count());
-  return launch_pdl(wide_kernel<C, GATHER>, dim3(grid), dim3(C::THREADS), C::SMEM, st, am, wm, d.args);
+  return launch_pdl(wide_kernel<C>, dim3(grid), dim3(C::THREADS), C::SMEM, st, am, wm, d.args);
 }
 
 template <class C, bool GATHER>
@@ -1054,8 +1064,8 @@ int launch(const Fp8Gemm& d, cudaStream_t st) {
   if (rows <= 40) return launch_few<FewCfg<32, 3, 2>, GATHER>(d, token_tiles(d, 32) * ng2, st);
   const int64_t tt = token_tiles(d, 128);
   if (!a.half && tt * ng2 < device_sm_count())
-    return launch_wide<WideCfg<1>, GATHER>(d, tt * ((a.N + 127) / 128), st);
-  return launch_wide<WideCfg<2>, GATHER>(d, tt * ng2, st);
+    return launch_wide<WideCfg<1, GATHER>>(d, tt * ((a.N + 127) / 128), st);
+  return launch_wide<WideCfg<2, GATHER>>(d, tt * ng2, st);
 }
 
 }  // namespace f8
