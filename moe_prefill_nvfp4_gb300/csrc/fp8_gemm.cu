@@ -428,18 +428,23 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       for (int g = blockIdx.x; ok && g < total; g += gridDim.x) {
         for (int kb = 0; kb < KB; ++kb, ++i) {
           const int s = i % NS, db = i & 1;
-          if (!warp_wait(d_empty(db), ((i >> 1) & 1) ^ 1, s_abort, err, limit) ||
-              !warp_wait(full(s), (i / NS) & 1, s_abort, err, limit)) {
+          // (the operands are usually there first: the accumulator's release is what an MMA waits for)
+          if (!warp_wait(full(s), (i / NS) & 1, s_abort, err, limit)) {
+            ok = false;
+            break;
+          }
+          if (GATHER) fence_proxy_async_shared();  // the gathered rows came through the generic proxy
+          const uint32_t st = sbase + s * C::STAGE;
+          const uint64_t a_desc = make_sdesc_sw128(st), b_desc = make_sdesc_sw128(st + BLK);
+          if (!warp_wait(d_empty(db), ((i >> 1) & 1) ^ 1, s_abort, err, limit)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          if (GATHER) fence_proxy_async_shared();  // the gathered rows came through the generic proxy
-          const uint32_t st = sbase + s * C::STAGE;
           if (elect_one()) {
-            mma4_e4m3_ss(tmem_base + (uint32_t)(db * C::BN), make_sdesc_sw128(st), make_sdesc_sw128(st + BLK), idesc);
-            mma_commit(empty(s));
+            mma4_e4m3_ss(tmem_base + (uint32_t)(db * C::BN), a_desc, b_desc, idesc);
             mma_commit(d_full(db));
+            mma_commit(empty(s));
           }
           __syncwarp();
         }
@@ -560,13 +565,6 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         }
         tc_fence_after();
         const uint32_t base = lane_base + (uint32_t)(db * C::BN);
-        uint64_t f[NB];
-#pragma unroll
-        for (int h = 0; h < NB; ++h) {
-          const float* slot = s_f + (i % C::NF) * C::F_SLOT;
-          const float v = slot[row] * slot[128 + h];
-          f[h] = pack_f32x2(v, v);
-        }
         // 16 columns at a time through two register buffers (column j of this warp's 64 NB is column
         // j % 64 of block j / 64); the accumulator is given back once its last columns are in registers
         uint32_t v[2][16];
@@ -575,6 +573,13 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         };
         load(0);
         load(1);
+        uint64_t f[NB];
+#pragma unroll
+        for (int h = 0; h < NB; ++h) {
+          const float* slot = s_f + (i % C::NF) * C::F_SLOT;
+          const float v = slot[row] * slot[128 + h];
+          f[h] = pack_f32x2(v, v);
+        }
 #pragma unroll
         for (int c = 0; c < 4 * NB; c += 2) {
           tmem_wait_ld_regs(v[0]);
