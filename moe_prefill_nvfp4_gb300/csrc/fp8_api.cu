@@ -64,7 +64,7 @@ int product(const moe_fp8_rows* A, const int32_t* gather_ids, const moe_fp8_weig
   int rc = check(A, W, R, E);
   if (rc != MOE_OK) return rc;
   if (C == nullptr || !dtype_ok(c_dtype)) return MOE_ERR_INVALID_ARG;
-  if (ldc < W->N || ldc % 8 != 0) return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (ldc < W->N || ldc % 8 != 0 || ldc >= (1ll << 38)) return MOE_ERR_UNSUPPORTED_SHAPE;
   if (!aligned(C, 16)) return MOE_ERR_INVALID_ARG;
   if (gather_ids == nullptr && A->rows < R) return MOE_ERR_UNSUPPORTED_SHAPE;
   if ((rc = ensure_device()) != MOE_OK || R == 0) return rc;

@@ -259,50 +259,67 @@ MOE_DEV void zero_absent(const Fp8GemmArgs& a, const int* s_offs, int64_t tid, i
   }
 }
 
-// Stores 64 bytes of each of the warp's 32 rows (w: this lane's row, columns n0 .. of T) through the
-// warp's staging rows: 16-byte chunk c of row r lies at c ^ ((r >> 1) & 3), free of bank conflicts both
-// ways, and leaves in 16-byte stores with 4 lanes to a row.  Rows from nrow and columns from N on are
-// left out; `out` is row 0, column 0.
+// 128 bytes of each of the warp's 32 rows into its staging box (w[8 c ..]: chunks of 16 bytes, chunk c of
+// row r at c ^ (r % 8), the 128-byte swizzle of the store's tensor map; free of bank conflicts).
+MOE_DEV void stage_row(uint32_t box, int lane, const uint32_t (&w)[32]) {
+#pragma unroll
+  for (int c = 0; c < 8; ++c)
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(box + lane * 128 + ((c ^ (lane & 7)) << 4)),
+                 "r"(w[4 * c]), "r"(w[4 * c + 1]), "r"(w[4 * c + 2]), "r"(w[4 * c + 3])
+                 : "memory");
+}
+
+// Stores a staged box at row `row`, column `col` of the output: asynchronously (columns past N are
+// clipped, in pieces of 16 bytes), or, where the tile's rows end inside the box or N inside a piece, with
+// plain stores of the rows below nrow.
 template <typename T>
-MOE_DEV void store_rows(uint8_t* stg, const uint32_t (&w)[16], T* out, int64_t ld, int nrow, int n0, int N) {
+MOE_DEV void store_box(uint32_t box, const uint8_t* box_ptr, const CUtensorMap* cmap, T* C, int64_t ldc, int64_t row,
+                       int col, int nrow, int N) {
   constexpr int PER = 16 / sizeof(T);
   const int lane = lane_id();
-#pragma unroll
-  for (int c = 0; c < 4; ++c)
-    *reinterpret_cast<uint4*>(stg + lane * 64 + ((c ^ ((lane >> 1) & 3)) * 16)) =
-        make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
-  __syncwarp();
-  const int c = lane & 3, col = n0 + c * PER;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = i * 8 + (lane >> 2);
-    if (r < nrow && col < N) {
-      const T* src = reinterpret_cast<const T*>(stg + r * 64 + ((c ^ ((r >> 1) & 3)) * 16));
-      T* dst = out + r * ld + col;
-      if (col + PER <= N) {
-        *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<const uint4*>(src);
-      } else {
-        for (int j = 0; col + j < N; ++j) dst[j] = src[j];
-      }
+  if (col >= N) return;
+  if (nrow >= 32 && (col + 8 * PER <= N || N % PER == 0)) {
+    if (lane == 0)
+      asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(cmap), "r"(col),
+                   "r"((int)row), "r"(box)
+                   : "memory");
+    return;
+  }
+  const int c = lane & 7, n = col + c * PER;
+  for (int r = lane >> 3; r < nrow; r += 4) {
+    const T* src = reinterpret_cast<const T*>(box_ptr + r * 128 + ((c ^ (r & 7)) << 4));
+    T* dst = C + (row + r) * ldc + n;
+    if (n + PER <= N) {
+      *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<const uint4*>(src);
+    } else {
+      for (int j = 0; n + j < N; ++j) dst[j] = src[j];
     }
   }
-  __syncwarp();
 }
+
+MOE_DEV void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+// Waits until this thread's bulk stores have read shared memory / are complete.
+MOE_DEV void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+MOE_DEV void bulk_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
 // ------------------------------------------------------------------------------------------------
 // wide kernel
 
-template <int NB_, bool GATHER_>
+template <int NB_, bool GATHER_, bool GATE_UP_>
 struct WideCfg {
   static constexpr int NB = NB_;           // weight blocks of 128 per tile
+  static constexpr bool GATE_UP = GATE_UP_;
   static constexpr bool GATHER = GATHER_;  // token rows through gather ids
   static constexpr int BN = NB * 128;
   // warpgroup 0: TMA, MMA, scales; 1 and 2: epilogue; 3: gathering
   static constexpr int THREADS = GATHER ? 512 : 384;
   static constexpr int STAGE = BLK + NB * BLK;
-  static constexpr int NS = NB == 2 ? 4 : 6;
+  // The plain form stages its whole BF16 tile (the FP32 tile in two parts) for asynchronous stores and
+  // has a stage less for it: stores from the epilogue warps held up the next tile for 1.4 us of the
+  // 7.3 us that a tile of K = 1536 took, the fourth stage is worth 1-2%.
+  static constexpr int NS = NB == 1 ? 5 : GATE_UP ? 4 : 3;
   static constexpr int TMEM_COLS = 2 * BN;
-  static constexpr int EPI_WARP = 32 * 64;  // 32 rows x 64 bytes
+  static constexpr int EPI_WARP = GATE_UP ? 0 : NB * 4096;     // NB boxes of 32 rows x 128 bytes
   static constexpr int OFF_EPI = NS * STAGE;
   static constexpr int OFF_AMAX = OFF_EPI + 8 * EPI_WARP;      // uint32 [2][128]
   static constexpr int NF = 4;              // k blocks whose scales are held
@@ -333,7 +350,7 @@ struct WideCfg {
 template <class C>
 __global__ void __launch_bounds__(C::THREADS, 1)
     wide_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap wmap,
-                const __grid_constant__ Fp8GemmArgs args) {
+                const __grid_constant__ CUtensorMap cmap, const __grid_constant__ Fp8GemmArgs args) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem);
@@ -374,7 +391,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   }
   griddep_wait();
   griddep_launch_dependents();
-  const int NG = args.half ? args.half / 128 : (args.N + C::BN - 1) / C::BN;
+  const int NG = C::GATE_UP ? args.half / 128 : (args.N + C::BN - 1) / C::BN;
   if (args.offsets == nullptr) {  // dense: one group of R rows
     if (tid == 0) {
       s_offs[0] = 0;
@@ -543,7 +560,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     reg_inc<C::REG_HIGH>();
     const int wg = (warp - 4) >> 2;
     const int q = warp & 3;
-    uint8_t* stg = smem + C::OFF_EPI + (warp - 4) * C::EPI_WARP;
+    const uint32_t stg = sbase + C::OFF_EPI + (warp - 4) * C::EPI_WARP;
     uint32_t* s_amax = reinterpret_cast<uint32_t*>(smem + C::OFF_AMAX);
     const uint32_t lane_base = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(wg * 64);
     const int row = q * 32 + lane;  // of the tile
@@ -597,14 +614,13 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           }
         }
       }
-      const bool gate_up = NB == 2 && args.half != 0;
       // (the gate/up form's warps exchange maxima below: all of them leave the loop at the same tile)
-      if (gate_up ? named_bar_any(1, 256, !ok) : !ok) {
+      if (C::GATE_UP ? named_bar_any(1, 256, !ok) : !ok) {
         ok = false;
         break;
       }
-      const bool live = row < t.cnt;
-      if (gate_up) {
+      if constexpr (C::GATE_UP) {
+        const bool live = row < t.cnt;
         // gate (block 0) and up (block 1) columns 64 wg .. of the act group
         uint32_t m = 0;
 #pragma unroll
@@ -638,38 +654,58 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         if (live && wg == 0) args.s[(int64_t)(t.p0 + row) * args.s_row + t.ng * args.s_grp] = scale;
       } else {
         const int nrow = min(32, t.cnt - q * 32);
-        const int64_t p0 = t.p0 + q * 32;
+        const int64_t row0 = t.p0 + q * 32;
+        const uint8_t* stg_ptr = smem + (stg - sbase);
+        uint32_t w[32];
+        if (args.c_dtype == MOE_DTYPE_BF16) {
+          if (lane == 0) bulk_wait_read();  // the last tile's boxes have left
+          __syncwarp();
 #pragma unroll
-        for (int h = 0; h < NB; ++h) {
-          const int n0 = block_row<NB>(args, t.ng, h) + wg * 64;
-          uint32_t w[16];
-          if (args.c_dtype == MOE_DTYPE_F32) {
+          for (int h = 0; h < NB; ++h) {
 #pragma unroll
-            for (int ps = 0; ps < 4; ++ps) {
-#pragma unroll
-              for (int j = 0; j < 8; ++j) {
-                float a0, a1;
-                unpack_f32x2(acc[h][ps * 8 + j], a0, a1);
-                w[2 * j] = __float_as_uint(a0);
-                w[2 * j + 1] = __float_as_uint(a1);
-              }
-              store_rows(stg, w, static_cast<uint32_t*>(args.C) + p0 * args.ldc, args.ldc, nrow, n0 + ps * 16, args.N);
+            for (int j = 0; j < 32; ++j) {
+              float a0, a1;
+              unpack_f32x2(acc[h][j], a0, a1);
+              w[j] = pack_bf16x2(a0, a1);
             }
-          } else {
+            stage_row(stg + h * 4096, lane, w);
+          }
+          fence_proxy_async_shared();
+          __syncwarp();
 #pragma unroll
-            for (int ps = 0; ps < 2; ++ps) {
+          for (int h = 0; h < NB; ++h)
+            store_box(stg + h * 4096, stg_ptr + h * 4096, &cmap, static_cast<uint16_t*>(args.C), args.ldc, row0,
+                      block_row<NB>(args, t.ng, h) + wg * 64, nrow, args.N);
+          if (lane == 0) bulk_commit();
+          __syncwarp();
+        } else {
+          // a box holds 32 columns: NB boxes at a time
 #pragma unroll
-              for (int j = 0; j < 16; ++j) {
-                float a0, a1;
-                unpack_f32x2(acc[h][ps * 16 + j], a0, a1);
-                w[j] = pack_bf16x2(a0, a1);
-              }
-              store_rows(stg, w, static_cast<uint16_t*>(args.C) + p0 * args.ldc, args.ldc, nrow, n0 + ps * 32, args.N);
+          for (int u = 0; u < 2 * NB; ++u) {  // columns 32 (u % 2).. of block u / 2
+            if (u % NB == 0) {
+              if (lane == 0) bulk_wait_read();
+              __syncwarp();
             }
+            const uint32_t box = (uint32_t)(u % NB) * 4096;
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              float a0, a1;
+              unpack_f32x2(acc[u >> 1][(u & 1) * 16 + j], a0, a1);
+              w[2 * j] = __float_as_uint(a0);
+              w[2 * j + 1] = __float_as_uint(a1);
+            }
+            stage_row(stg + box, lane, w);
+            fence_proxy_async_shared();
+            __syncwarp();
+            store_box(stg + box, stg_ptr + box, &cmap, static_cast<float*>(args.C), args.ldc, row0,
+                      block_row<NB>(args, t.ng, u >> 1) + wg * 64 + (u & 1) * 32, nrow, args.N);
+            if (lane == 0) bulk_commit();
+            __syncwarp();
           }
         }
       }
     }
+    if (!C::GATE_UP && lane == 0) bulk_wait();
   }
 
   tc_fence_before();
@@ -1023,16 +1059,29 @@ int w_map(CUtensorMap* m, const Fp8Gemm& d) {
                      CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
+// stores of 32-row boxes, 128 bytes wide
+int c_map(CUtensorMap* m, const Fp8Gemm& d) {
+  const Fp8GemmArgs& a = d.args;
+  const bool bf16 = a.c_dtype == MOE_DTYPE_BF16;
+  const cuuint64_t dims[2] = {(cuuint64_t)a.N, (cuuint64_t)a.R};
+  const cuuint64_t strides[1] = {(cuuint64_t)a.ldc * (bf16 ? 2 : 4)};
+  const cuuint32_t box[2] = {bf16 ? 64u : 32u, 32};
+  const cuuint32_t estr[2] = {1, 1};
+  return encode_tmap(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, a.C, dims,
+                     strides, box, estr, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
 template <class C>
 int launch_wide(const Fp8Gemm& d, int64_t tiles, cudaStream_t st) {
-  CUtensorMap am, wm;
+  CUtensorMap am, wm, cm = {};
   int rc = a_map(&am, d, 128);
   if (rc == MOE_OK) rc = w_map(&wm, d);
+  if (rc == MOE_OK && !C::GATE_UP) rc = c_map(&cm, d);
   if (rc != MOE_OK) return rc;
   static std::atomic<int> configured[64];
   if ((rc = configure(wide_kernel<C>, C::SMEM, configured)) != MOE_OK) return rc;
   const int grid = (int)std::min<int64_t>(tiles, device_sm_count());
-  return launch_pdl(wide_kernel<C>, dim3(grid), dim3(C::THREADS), C::SMEM, st, am, wm, d.args);
+  return launch_pdl(wide_kernel<C>, dim3(grid), dim3(C::THREADS), C::SMEM, st, am, wm, cm, d.args);
 }
 
 template <class C, bool GATHER>
@@ -1068,9 +1117,9 @@ int launch(const Fp8Gemm& d, cudaStream_t st) {
   if (rows <= 12) return launch_few<FewCfg<16, 3, 2>, GATHER>(d, token_tiles(d, 16) * ng2, st);
   if (rows <= 40) return launch_few<FewCfg<32, 3, 2>, GATHER>(d, token_tiles(d, 32) * ng2, st);
   const int64_t tt = token_tiles(d, 128);
-  if (!a.half && tt * ng2 < device_sm_count())
-    return launch_wide<WideCfg<1, GATHER>>(d, tt * ((a.N + 127) / 128), st);
-  return launch_wide<WideCfg<2, GATHER>>(d, tt * ng2, st);
+  if (a.half) return launch_wide<WideCfg<2, GATHER, true>>(d, tt * ng2, st);
+  if (tt * ng2 < device_sm_count()) return launch_wide<WideCfg<1, GATHER, false>>(d, tt * ((a.N + 127) / 128), st);
+  return launch_wide<WideCfg<2, GATHER, false>>(d, tt * ng2, st);
 }
 
 }  // namespace f8
