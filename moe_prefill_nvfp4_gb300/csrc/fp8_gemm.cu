@@ -1084,6 +1084,31 @@ int launch_wide(const Fp8Gemm& d, int64_t tiles, cudaStream_t st) {
   return launch_pdl(wide_kernel<C>, dim3(grid), dim3(C::THREADS), C::SMEM, st, am, wm, cm, d.args);
 }
 
+// Clusters of S CTAs of this kernel that the device holds at once (they do not cross its groups of SMs, so
+// fewer than the CTAs would suggest), asked once for each S.
+template <class C, bool GATHER>
+int resident_clusters(int S) {
+  static std::atomic<int> known[64][9];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  int n = known[dev][S].load(std::memory_order_relaxed);
+  if (n > 0) return n;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = S;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.gridDim = dim3(S);
+  cfg.blockDim = dim3(C::THREADS);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaOccupancyMaxActiveClusters(&n, few_kernel<C, GATHER>, &cfg) != cudaSuccess) return 0;
+  known[dev][S].store(n, std::memory_order_relaxed);
+  return n;
+}
+
 template <class C, bool GATHER>
 int launch_few(const Fp8Gemm& d, int64_t tiles, cudaStream_t st) {
   CUtensorMap am, wm;
@@ -1092,11 +1117,13 @@ int launch_few(const Fp8Gemm& d, int64_t tiles, cudaStream_t st) {
   if (rc != MOE_OK) return rc;
   static std::atomic<int> configured[64];
   if ((rc = configure(few_kernel<C, GATHER>, C::SMEM, configured)) != MOE_OK) return rc;
-  // split k while the tiles leave CTA slots free and every CTA keeps two k blocks
-  const int slots = device_sm_count() * C::PER_SM;
+  // Split k as far as every CTA is still resident at once and keeps two k blocks: more CTAs than that
+  // queue for SMs, and each costs ~4 us of start and join (one token's gate/up at 160 experts, 96 tiles:
+  // 26.4 us with one CTA to a tile, 24.1 with three, 30.4 with four, which no longer fit).
   const int KB = (d.args.K + BK - 1) / BK;
   int S = 1;
-  while (S < 8 && tiles * 2 * S <= slots && KB >= 4 * S) S *= 2;
+  for (int t = 2; t <= 8 && 2 * t <= KB; ++t)
+    if (tiles <= resident_clusters<C, GATHER>(t)) S = t;
   return launch_pdl_cluster(few_kernel<C, GATHER>, dim3((unsigned)(tiles * S)), dim3(C::THREADS), C::SMEM, st, S, am,
                             wm, d.args);
 }
@@ -1114,9 +1141,12 @@ int launch(const Fp8Gemm& d, cudaStream_t st) {
   const int groups = a.offsets == nullptr ? 1 : std::min(a.E, a.R);
   const double rows = (double)a.R / groups;  // per expert
   const int64_t ng2 = a.half ? a.half / 128 : (a.N + 255) / 256;
-  if (rows <= 12) return launch_few<FewCfg<16, 3, 2>, GATHER>(d, token_tiles(d, 16) * ng2, st);
-  if (rows <= 40) return launch_few<FewCfg<32, 3, 2>, GATHER>(d, token_tiles(d, 32) * ng2, st);
   const int64_t tt = token_tiles(d, 128);
+  const int64_t wide_tiles = a.half ? tt * ng2 : tt * ((a.N + 127) / 128);
+  if (rows <= 8 || (rows <= 256 && 2 * wide_tiles <= device_sm_count())) {
+    if (rows <= 48) return launch_few<FewCfg<16, 3, 2>, GATHER>(d, token_tiles(d, 16) * ng2, st);
+    return launch_few<FewCfg<32, 3, 2>, GATHER>(d, token_tiles(d, 32) * ng2, st);
+  }
   if (a.half) return launch_wide<WideCfg<2, GATHER, true>>(d, tt * ng2, st);
   if (tt * ng2 < device_sm_count()) return launch_wide<WideCfg<1, GATHER, false>>(d, tt * ((a.N + 127) / 128), st);
   return launch_wide<WideCfg<2, GATHER, false>>(d, tt * ng2, st);
