@@ -9,6 +9,7 @@ library is missing the import of this module's functions fails loudly.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 import re
 from typing import Optional, Sequence
@@ -455,77 +456,28 @@ def moe_shared_expert_forward(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch
 # ------------------------------------------------------------------------------------------ FP8
 
 
-# These calls run once per projection of every token batch, where a call's own time on the host counts
-# (a single token's product takes a few microseconds on the GPU): each reads a tensor's shape and strides
-# once, allocates with one torch call per output and takes the current stream's handle without making a
-# Stream object.
+# Argument checks and marshalling of these calls are in C (csrc/fp8_call.c): they run once per projection
+# of every token batch, where a call's own time on the host counts.
 
-_F8 = torch.float8_e4m3fn
-_FP8_DT = {torch.bfloat16: MOE_DTYPE_BF16, torch.float32: MOE_DTYPE_F32}
-_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_FP8 = None
 
 
-def _raw_stream(stream, t: torch.Tensor) -> int:
-    if stream is not None:
-        return stream.cuda_stream
-    if _current_raw_stream is not None:
-        return _current_raw_stream(t.get_device())
-    return torch.cuda.current_stream(t.device).cuda_stream
-
-
-def _bad_codes(t, name: str):
-    raise ValueError(f"{name}: need a CUDA {_F8} tensor with unit column stride, got {t.dtype} {tuple(t.shape)} on "
-                     f"{t.device}, strides {tuple(t.stride())}")
-
-
-def _matrix(t: torch.Tensor, name: str):
-    """(rows, columns, row stride) of an E4M3 matrix; a single row's stride, which torch leaves
-    arbitrary, counts as whole 16-byte pieces."""
-    if t.dtype is not _F8 or not t.is_cuda or t.dim() != 2:
-        _bad_codes(t, name)
-    rows, cols = t.shape
-    ld, one = t.stride()
-    if one != 1 and cols != 1:
-        _bad_codes(t, name)
-    if rows <= 1:
-        ld = max(ld, -(-cols // 16) * 16)
-    return rows, cols, ld
-
-
-def _fp8_out(t, name: str, rows: int, cols: int, device):
-    """(codes [rows, cols], row stride): given, or new with rows whole 16-byte pieces apart."""
-    if t is None:
-        ld = -(-cols // 16) * 16
-        return torch.empty_strided((rows, cols), (ld, 1), dtype=_F8, device=device), ld
-    r, c, ld = _matrix(t, name)
-    if r != rows or c != cols:
-        raise ValueError(f"{name}: need [{rows}, {cols}], got {tuple(t.shape)}")
-    return t, ld
-
-
-def _fp8_scales_out(t, name: str, rows: int, groups: int, device):
-    """(scales [rows, groups], row stride, group stride): given, or new, stored group by group."""
-    if t is None:
-        return torch.empty_strided((rows, groups), (1, rows), dtype=torch.float32, device=device), 1, rows
-    return (t, *_fp8_scales_in(t, name, (rows, groups)))
-
-
-def _fp8_scales_in(t, name: str, shape):
-    if t.dtype is not torch.float32 or not t.is_cuda or t.shape != shape:
-        raise ValueError(f"{name}: need a CUDA FP32 tensor of shape {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
-    return t.stride()
-
-
-def _fp8_source(t: torch.Tensor, name: str):
-    """(element type, rows, columns, row stride) of a BF16 or FP32 matrix."""
-    dt = _FP8_DT.get(t.dtype)
-    if dt is None or not t.is_cuda or t.dim() != 2:
-        raise ValueError(f"{name}: need a CUDA BF16 or FP32 matrix, got {t.dtype} {tuple(t.shape)} on {t.device}")
-    rows, cols = t.shape
-    ld, one = t.stride()
-    if one != 1 and cols != 1:
-        raise ValueError(f"{name}: need unit column stride, got {tuple(t.stride())}")
-    return dt, rows, cols, ld if rows > 1 else max(ld, cols)
+def _fp8():
+    global _FP8
+    if _FP8 is None:
+        lib()
+        path = _build.call_path()
+        if not os.path.exists(path):
+            raise FileNotFoundError(f"call module not built: {path}")
+        spec = importlib.util.spec_from_file_location("_fp8_call", path)
+        m = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(m)
+        # the current stream's handle without making a Stream object, where torch offers it
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda index: torch.cuda.current_stream(index).cuda_stream)
+        m.init(MoeError, torch.empty_strided, torch.float8_e4m3fn, torch.bfloat16, torch.float32, torch.int32, raw)
+        _FP8 = m
+    return _FP8
 
 
 def moe_fp8_quantize_rows(x: torch.Tensor, out: Optional[torch.Tensor] = None, scales: Optional[torch.Tensor] = None,
@@ -533,97 +485,20 @@ def moe_fp8_quantize_rows(x: torch.Tensor, out: Optional[torch.Tensor] = None, s
     """Rows [R, K] (BF16 or FP32, any row stride) -> (E4M3 [R, K], FP32 [R, ceil(K/128)]): one scale
     for each 128 columns of a row.  New outputs have rows whole 16-byte pieces apart and scales stored
     group by group, the layouts the products read fastest."""
-    dt, R, K, ld_x = _fp8_source(x, "x")
-    device = x.device
-    out, ld = _fp8_out(out, "out", R, K, device)
-    scales, s_row, s_grp = _fp8_scales_out(scales, "scales", R, -(-K // 128), device)
-    if R:
-        rc = lib().moe_fp8_quantize_rows(x.data_ptr(), dt, ld_x, R, K, out.data_ptr(), ld, scales.data_ptr(), s_row,
-                                         s_grp, _raw_stream(stream, x))
-        if rc:
-            raise MoeError(rc, "moe_fp8_quantize_rows")
-    return out, scales
+    return (_FP8 or _fp8()).quantize(x, out, scales, stream, False)
 
 
 def moe_fp8_quantize_blocks(w: torch.Tensor, out: Optional[torch.Tensor] = None, scales: Optional[torch.Tensor] = None,
                             stream=None):
     """Weight [N, K] (BF16 or FP32, any row stride) -> (E4M3 [N, K], FP32 [ceil(N/128), ceil(K/128)]): one
     scale for each 128 x 128 block."""
-    dt, N, K, ld_w = _fp8_source(w, "w")
-    device = w.device
-    out, ld = _fp8_out(out, "out", N, K, device)
-    shape = (-(-N // 128), -(-K // 128))
-    if scales is None:
-        scales = torch.empty(shape, dtype=torch.float32, device=device)
-    else:
-        _need(scales, torch.float32, "scales")
-        _fp8_scales_in(scales, "scales", shape)
-    rc = lib().moe_fp8_quantize_blocks(w.data_ptr(), dt, ld_w, N, K, out.data_ptr(), ld, scales.data_ptr(),
-                                       _raw_stream(stream, w))
-    if rc:
-        raise MoeError(rc, "moe_fp8_quantize_blocks")
-    return out, scales
-
-
-def _fp8_operands(A, a_scales, W, w_scales, dims: int, first: int):
-    """C views of activation rows [rows, K] and of a weight [N, K] (dims 2) or [experts, N, K] (dims 3)."""
-    rows, K, lda = _matrix(A, "A")
-    shape = W.shape
-    if W.dtype is not _F8 or not W.is_cuda or len(shape) != dims:
-        _bad_codes(W, "W")
-    N, k = shape[-2:]
-    strides = W.stride()
-    if strides[-1] != 1 and k != 1:
-        _bad_codes(W, "W")
-    if k != K:
-        raise ValueError(f"A, W: {K} and {k} columns")
-    g = -(-K // 128)
-    s_row, s_grp = _fp8_scales_in(a_scales, "a_scales", (rows, g))
-    _fp8_scales_in(w_scales, "w_scales", (*shape[:-2], -(-N // 128), g))
-    if not w_scales.is_contiguous():
-        raise ValueError("w_scales: need a contiguous tensor")
-    ldw = strides[-2] if N > 1 else max(strides[-2], -(-K // 16) * 16)
-    count, expert = (shape[0], strides[0]) if dims == 3 else (1, 0)
-    return (Fp8Rows(A.data_ptr(), lda, a_scales.data_ptr(), s_row, s_grp, rows),
-            Fp8Weight(W.data_ptr(), ldw, expert, w_scales.data_ptr(), first, count, N, K), rows, N)
-
-
-def _fp8_product_out(t, R: int, N: int, c_dtype, device):
-    """(C [R, N], row stride, type code): given, or new with rows a multiple of 8 elements apart."""
-    code = _FP8_DT.get(c_dtype)
-    if code is None:
-        raise ValueError("c_dtype: torch.bfloat16 or torch.float32")
-    if t is None:
-        ld = -(-N // 8) * 8
-        return torch.empty_strided((R, N), (ld, 1), dtype=c_dtype, device=device), ld, code
-    if not t.is_cuda or t.dtype is not c_dtype or t.dim() != 2 or t.shape[0] < R or t.shape[1] != N or (
-            t.stride(1) != 1 and N != 1):
-        raise ValueError(f"out: need a CUDA {c_dtype} [{R}, {N}] tensor with unit column stride")
-    ld = t.stride(0)
-    return t, ld if t.shape[0] > 1 else max(ld, -(-N // 8) * 8), code
+    return (_FP8 or _fp8()).quantize(w, out, scales, stream, True)
 
 
 def moe_fp8_gemm(A: torch.Tensor, a_scales: torch.Tensor, W: torch.Tensor, w_scales: torch.Tensor,
                  out: Optional[torch.Tensor] = None, c_dtype: torch.dtype = torch.bfloat16, stream=None) -> torch.Tensor:
     """Quantised rows A [R, K] times a quantised weight W [N, K] transposed: BF16 or FP32 [R, N]."""
-    a, w, R, N = _fp8_operands(A, a_scales, W, w_scales, 2, 0)
-    out, ld, code = _fp8_product_out(out, R, N, c_dtype, A.device)
-    if R:
-        rc = lib().moe_fp8_gemm(ctypes.byref(a), ctypes.byref(w), out.data_ptr(), ld, code, _raw_stream(stream, A))
-        if rc:
-            raise MoeError(rc, "moe_fp8_gemm")
-    return out
-
-
-def _fp8_groups(expert_offsets, R: int, gather_ids):
-    """(E, gather_ids' address) of a grouped call."""
-    _need(expert_offsets, torch.int32, "expert_offsets")
-    if gather_ids is None:
-        return expert_offsets.numel() - 1, None
-    _need(gather_ids, torch.int32, "gather_ids")
-    if gather_ids.numel() < R:
-        raise ValueError(f"gather_ids: need {R} entries")
-    return expert_offsets.numel() - 1, gather_ids.data_ptr()
+    return (_FP8 or _fp8()).gemm(A, a_scales, W, w_scales, out, c_dtype, stream)
 
 
 def moe_fp8_grouped_gemm(A: torch.Tensor, a_scales: torch.Tensor, W: torch.Tensor, w_scales: torch.Tensor,
@@ -633,15 +508,7 @@ def moe_fp8_grouped_gemm(A: torch.Tensor, a_scales: torch.Tensor, W: torch.Tenso
     """Expert-sorted rows times their expert's weight, W [experts, N, K]: BF16 or FP32 [R, N].  Sorted row p
     is row ``gather_ids[p]`` of A (row p without).  W holds the experts from ``first`` on; the others' rows
     are zeros."""
-    a, w, _, N = _fp8_operands(A, a_scales, W, w_scales, 3, first)
-    E, gather = _fp8_groups(expert_offsets, R, gather_ids)
-    out, ld, code = _fp8_product_out(out, R, N, c_dtype, A.device)
-    if R:
-        rc = lib().moe_fp8_grouped_gemm(ctypes.byref(a), gather, ctypes.byref(w), expert_offsets.data_ptr(), E, R,
-                                        out.data_ptr(), ld, code, _raw_stream(stream, A))
-        if rc:
-            raise MoeError(rc, "moe_fp8_grouped_gemm")
-    return out
+    return (_FP8 or _fp8()).grouped(A, a_scales, W, w_scales, expert_offsets, R, gather_ids, first, out, c_dtype, stream)
 
 
 def moe_fp8_grouped_gemm_swiglu(A: torch.Tensor, a_scales: torch.Tensor, W: torch.Tensor, w_scales: torch.Tensor,
@@ -650,19 +517,8 @@ def moe_fp8_grouped_gemm_swiglu(A: torch.Tensor, a_scales: torch.Tensor, W: torc
                                 out: Optional[torch.Tensor] = None, scales: Optional[torch.Tensor] = None, stream=None):
     """Gate/up product over W [experts, 2I, K], clamped SwiGLU, and the row quantiser on its result:
     (E4M3 [R, I], FP32 [R, I/128]), the operands of the down product."""
-    a, w, _, N = _fp8_operands(A, a_scales, W, w_scales, 3, first)
-    E, gather = _fp8_groups(expert_offsets, R, gather_ids)
-    inter = N // 2
-    device = A.device
-    out, ld = _fp8_out(out, "out", R, inter, device)
-    scales, s_row, s_grp = _fp8_scales_out(scales, "scales", R, -(-inter // 128), device)
-    if R:
-        rc = lib().moe_fp8_grouped_gemm_swiglu(ctypes.byref(a), gather, ctypes.byref(w), expert_offsets.data_ptr(), E, R,
-                                               limit, out.data_ptr(), ld, scales.data_ptr(), s_row, s_grp,
-                                               _raw_stream(stream, A))
-        if rc:
-            raise MoeError(rc, "moe_fp8_grouped_gemm_swiglu")
-    return out, scales
+    return (_FP8 or _fp8()).grouped_swiglu(A, a_scales, W, w_scales, expert_offsets, R, limit, gather_ids, first, out,
+                                           scales, stream)
 
 
 def moe_get_device_error(stream=None) -> int:

@@ -4,7 +4,8 @@ Each ``csrc/*.cu`` file is compiled in parallel (``-gencode arch=compute_103a,co
 then linked into one shared library against the shared CUDA runtime (the same libcudart that
 PyTorch loads, so streams and the primary context are shared) and nothing else: every product,
 the shared expert's dense ones included, runs in this library's own kernels.  No cmake, no torch extension machinery: the library exports a plain C ABI
-(``include/moe_prefill.h``).
+(``include/moe_prefill.h``).  ``csrc/fp8_call.c``, the FP8 calls' argument marshalling, becomes the
+extension module ``lib/_fp8_call.so`` beside it (the host compiler and Python's own headers, no others).
 """
 
 from __future__ import annotations
@@ -14,6 +15,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -38,16 +40,19 @@ def lib_path() -> str:
     return os.path.join(LIBDIR, LIBNAME)
 
 
+def call_path() -> str:
+    return os.path.join(LIBDIR, "_fp8_call.so")
+
+
 def _newest_input() -> float:
-    files = sources() + [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))]
+    files = sources() + [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h", ".c"))]
     files.append(os.path.join(ROOT, "include", "moe_prefill.h"))
     files.append(os.path.abspath(__file__))
     return max(os.path.getmtime(f) for f in files)
 
 
 def up_to_date() -> bool:
-    p = lib_path()
-    return os.path.exists(p) and os.path.getmtime(p) >= _newest_input()
+    return all(os.path.exists(p) and os.path.getmtime(p) >= _newest_input() for p in (lib_path(), call_path()))
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = False) -> str:
@@ -84,6 +89,14 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stderr}")
     os.replace(tmp, lib_path())
+    tmp = call_path() + ".tmp"
+    cmd = [os.environ.get("CC", "gcc"), "-O2", "-fPIC", "-shared", "-I", sysconfig.get_paths()["include"], "-I",
+           os.path.join(ROOT, "include"), os.path.join(CSRC, "fp8_call.c"), "-o", tmp, "-L", LIBDIR,
+           "-l:" + LIBNAME, "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"building the call module failed:\n{r.stderr}")
+    os.replace(tmp, call_path())
     return lib_path()
 
 
