@@ -99,6 +99,12 @@ MOE_DEV void fma_f32x2(uint64_t& acc, uint32_t v0, uint32_t v1, uint64_t f) {
   asm("{\n .reg .b64 d;\n mov.b64 d, {%1, %2};\n fma.rn.f32x2 %0, d, %3, %0;\n}" : "+l"(acc) : "r"(v0), "r"(v1), "l"(f));
 }
 
+MOE_DEV uint64_t mul_f32x2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
 template <uint32_t N>
 MOE_DEV void reg_inc() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
@@ -718,31 +724,45 @@ __global__ void __launch_bounds__(C::THREADS, 1)
 
 // ------------------------------------------------------------------------------------------------
 // few-row kernel
+//
+// Bound by the weights it streams.  Persistent, with loads under way across tiles.  One SM draws 77 GB/s
+// from DRAM at most (44.7 is its share when all of them do), so it pays to have every tile's CTA resident
+// at once: two CTAs to an SM where their stages fit, k split over a cluster where tiles are few.
 
 template <int NT_, int NS_, int PER_SM_>
 struct FewCfg {
   static constexpr int NT = NT_;            // token rows per tile
   static constexpr int NS = NS_;
   static constexpr int PER_SM = PER_SM_;    // CTAs per SM
-  static constexpr int THREADS = 192;
+  static constexpr int THREADS = 224;
   static constexpr int STAGE = 2 * BLK + NT * BK;
-  static constexpr int TMEM_COLS = 4 * NT;  // two buffers x two blocks
-  static constexpr int PART = NT * 256 * 4; // partial sums [NT][256], over the drained stages
-  static constexpr int OFF_SCALE = NS * STAGE;                      // float [4 warps][2][2][NT]
-  static constexpr int OFF_AMAX = OFF_SCALE + 4 * 4 * NT * 4;       // uint32 [NT][4]
-  static constexpr int OFF_BAR = OFF_AMAX + NT * 4 * 4;
-  static constexpr int OFF_OFFS = 0;  // the tile tables, over the stages (read before the first load)
-  static constexpr int OFF_TBASE = (MAX_E + 1) * 4;
-  static constexpr int NBAR = 2 * NS + 5;
+  // accumulators: a k block of a tile is little work for the MMA and the epilogue, most of its way through
+  // both is latency, which eight on their way hide (with two, one SM could draw 77 GB/s of the 140 or so)
+  static constexpr int ND = 8;
+  static constexpr int TMEM_COLS = ND * 2 * NT;
+  static constexpr int PART = NT * 256 * 4;  // a tile's partial sums [NT][256] of a cluster, over the drained stages
+  static constexpr int AHEAD = 4;           // k blocks that the copies of scales run ahead
+  static constexpr int NF = 16;             // k blocks whose scales are held, at least ND + AHEAD
+  static constexpr int F_SLOT = NT + 4;     // sa of the rows, then sw of the two blocks
+  static constexpr int OFF_F = NS * STAGE;                   // float [NF][F_SLOT]
+  static constexpr int OFF_AMAX = OFF_F + NF * F_SLOT * 4;   // uint32 [2][NT][4]
+  static constexpr int OFF_OFFS = OFF_AMAX + 2 * NT * 4 * 4;
+  static constexpr int OFF_TBASE = OFF_OFFS + (MAX_E + 1) * 4;
+  static constexpr int OFF_BAR = (OFF_TBASE + (MAX_E + 1) * 4 + 7) & ~7;
+  static constexpr int NBAR = 2 * NS + 2 * ND + 1;  // full[NS] empty[NS] d_full[ND] d_empty[ND] drain
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
   static constexpr int BYTES = OFF_MISC + 16;
   static constexpr int SMEM = BYTES + 1024;
-  static_assert(NT % 16 == 0 && STAGE % 1024 == 0 && PART <= NS * STAGE, "tile");
+  static_assert(NF >= ND + AHEAD && TMEM_COLS <= 512 && (TMEM_COLS & (TMEM_COLS - 1)) == 0, "accumulators");
+  static_assert(NT % 16 == 0 && NT <= 32 && STAGE % 1024 == 0 && F_SLOT % 4 == 0 && PART <= NS * STAGE, "tile");
   static_assert(PER_SM * (SMEM + 1024) <= 228 * 1024 && PER_SM * TMEM_COLS <= 512, "CTAs per SM");
 };
 
-// Warp roles: 0 TMA producer, 1 MMA issuer and TMEM owner, 2-5 epilogue (TMEM lanes 32 (w % 4)..).
-// One tile per cluster; CTA `rank` of the cluster takes k blocks KB rank / S .. KB (rank + 1) / S.
+// Warp roles: 0 TMA producer, 1 MMA issuer and TMEM owner, 2-5 epilogue (TMEM lanes 32 (w % 4)..), 6 the
+// scales of each k block, as in the wide kernel.
+// Persistent; CTAs that are a cluster of their own take tiles g, g + CTAs, ...  A cluster of S > 1 has one
+// tile, with the partial sums in shared memory when the last k block is done: CTA
+// `rank` takes its k blocks KB rank / S .. KB (rank + 1) / S.
 template <class C, bool GATHER>
 __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
     few_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap wmap,
@@ -750,15 +770,15 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem);
-  constexpr int NS = C::NS, NT = C::NT;
+  constexpr int NS = C::NS, NT = C::NT, ND = C::ND;
   int* s_offs = reinterpret_cast<int*>(smem + C::OFF_OFFS);
   int* s_tbase = reinterpret_cast<int*>(smem + C::OFF_TBASE);
   const uint32_t bar0 = sbase + C::OFF_BAR;
   auto full = [&](int s) { return bar0 + 8u * s; };
   auto empty = [&](int s) { return bar0 + 8u * (NS + s); };
   auto d_full = [&](int d) { return bar0 + 8u * (2 * NS + d); };
-  auto d_empty = [&](int d) { return bar0 + 8u * (2 * NS + 2 + d); };
-  const uint32_t drain_bar = bar0 + 8u * (2 * NS + 4);
+  auto d_empty = [&](int d) { return bar0 + 8u * (2 * NS + ND + d); };
+  const uint32_t drain_bar = bar0 + 8u * (2 * NS + 2 * ND);
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
   volatile int* s_abort = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
 
@@ -772,9 +792,9 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
       mbar_init(full(s), 1);
       mbar_init(empty(s), 1);
     }
-    for (int d = 0; d < 2; ++d) {
-      mbar_init(d_full(d), 1);
-      mbar_init(d_empty(d), 4);
+    for (int d = 0; d < ND; ++d) {
+      mbar_init(d_full(d), 2);   // MMA commit, scales
+      mbar_init(d_empty(d), 4);  // the epilogue warps
     }
     mbar_init(drain_bar, 1);
     *s_abort = 0;
@@ -783,6 +803,10 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
   if (warp == 1) {
     tmem_alloc(smem_u32(s_tmem), C::TMEM_COLS);
     tmem_relinquish();
+  }
+  if (warp == 0 && lane == 0) {
+    prefetch_tmap(&amap);
+    prefetch_tmap(&wmap);
   }
   griddep_wait();
   griddep_launch_dependents();
@@ -803,70 +827,102 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
   const uint32_t tmem_base = *s_tmem;
   const int KB = (args.K + BK - 1) / BK;
   const int total = s_tbase[args.E];
-  const int g = (int)cluster_id_x();
+  const int first = (int)cluster_id_x(), step = (int)cluster_count_x();
   const int kb0 = (int)((int64_t)KB * rank / S), kb1 = (int)((int64_t)KB * (rank + 1) / S);
-  // (a cluster beyond the last tile has nothing to do; the tile index is uniform over a cluster)
-  const bool work = g < total;
-  Tile t = {0, 0, 0, 0};
-  if (work) t = decode_tile(g, args, s_offs, s_tbase, NT, NG);
+  float* part = reinterpret_cast<float*>(smem);
 
-  if (total >= 0) zero_absent(args, s_offs, (int64_t)blockIdx.x * C::THREADS + tid, (int64_t)gridDim.x * C::THREADS);
-  fence_proxy_async_shared();
-  __syncthreads();  // the tables have been read: the stages may be loaded
-
-  float* part = reinterpret_cast<float*>(smem);  // [NT][256], after the last MMA has read the stages
-  bool ok = true;
-  if (work && warp == 0) {
-    // ------------------------------------------------------------------ TMA producer (whole warp)
-    int r[4] = {0, 0, 0, 0};
-    const int nrow4 = (t.cnt + 3) >> 2;
-    if (GATHER && lane < nrow4) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) r[j] = source_row(args, t.p0 + min(4 * lane + j, t.cnt - 1));
+  // Output of token n of tile t from this thread's sums v0 (block 0) and v1 (block 1); the gate/up form
+  // returns the activation, its token's largest among the warp's in s_amax, and is finished by quantise()
+  // once the four epilogue warps have met.
+  const int q = warp & 3;
+  const int j = q * 32 + lane;  // weight row of each block
+  uint32_t* s_amax = reinterpret_cast<uint32_t*>(smem + C::OFF_AMAX);
+  auto store = [&](const Tile& t, int n, float v0, float v1, uint32_t* amax) {
+    const int64_t p = t.p0 + n;
+    if (args.half) {
+      const float act = swiglu_keep_nan(v0, v1, args.limit);
+      const uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(act) & 0x7FFFFFFFu);
+      if (lane == 0) amax[n * 4 + q] = m;
+      return act;
     }
-    const uint32_t bytes = 2 * BLK + (GATHER ? nrow4 * 4 : NT) * BK;
+    const int n0 = block_row<2>(args, t.ng, 0) + j, n1 = n0 + 128;
+    if (args.c_dtype == MOE_DTYPE_BF16) {
+      __nv_bfloat16* c = static_cast<__nv_bfloat16*>(args.C) + p * args.ldc;
+      if (n0 < args.N) c[n0] = __float2bfloat16_rn(v0);
+      if (n1 < args.N) c[n1] = __float2bfloat16_rn(v1);
+    } else {
+      float* c = static_cast<float*>(args.C) + p * args.ldc;
+      if (n0 < args.N) c[n0] = v0;
+      if (n1 < args.N) c[n1] = v1;
+    }
+    return 0.f;
+  };
+  auto quantise = [&](const Tile& t, int n, float act, const uint32_t* amax) {
+    const uint4 m4 = *reinterpret_cast<const uint4*>(amax + n * 4);
+    float scale, inv;
+    fp8_scale(max(max(m4.x, m4.y), max(m4.z, m4.w)), scale, inv);
+    const int64_t p = t.p0 + n;
+    args.q[p * args.ld_q + t.ng * 128 + j] = (uint8_t)pack_e4m3x4(act * inv, 0.f, 0.f, 0.f);
+    if (j == 0) args.s[p * args.s_row + t.ng * args.s_grp] = scale;
+  };
+
+  bool ok = true;
+  if (warp == 0) {
+    // ------------------------------------------------------------------ TMA producer (whole warp)
     int i = 0;
-    for (int kb = kb0; kb < kb1; ++kb, ++i) {
-      const int s = i % NS;
-      if (!warp_wait(empty(s), ((i / NS) & 1) ^ 1, s_abort, err, limit)) {
-        ok = false;
-        break;
+    for (int g = first; ok && g < total; g += step) {
+      const Tile t = decode_tile(g, args, s_offs, s_tbase, NT, NG);
+      int r[4] = {0, 0, 0, 0};
+      const int nrow4 = (t.cnt + 3) >> 2;
+      if (GATHER && lane < nrow4) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) r[j] = source_row(args, t.p0 + min(4 * lane + j, t.cnt - 1));
       }
-      const uint32_t st = sbase + s * C::STAGE;
-      if (lane == 0) {
-        mbar_arrive_expect_tx(full(s), bytes);
-        tma_load_3d(st, &wmap, kb * BK, block_row<2>(args, t.ng, 0), t.e, full(s));
-        tma_load_3d(st + BLK, &wmap, kb * BK, block_row<2>(args, t.ng, 1), t.e, full(s));
-        if (!GATHER) tma_load_2d(st + 2 * BLK, &amap, kb * BK, t.p0, full(s));
-      }
-      if (GATHER) {
-        __syncwarp();
-        if (lane < nrow4) tma_gather4(st + 2 * BLK + lane * 4 * BK, &amap, kb * BK, r[0], r[1], r[2], r[3], full(s));
+      const uint32_t bytes = 2 * BLK + (GATHER ? nrow4 * 4 : NT) * BK;
+      for (int kb = kb0; kb < kb1; ++kb, ++i) {
+        const int s = i % NS;
+        if (!warp_wait(empty(s), ((i / NS) & 1) ^ 1, s_abort, err, limit)) {
+          ok = false;
+          break;
+        }
+        const uint32_t st = sbase + s * C::STAGE;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(full(s), bytes);
+          tma_load_3d(st, &wmap, kb * BK, block_row<2>(args, t.ng, 0), t.e, full(s));
+          tma_load_3d(st + BLK, &wmap, kb * BK, block_row<2>(args, t.ng, 1), t.e, full(s));
+          if (!GATHER) tma_load_2d(st + 2 * BLK, &amap, kb * BK, t.p0, full(s));
+        }
+        if (GATHER) {
+          __syncwarp();
+          if (lane < nrow4) tma_gather4(st + 2 * BLK + lane * 4 * BK, &amap, kb * BK, r[0], r[1], r[2], r[3], full(s));
+        }
       }
     }
     if (!ok && lane == 0)
       for (int j = max(0, i - NS); j < i; ++j) mbar_wait_drain(full(j % NS), (j / NS) & 1);
-  } else if (work && warp == 1) {
+  } else if (warp == 1) {
     // ------------------------------------------------------------------ MMA issuer
     constexpr uint32_t idesc = make_idesc_e4m3(128, NT);
     int i = 0;
-    for (int kb = kb0; kb < kb1; ++kb, ++i) {
-      const int s = i % NS, db = i & 1;
-      if (!warp_wait(d_empty(db), ((i >> 1) & 1) ^ 1, s_abort, err, limit) ||
-          !warp_wait(full(s), (i / NS) & 1, s_abort, err, limit)) {
-        ok = false;
-        break;
+    for (int g = first; ok && g < total; g += step) {
+      for (int kb = kb0; kb < kb1; ++kb, ++i) {
+        const int s = i % NS, db = i % ND;
+        if (!warp_wait(full(s), (i / NS) & 1, s_abort, err, limit) ||
+            !warp_wait(d_empty(db), ((i / ND) & 1) ^ 1, s_abort, err, limit)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t st = sbase + s * C::STAGE;
+        if (elect_one()) {
+          const uint64_t tok = make_sdesc_sw128(st + 2 * BLK);
+          mma4_e4m3_ss(tmem_base + (uint32_t)(db * 2 * NT), make_sdesc_sw128(st), tok, idesc);
+          mma4_e4m3_ss(tmem_base + (uint32_t)(db * 2 * NT + NT), make_sdesc_sw128(st + BLK), tok, idesc);
+          mma_commit(d_full(db));
+          mma_commit(empty(s));
+        }
+        __syncwarp();
       }
-      tc_fence_after();
-      const uint32_t st = sbase + s * C::STAGE;
-      if (elect_one()) {
-        const uint64_t tok = make_sdesc_sw128(st + 2 * BLK);
-        mma4_e4m3_ss(tmem_base + (uint32_t)(db * 2 * NT), make_sdesc_sw128(st), tok, idesc);
-        mma4_e4m3_ss(tmem_base + (uint32_t)(db * 2 * NT + NT), make_sdesc_sw128(st + BLK), tok, idesc);
-        mma_commit(empty(s));
-        mma_commit(d_full(db));
-      }
-      __syncwarp();
     }
     if (!ok) {
       if (elect_one()) {
@@ -875,149 +931,155 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
       }
       __syncwarp();
     }
-  } else if (work) {
-    // ------------------------------------------------------------------ accumulation
-    const int q = warp & 3;
-    const uint32_t lane_base = tmem_base + ((uint32_t)(q * 32) << 16);
-    // this warp's products sa * sw of the k block for both weight blocks: [2 buffers][2][NT]
-    float* s_f = reinterpret_cast<float*>(smem + C::OFF_SCALE) + (warp - 2) * 4 * NT;
-    constexpr int PT = (NT + 31) / 32;  // tokens whose scales this lane holds
-    const float* sa[PT];
-#pragma unroll
-    for (int j = 0; j < PT; ++j)
-      sa[j] = args.sa + (int64_t)source_row(args, t.p0 + min(lane + 32 * j, t.cnt - 1)) * args.sa_row;
-    const float* sw0 = args.sw + ((int64_t)t.e * args.nblk + (block_row<2>(args, t.ng, 0) >> 7)) * KB;
-    const float* sw1 =
-        args.sw + ((int64_t)t.e * args.nblk + min(block_row<2>(args, t.ng, 1) >> 7, args.nblk - 1)) * KB;
-    uint64_t acc[2][NT / 2];
-#pragma unroll
-    for (int j = 0; j < NT / 2; ++j) acc[0][j] = acc[1][j] = 0;
-    float pa[2][PT], pw[2][2];
-#pragma unroll
-    for (int d = 0; d < 2; ++d) {
-      const int k = min(kb0 + d, KB - 1);
-#pragma unroll
-      for (int j = 0; j < PT; ++j) pa[d][j] = __ldg(sa[j] + k * args.sa_grp);
-      pw[d][0] = __ldg(sw0 + k);
-      pw[d][1] = __ldg(sw1 + k);
-    }
-    int i = 0;
-    for (int kb = kb0; kb < kb1; ++kb, ++i) {
-      const int db = i & 1;
-      float* f = s_f + db * 2 * NT;
-#pragma unroll
-      for (int j = 0; j < PT; ++j) {
-        if (lane + 32 * j < NT) {
-          f[lane + 32 * j] = pa[0][j] * pw[0][0];
-          f[NT + lane + 32 * j] = pa[0][j] * pw[0][1];
+  } else if (warp == 6) {
+    // ------------------------------------------------------------------ scales of every k block
+    const float* sa = nullptr;
+    const float* sw = nullptr;
+    int g = first, kb = kb0, n = 0;
+    auto copy_next = [&]() {
+      if (g < total) {
+        if (kb == kb0) {
+          const Tile t = decode_tile(g, args, s_offs, s_tbase, NT, NG);
+          sa = args.sa + (int64_t)source_row(args, t.p0 + min(lane, t.cnt - 1)) * args.sa_row + kb0 * args.sa_grp;
+          const int blk = min(block_row<2>(args, t.ng, lane & 1) >> 7, args.nblk - 1);
+          sw = args.sw + ((int64_t)t.e * args.nblk + blk) * KB;
         }
-        pa[0][j] = pa[1][j];
-        pa[1][j] = __ldg(sa[j] + min(kb + 2, KB - 1) * args.sa_grp);
+        const uint32_t dst = sbase + C::OFF_F + (uint32_t)((n % C::NF) * C::F_SLOT + lane) * 4u;
+        if (lane < NT) cp_async4(dst, sa);
+        sa += args.sa_grp;
+        if (lane < 2) cp_async4(dst + NT * 4u, sw + kb);
+        if (++kb == kb1) {
+          kb = kb0;
+          g += step;
+        }
+        ++n;
       }
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        pw[0][h] = pw[1][h];
-        pw[1][h] = __ldg((h ? sw1 : sw0) + min(kb + 2, KB - 1));
-      }
+      cp_async_commit();  // (an empty group past the last block)
+    };
+    for (int j = 0; j < C::AHEAD; ++j) copy_next();
+    for (int i = 0; i < n; ++i) {
+      if (!warp_wait(d_empty(i % ND), ((i / ND) & 1) ^ 1, s_abort, err, limit)) break;
+      cp_async_wait<C::AHEAD - 1>();
       __syncwarp();
-      if (!warp_wait(d_full(db), (i >> 1) & 1, s_abort, err, limit)) {
+      if (lane == 0) mbar_arrive(d_full(i % ND));
+      copy_next();
+    }
+    cp_async_wait<0>();
+  } else {
+    // ------------------------------------------------------------------ epilogue
+    const uint32_t lane_base = tmem_base + ((uint32_t)(q * 32) << 16);
+    const float* s_f = reinterpret_cast<const float*>(smem + C::OFF_F);
+    int i = 0, tile = 0;
+    for (int g = first; ok && g < total; g += step, ++tile) {
+      uint64_t acc[2][NT / 2];
+#pragma unroll
+      for (int j = 0; j < NT / 2; ++j) acc[0][j] = acc[1][j] = 0;
+      for (int kb = kb0; kb < kb1; ++kb, ++i) {
+        const int db = i % ND;
+        if (!warp_wait(d_full(db), (i / ND) & 1, s_abort, err, limit)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        uint32_t v[2 * NT / 16][16];
+#pragma unroll
+        for (int c = 0; c < 2 * NT / 16; ++c)
+          tmem_ld_32x32b_x16(lane_base + (uint32_t)(db * 2 * NT + c * 16), v[c]);
+        const float* slot = s_f + (i % C::NF) * C::F_SLOT;
+        uint64_t sa[NT / 2];  // of tokens 2 j and 2 j + 1
+#pragma unroll
+        for (int j = 0; j < NT / 4; ++j) {
+          const ulonglong2 u = reinterpret_cast<const ulonglong2*>(slot)[j];
+          sa[2 * j] = u.x;
+          sa[2 * j + 1] = u.y;
+        }
+        const uint64_t sw[2] = {pack_f32x2(slot[NT], slot[NT]), pack_f32x2(slot[NT + 1], slot[NT + 1])};
+#pragma unroll
+        for (int c = 0; c < 2 * NT / 16; ++c) tmem_wait_ld_regs(v[c]);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(d_empty(db));
+#pragma unroll
+        for (int c = 0; c < 2 * NT / 16; ++c) {  // 16 columns: tokens 16 (c % (NT / 16)).. of block c / (NT / 16)
+          constexpr int PER = NT / 16;
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            fma_f32x2(acc[c / PER][(c % PER) * 8 + j], v[c][2 * j], v[c][2 * j + 1],
+                      mul_f32x2(sa[(c % PER) * 8 + j], sw[c / PER]));
+        }
+      }
+      // (all four warps leave the loop at the same tile)
+      if (named_bar_any(1, 128, !ok)) {
         ok = false;
         break;
       }
-      tc_fence_after();
-      const uint32_t base = lane_base + (uint32_t)(db * 2 * NT);
+      if (S > 1) {
+        // every k block has been accumulated, so the stages are drained
 #pragma unroll
-      for (int c = 0; c < 2 * NT / 16; ++c) {  // 16 columns: tokens 16 (c % (NT / 16)).. of block c / (NT / 16)
-        uint32_t v[16];
-        tmem_ld_32x32b_x16(base + c * 16, v);
-        tmem_wait_ld_regs(v);
-        if (c + 1 == 2 * NT / 16) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(d_empty(db));
+        for (int n = 0; n < NT / 2; ++n)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            float a0, a1;
+            unpack_f32x2(acc[h][n], a0, a1);
+            part[(2 * n) * 256 + h * 128 + j] = a0;
+            part[(2 * n + 1) * 256 + h * 128 + j] = a1;
+          }
+      } else {
+        const Tile t = decode_tile(g, args, s_offs, s_tbase, NT, NG);
+        uint32_t* amax = s_amax + (tile & 1) * NT * 4;
+#pragma unroll
+        for (int n = 0; n < NT; n += 2) {
+          if (n >= t.cnt) break;
+          float g0, g1, u0, u1;
+          unpack_f32x2(acc[0][n / 2], g0, g1);
+          unpack_f32x2(acc[1][n / 2], u0, u1);
+          g0 = store(t, n, g0, u0, amax);
+          if (n + 1 < t.cnt) g1 = store(t, n + 1, g1, u1, amax);
+          acc[0][n / 2] = pack_f32x2(g0, g1);
         }
-        const ulonglong2* fc = reinterpret_cast<const ulonglong2*>(f + c * 16);
+        if (args.half) {
+          named_bar_sync(1, 128);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const ulonglong2 ff = fc[j];
-          uint64_t* a = &acc[c / (NT / 16)][(c % (NT / 16)) * 8 + 2 * j];
-          fma_f32x2(a[0], v[4 * j], v[4 * j + 1], ff.x);
-          fma_f32x2(a[1], v[4 * j + 2], v[4 * j + 3], ff.y);
+          for (int n = 0; n < NT; n += 2) {
+            if (n >= t.cnt) break;
+            float a0, a1;
+            unpack_f32x2(acc[0][n / 2], a0, a1);
+            quantise(t, n, a0, amax);
+            if (n + 1 < t.cnt) quantise(t, n + 1, a1, amax);
+          }
         }
       }
     }
-    // Partial sums to shared memory: the last accumulator is complete, so every stage has been
-    // read and no copy is in flight.  (All four warps pass the last d_full before any writes.)
-    named_bar_sync(1, 128);
-    if (ok) {
-#pragma unroll
-      for (int j = 0; j < NT / 2; ++j)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          float a0, a1;
-          unpack_f32x2(acc[h][j], a0, a1);
-          part[(2 * j) * 256 + h * 128 + q * 32 + lane] = a0;
-          part[(2 * j + 1) * 256 + h * 128 + q * 32 + lane] = a1;
-        }
-    }
   }
+  if (total >= 0)
+    zero_absent(args, s_offs, (int64_t)blockIdx.x * C::THREADS + tid, (int64_t)gridDim.x * C::THREADS);
 
   if (S > 1) {
     __syncwarp();
     cluster_sync_all();
-  } else {
-    __syncthreads();
-  }
-  if (work && warp >= 2 && *s_abort == 0) {
-    // ------------------------------------------------------------------ join and store
-    // token n belongs to rank n % S, which adds the S partial sums in rank order
-    const int q = warp & 3;
-    const int j = q * 32 + lane;  // weight row of each block
-    uint32_t* s_amax = reinterpret_cast<uint32_t*>(smem + C::OFF_AMAX);
-    for (int n = rank; n < t.cnt; n += S) {
-      float v0 = 0.f, v1 = 0.f;
-      for (int c = 0; c < S; ++c) {
-        const uint32_t at = sbase + (uint32_t)(n * 256 + j) * 4u;
-        v0 += ld_shared_cluster_f32(at, (uint32_t)c);
-        v1 += ld_shared_cluster_f32(at + 512u, (uint32_t)c);
-      }
-      const int64_t p = t.p0 + n;
-      if (args.half) {
-        const float act = swiglu_keep_nan(v0, v1, args.limit);
-        part[n * 256 + j] = act;  // only this thread reads this element of this CTA's token n
-        const uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(act) & 0x7FFFFFFFu);
-        if (lane == 0) s_amax[n * 4 + q] = m;
-      } else {
-        const int n0 = block_row<2>(args, t.ng, 0) + j, n1 = n0 + 128;
-        if (args.c_dtype == MOE_DTYPE_BF16) {
-          __nv_bfloat16* c = static_cast<__nv_bfloat16*>(args.C) + p * args.ldc;
-          if (n0 < args.N) c[n0] = __float2bfloat16_rn(v0);
-          if (n1 < args.N) c[n1] = __float2bfloat16_rn(v1);
-        } else {
-          float* c = static_cast<float*>(args.C) + p * args.ldc;
-          if (n0 < args.N) c[n0] = v0;
-          if (n1 < args.N) c[n1] = v1;
-        }
-      }
-    }
-    if (args.half) {
-      named_bar_sync(1, 128);
+    if (warp >= 2 && warp < 6 && ok && first < total) {
+      // token n belongs to rank n % S, which adds the S partial sums in rank order
+      const Tile t = decode_tile(first, args, s_offs, s_tbase, NT, NG);
       for (int n = rank; n < t.cnt; n += S) {
-        const uint4 m4 = *reinterpret_cast<const uint4*>(s_amax + n * 4);
-        float scale, inv;
-        fp8_scale(max(max(m4.x, m4.y), max(m4.z, m4.w)), scale, inv);
-        const int64_t p = t.p0 + n;
-        const uint32_t code = pack_e4m3x4(part[n * 256 + j] * inv, 0.f, 0.f, 0.f);
-        args.q[p * args.ld_q + t.ng * 128 + j] = (uint8_t)code;
-        if (j == 0) args.s[p * args.s_row + t.ng * args.s_grp] = scale;
+        float v0 = 0.f, v1 = 0.f;
+        for (int c = 0; c < S; ++c) {
+          const uint32_t at = sbase + (uint32_t)(n * 256 + j) * 4u;
+          v0 += ld_shared_cluster_f32(at, (uint32_t)c);
+          v1 += ld_shared_cluster_f32(at + 512u, (uint32_t)c);
+        }
+        v0 = store(t, n, v0, v1, s_amax);
+        if (args.half) part[n * 256 + j] = v0;  // (only this thread reads this element of this CTA's)
+      }
+      if (args.half) {
+        named_bar_sync(1, 128);
+        for (int n = rank; n < t.cnt; n += S) quantise(t, n, part[n * 256 + j], s_amax);
       }
     }
-  }
-  tc_fence_before();
-  if (S > 1) {  // the other CTAs have read this one's partial sums
+    tc_fence_before();
     __syncwarp();
-    cluster_sync_all();
+    cluster_sync_all();  // the other CTAs have read this one's sums
   } else {
+    tc_fence_before();
     __syncthreads();
   }
   if (warp == 1) {
@@ -1117,15 +1179,14 @@ int launch_few(const Fp8Gemm& d, int64_t tiles, cudaStream_t st) {
   if (rc != MOE_OK) return rc;
   static std::atomic<int> configured[64];
   if ((rc = configure(few_kernel<C, GATHER>, C::SMEM, configured)) != MOE_OK) return rc;
-  // Split k as far as every CTA is still resident at once and keeps two k blocks: more CTAs than that
-  // queue for SMs, and each costs ~4 us of start and join (one token's gate/up at 160 experts, 96 tiles:
-  // 26.4 us with one CTA to a tile, 24.1 with three, 30.4 with four, which no longer fit).
+  // Split k as far as every CTA is still resident at once and keeps two k blocks.
   const int KB = (d.args.K + BK - 1) / BK;
   int S = 1;
   for (int t = 2; t <= 8 && 2 * t <= KB; ++t)
     if (tiles <= resident_clusters<C, GATHER>(t)) S = t;
-  return launch_pdl_cluster(few_kernel<C, GATHER>, dim3((unsigned)(tiles * S)), dim3(C::THREADS), C::SMEM, st, S, am,
-                            wm, d.args);
+  const int64_t grid = S > 1 ? tiles * S : std::min<int64_t>(tiles, device_sm_count() * C::PER_SM);
+  return launch_pdl_cluster(few_kernel<C, GATHER>, dim3((unsigned)grid), dim3(C::THREADS), C::SMEM, st, S, am, wm,
+                            d.args);
 }
 
 // Upper bound of the number of token tiles of BT rows: experts with rows plus their full tiles.
@@ -1145,7 +1206,7 @@ int launch(const Fp8Gemm& d, cudaStream_t st) {
   const int64_t wide_tiles = a.half ? tt * ng2 : tt * ((a.N + 127) / 128);
   if (rows <= 8 || (rows <= 256 && 2 * wide_tiles <= device_sm_count())) {
     if (rows <= 48) return launch_few<FewCfg<16, 3, 2>, GATHER>(d, token_tiles(d, 16) * ng2, st);
-    return launch_few<FewCfg<32, 3, 2>, GATHER>(d, token_tiles(d, 32) * ng2, st);
+    return launch_few<FewCfg<32, 5, 1>, GATHER>(d, token_tiles(d, 32) * ng2, st);
   }
   if (a.half) return launch_wide<WideCfg<2, GATHER, true>>(d, tt * ng2, st);
   if (tt * ng2 < device_sm_count()) return launch_wide<WideCfg<1, GATHER, false>>(d, tt * ((a.N + 127) / 128), st);
