@@ -527,7 +527,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     // ------------------------------------------------------------------ gathered token rows
     // 16-byte cp.async into the swizzled layout (chunk c of row r at c ^ (r % 8)): 8 lanes to a row of
     // the k block, 4 rows to an instruction, every fourth group of 4 rows to a warp.  (TMA gather4
-    // moved ~12 bytes per cycle and SM where a tile takes ~20.)  Rows past the tile's repeat its last.
+    // moved ~12 bytes per cycle and SM where a tile takes ~20.)  Sixteens of rows past the tile's are left as
+    // they are (their accumulator rows are not stored), single rows repeat its last.
     reg_dec<C::REG_LOW>();
     const int r0 = (warp - 12) * 4 + (lane >> 3);  // rows r0 + 16 j: the same chunk place in all of them
     const int chunk = lane & 7;
@@ -549,11 +550,13 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         const int left = args.K - kb * BK - chunk * 16;
         if (left >= 16) {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) cp_async16(dst + s * C::STAGE + j * 16 * BK, src[j], 16);
+          for (int j = 0; j < 8; ++j)
+            if (16 * j < t.cnt) cp_async16(dst + s * C::STAGE + j * 16 * BK, src[j], 16);
         } else {  // past K: zeros (an address inside the row, of which nothing or the rest is read)
 #pragma unroll
           for (int j = 0; j < 8; ++j)
-            cp_async16(dst + s * C::STAGE + j * 16 * BK, left > 0 ? src[j] : args.A, (uint32_t)max(left, 0));
+            if (16 * j < t.cnt)
+              cp_async16(dst + s * C::STAGE + j * 16 * BK, left > 0 ? src[j] : args.A, (uint32_t)max(left, 0));
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j) src[j] += BK;
@@ -588,35 +591,37 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         }
         tc_fence_after();
         const uint32_t base = lane_base + (uint32_t)(db * C::BN);
-        // 16 columns at a time through two register buffers (column j of this warp's 64 NB is column
+        // 16 columns at a time through three register buffers (column j of this warp's 64 NB is column
         // j % 64 of block j / 64); the accumulator is given back once its last columns are in registers
-        uint32_t v[2][16];
+        constexpr int NV = 3;
+        uint32_t v[NV][16];
         auto load = [&](int c) {
-          tmem_ld_32x32b_x16(base + (uint32_t)((c >> 2) * 128 + (c & 3) * 16), v[c & 1]);
+          tmem_ld_32x32b_x16(base + (uint32_t)((c >> 2) * 128 + (c & 3) * 16), v[c % NV]);
         };
-        load(0);
-        load(1);
+#pragma unroll
+        for (int c = 0; c < NV; ++c) load(c);
         uint64_t f[NB];
 #pragma unroll
         for (int h = 0; h < NB; ++h) {
           const float* slot = s_f + (i % C::NF) * C::F_SLOT;
-          const float v = slot[row] * slot[128 + h];
-          f[h] = pack_f32x2(v, v);
+          const float x = slot[row] * slot[128 + h];
+          f[h] = pack_f32x2(x, x);
         }
 #pragma unroll
-        for (int c = 0; c < 4 * NB; c += 2) {
-          tmem_wait_ld_regs(v[0]);
-          tmem_wait_ld_regs(v[1]);
-          if (c == 4 * NB - 2) {
+        for (int c = 0; c < 4 * NB; c += NV) {
+#pragma unroll
+          for (int d = 0; d < NV; ++d) tmem_wait_ld_regs(v[d]);
+          if (c + NV >= 4 * NB) {
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(d_empty(db));
           }
 #pragma unroll
-          for (int d = c; d < c + 2; ++d) {
+          for (int d = c; d < c + NV && d < 4 * NB; ++d) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) fma_f32x2(acc[d >> 2][(d & 3) * 8 + j], v[d & 1][2 * j], v[d & 1][2 * j + 1], f[d >> 2]);
-            if (d + 2 < 4 * NB) load(d + 2);
+            for (int j = 0; j < 8; ++j)
+              fma_f32x2(acc[d >> 2][(d & 3) * 8 + j], v[d % NV][2 * j], v[d % NV][2 * j + 1], f[d >> 2]);
+            if (d + NV < 4 * NB) load(d + NV);
           }
         }
       }
@@ -835,7 +840,7 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
   // returns the activation, its token's largest among the warp's in s_amax, and is finished by quantise()
   // once the four epilogue warps have met.
   const int q = warp & 3;
-  const int j = q * 32 + lane;  // weight row of each block
+  const int wr = q * 32 + lane;  // weight row of each block
   uint32_t* s_amax = reinterpret_cast<uint32_t*>(smem + C::OFF_AMAX);
   auto store = [&](const Tile& t, int n, float v0, float v1, uint32_t* amax) {
     const int64_t p = t.p0 + n;
@@ -845,7 +850,7 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
       if (lane == 0) amax[n * 4 + q] = m;
       return act;
     }
-    const int n0 = block_row<2>(args, t.ng, 0) + j, n1 = n0 + 128;
+    const int n0 = block_row<2>(args, t.ng, 0) + wr, n1 = n0 + 128;
     if (args.c_dtype == MOE_DTYPE_BF16) {
       __nv_bfloat16* c = static_cast<__nv_bfloat16*>(args.C) + p * args.ldc;
       if (n0 < args.N) c[n0] = __float2bfloat16_rn(v0);
@@ -862,8 +867,8 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
     float scale, inv;
     fp8_scale(max(max(m4.x, m4.y), max(m4.z, m4.w)), scale, inv);
     const int64_t p = t.p0 + n;
-    args.q[p * args.ld_q + t.ng * 128 + j] = (uint8_t)pack_e4m3x4(act * inv, 0.f, 0.f, 0.f);
-    if (j == 0) args.s[p * args.s_row + t.ng * args.s_grp] = scale;
+    args.q[p * args.ld_q + t.ng * 128 + wr] = (uint8_t)pack_e4m3x4(act * inv, 0.f, 0.f, 0.f);
+    if (wr == 0) args.s[p * args.s_row + t.ng * args.s_grp] = scale;
   };
 
   bool ok = true;
@@ -1021,8 +1026,8 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
           for (int h = 0; h < 2; ++h) {
             float a0, a1;
             unpack_f32x2(acc[h][n], a0, a1);
-            part[(2 * n) * 256 + h * 128 + j] = a0;
-            part[(2 * n + 1) * 256 + h * 128 + j] = a1;
+            part[(2 * n) * 256 + h * 128 + wr] = a0;
+            part[(2 * n + 1) * 256 + h * 128 + wr] = a1;
           }
       } else {
         const Tile t = decode_tile(g, args, s_offs, s_tbase, NT, NG);
@@ -1063,16 +1068,16 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
       for (int n = rank; n < t.cnt; n += S) {
         float v0 = 0.f, v1 = 0.f;
         for (int c = 0; c < S; ++c) {
-          const uint32_t at = sbase + (uint32_t)(n * 256 + j) * 4u;
+          const uint32_t at = sbase + (uint32_t)(n * 256 + wr) * 4u;
           v0 += ld_shared_cluster_f32(at, (uint32_t)c);
           v1 += ld_shared_cluster_f32(at + 512u, (uint32_t)c);
         }
         v0 = store(t, n, v0, v1, s_amax);
-        if (args.half) part[n * 256 + j] = v0;  // (only this thread reads this element of this CTA's)
+        if (args.half) part[n * 256 + wr] = v0;  // (only this thread reads this element of this CTA's)
       }
       if (args.half) {
         named_bar_sync(1, 128);
-        for (int n = rank; n < t.cnt; n += S) quantise(t, n, part[n * 256 + j], s_amax);
+        for (int n = rank; n < t.cnt; n += S) quantise(t, n, part[n * 256 + wr], s_amax);
       }
     }
     tc_fence_before();
@@ -1204,7 +1209,7 @@ int launch(const Fp8Gemm& d, cudaStream_t st) {
   const int64_t ng2 = a.half ? a.half / 128 : (a.N + 255) / 256;
   const int64_t tt = token_tiles(d, 128);
   const int64_t wide_tiles = a.half ? tt * ng2 : tt * ((a.N + 127) / 128);
-  if (rows <= 8 || (rows <= 256 && 2 * wide_tiles <= device_sm_count())) {
+  if (rows <= 16 || (rows <= 256 && 2 * wide_tiles <= device_sm_count())) {
     if (rows <= 48) return launch_few<FewCfg<16, 3, 2>, GATHER>(d, token_tiles(d, 16) * ng2, st);
     return launch_few<FewCfg<32, 5, 1>, GATHER>(d, token_tiles(d, 32) * ng2, st);
   }
