@@ -12,6 +12,7 @@
 // rounding), its code is written once.
 
 #include <algorithm>
+#include <atomic>
 
 #include "fp8.cuh"
 #include "internal.h"
@@ -36,31 +37,61 @@ MOE_DEV float load1<float>(const float* p) {
   return __ldg(p);
 }
 
-// 16 consecutive elements, 16-byte aligned
-MOE_DEV void load16(const uint16_t* p, float (&v)[16]) {
-  const uint4 a = __ldg(reinterpret_cast<const uint4*>(p));
-  const uint4 b = __ldg(reinterpret_cast<const uint4*>(p) + 1);
-  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+// 16 consecutive elements, 16-byte aligned, as they are in memory
+template <typename T>
+struct Raw16 {
+  uint4 w[sizeof(T)];
+};
+template <typename T>
+MOE_DEV Raw16<T> load16(const T* p) {
+  Raw16<T> r;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    v[2 * i] = bf16_lo(w[i]);
-    v[2 * i + 1] = bf16_hi(w[i]);
+  for (int i = 0; i < (int)sizeof(T); ++i) r.w[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
+  return r;
+}
+MOE_DEV void unpack16(const Raw16<uint16_t>& r, float (&v)[16]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t w[4] = {r.w[i].x, r.w[i].y, r.w[i].z, r.w[i].w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      v[8 * i + 2 * j] = bf16_lo(w[j]);
+      v[8 * i + 2 * j + 1] = bf16_hi(w[j]);
+    }
   }
 }
-MOE_DEV void load16(const float* p, float (&v)[16]) {
+MOE_DEV void unpack16(const Raw16<float>& r, float (&v)[16]) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float4 a = __ldg(reinterpret_cast<const float4*>(p) + i);
-    v[4 * i] = a.x;
-    v[4 * i + 1] = a.y;
-    v[4 * i + 2] = a.z;
-    v[4 * i + 3] = a.w;
+    v[4 * i] = __uint_as_float(r.w[i].x);
+    v[4 * i + 1] = __uint_as_float(r.w[i].y);
+    v[4 * i + 2] = __uint_as_float(r.w[i].z);
+    v[4 * i + 3] = __uint_as_float(r.w[i].w);
   }
 }
 
+// A warp's place in the items (row, one of per_row pieces of it), advanced without divisions.
+struct Walk {
+  uint32_t row, piece, drow, dpiece, per_row;
+  MOE_DEV Walk(uint32_t warps, uint32_t first, uint32_t per) : per_row(per) {
+    row = first / per;
+    piece = first - row * per;
+    drow = warps / per;
+    dpiece = warps - drow * per;
+  }
+  MOE_DEV void next() {
+    row += drow;
+    piece += dpiece;
+    if (piece >= per_row) {
+      piece -= per_row;
+      ++row;
+    }
+  }
+};
+
 // Rows, 16 elements to a lane and 8 lanes to a group: a warp takes four consecutive groups of one
-// row.  For 16-byte aligned rows (VEC); K need not be a multiple of 16 (the last lane's elements
-// are then loaded one by one).
+// row, the next four on their way meanwhile.  For 16-byte aligned rows; K need not be a multiple of 16
+// (the last lane's elements are then loaded one by one).
 template <typename T>
 __global__ void __launch_bounds__(256) rows_vec_kernel(const T* __restrict__ x, int64_t ld_x, int R, int K, uint8_t* q,
                                                        int64_t ld_q, float* s, int64_t s_row, int64_t s_grp) {
@@ -69,20 +100,26 @@ __global__ void __launch_bounds__(256) rows_vec_kernel(const T* __restrict__ x, 
   const int lane = threadIdx.x & 31;
   const int sub = lane & 7;
   const int ngrp = (K + G - 1) / G;
-  const int per_row = (ngrp + 3) / 4;
-  const int64_t items = (int64_t)R * per_row;
-  const int64_t step = (int64_t)gridDim.x * (blockDim.x >> 5);
-  for (int64_t it = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); it < items; it += step) {
-    const int64_t row = it / per_row;
-    const int grp = (int)(it - row * per_row) * 4 + (lane >> 3);
-    const int k0 = grp * G + sub * 16;
+  Walk at(gridDim.x * 8, blockIdx.x * 8 + (threadIdx.x >> 5), (ngrp + 3) / 4);
+  // this lane's elements of piece p of a row: group, first column, how many
+  auto group = [&](uint32_t p) { return (int)p * 4 + (lane >> 3); };
+  auto load = [&](const Walk& w, Raw16<T>& r) {
+    const int k0 = group(w.piece) * G + sub * 16;
+    if (w.row < (uint32_t)R && k0 + 16 <= K) r = load16(x + w.row * ld_x + k0);
+  };
+  Raw16<T> cur = {}, nxt = {};
+  load(at, cur);
+  while (at.row < (uint32_t)R) {
+    Walk then = at;
+    then.next();
+    load(then, nxt);
+    const int grp = group(at.piece), k0 = grp * G + sub * 16;
     const int n = max(0, min(16, K - k0));
     float v[16];
-    if (n == 16) {
-      load16(x + row * ld_x + k0, v);
-    } else {
+    unpack16(cur, v);
+    if (n < 16) {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) v[i] = i < n ? load1(x + row * ld_x + k0 + i) : 0.f;
+      for (int i = 0; i < 16; ++i) v[i] = i < n ? load1(x + at.row * ld_x + k0 + i) : 0.f;
     }
     uint32_t m = 0;
 #pragma unroll
@@ -95,7 +132,7 @@ __global__ void __launch_bounds__(256) rows_vec_kernel(const T* __restrict__ x, 
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       w[i] = pack_e4m3x4(v[4 * i] * inv, v[4 * i + 1] * inv, v[4 * i + 2] * inv, v[4 * i + 3] * inv);
-    uint8_t* dst = q + row * ld_q + k0;
+    uint8_t* dst = q + at.row * ld_q + k0;
     if (n == 16) {
       *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
     } else {
@@ -103,12 +140,14 @@ __global__ void __launch_bounds__(256) rows_vec_kernel(const T* __restrict__ x, 
       for (int i = 0; i < 16; ++i)
         if (i < n) dst[i] = (uint8_t)(w[i >> 2] >> (8 * (i & 3)));
     }
-    if (sub == 0 && grp < ngrp) s[row * s_row + grp * s_grp] = scale;
+    if (sub == 0 && grp < ngrp) s[at.row * s_row + grp * s_grp] = scale;
+    at = then;
+    cur = nxt;
   }
 }
 
-// Rows of any alignment, 4 consecutive elements to a lane and a warp to a group; U groups in flight
-// per warp.  Codes are stored as words (q is 16-byte aligned with ld_q a multiple of 16).
+// Rows of any alignment, 4 consecutive elements to a lane and a warp to a group; U groups of a row in
+// flight per warp.  Codes are stored as words (q is 16-byte aligned with ld_q a multiple of 16).
 template <typename T, int U>
 __global__ void __launch_bounds__(256) rows_any_kernel(const T* __restrict__ x, int64_t ld_x, int R, int K, uint8_t* q,
                                                        int64_t ld_q, float* s, int64_t s_row, int64_t s_grp) {
@@ -116,12 +155,9 @@ __global__ void __launch_bounds__(256) rows_any_kernel(const T* __restrict__ x, 
   griddep_launch_dependents();
   const int lane = threadIdx.x & 31;
   const int ngrp = (K + G - 1) / G;
-  const int per_row = (ngrp + U - 1) / U;
-  const int64_t items = (int64_t)R * per_row;
-  const int64_t step = (int64_t)gridDim.x * (blockDim.x >> 5);
-  for (int64_t it = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); it < items; it += step) {
-    const int64_t row = it / per_row;
-    const int g0 = (int)(it - row * per_row) * U;
+  for (Walk at(gridDim.x * 8, blockIdx.x * 8 + (threadIdx.x >> 5), (ngrp + U - 1) / U); at.row < (uint32_t)R; at.next()) {
+    const int64_t row = at.row;
+    const int g0 = (int)at.piece * U;
     const T* src = x + row * ld_x;
     float v[U][4];
 #pragma unroll
@@ -168,25 +204,34 @@ __global__ void __launch_bounds__(256) blocks_kernel(const T* __restrict__ w, in
   const int n0 = blockIdx.y * G + warp;
   float v[16][4];
   uint32_t m = 0;
+  if (VEC && (blockIdx.x + 1) * G <= K && (blockIdx.y + 1) * G <= N) {
+    // every load before the first use
+    uint32_t raw[16][sizeof(T)];
 #pragma unroll
-  for (int r = 0; r < 16; ++r) {
-    const int n = n0 + 8 * r;
-    const T* src = w + (int64_t)n * ld_w + k0;
-    if (VEC && n < N && k0 + 4 <= K) {
+    for (int r = 0; r < 16; ++r) {
+      const T* src = w + (int64_t)(n0 + 8 * r) * ld_w + k0;
       if constexpr (sizeof(T) == 2) {
         const uint2 a = __ldg(reinterpret_cast<const uint2*>(src));
-        v[r][0] = bf16_lo(a.x);
-        v[r][1] = bf16_hi(a.x);
-        v[r][2] = bf16_lo(a.y);
-        v[r][3] = bf16_hi(a.y);
+        raw[r][0] = a.x;
+        raw[r][1] = a.y;
       } else {
-        const float4 a = __ldg(reinterpret_cast<const float4*>(src));
-        v[r][0] = a.x;
-        v[r][1] = a.y;
-        v[r][2] = a.z;
-        v[r][3] = a.w;
+        const uint4 a = __ldg(reinterpret_cast<const uint4*>(src));
+        raw[r][0] = a.x;
+        raw[r][1] = a.y;
+        raw[r][2] = a.z;
+        raw[r][3] = a.w;
       }
-    } else {
+    }
+#pragma unroll
+    for (int r = 0; r < 16; ++r)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        v[r][i] = sizeof(T) == 4 ? __uint_as_float(raw[r][i]) : i & 1 ? bf16_hi(raw[r][i >> 1]) : bf16_lo(raw[r][i >> 1]);
+  } else {
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+      const int n = n0 + 8 * r;
+      const T* src = w + (int64_t)n * ld_w + k0;
 #pragma unroll
       for (int i = 0; i < 4; ++i) v[r][i] = n < N && k0 + i < K ? load1(src + i) : 0.f;
     }
@@ -219,6 +264,16 @@ __global__ void __launch_bounds__(256) blocks_kernel(const T* __restrict__ w, in
   if (threadIdx.x == 0) s[(int64_t)blockIdx.y * gridDim.x + blockIdx.x] = scale;
 }
 
+// CTAs of 256 threads of this kernel that one SM holds, asked once.
+template <class K>
+int per_sm(K kernel, std::atomic<int>& known) {
+  int n = known.load(std::memory_order_relaxed);
+  if (n > 0) return n;
+  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, 256, 0) != cudaSuccess || n < 1) return 1;
+  known.store(n, std::memory_order_relaxed);
+  return n;
+}
+
 template <typename T>
 int rows(const T* x, int64_t ld_x, int R, int K, uint8_t* q, int64_t ld_q, float* s, int64_t s_row, int64_t s_grp,
          cudaStream_t st) {
@@ -226,11 +281,13 @@ int rows(const T* x, int64_t ld_x, int R, int K, uint8_t* q, int64_t ld_q, float
   if (nsm <= 0) return MOE_ERR_CUDA;
   const int ngrp = (K + G - 1) / G;
   const bool vec = reinterpret_cast<uintptr_t>(x) % 16 == 0 && (ld_x * (int64_t)sizeof(T)) % 16 == 0;
-  constexpr int U = 4;
   const int64_t warps = (int64_t)R * ((ngrp + 3) / 4);  // both kernels give a warp four groups
-  const int grid = (int)std::min<int64_t>((warps + 7) / 8, (int64_t)nsm * 8);
+  if (warps >= (1ll << 31)) return MOE_ERR_UNSUPPORTED_SHAPE;
+  static std::atomic<int> vec_per_sm, any_per_sm;
+  const int fit = vec ? per_sm(rows_vec_kernel<T>, vec_per_sm) : per_sm(rows_any_kernel<T, 4>, any_per_sm);
+  const int grid = (int)std::min<int64_t>((warps + 7) / 8, (int64_t)nsm * fit);
   return vec ? launch_pdl(rows_vec_kernel<T>, dim3(grid), dim3(256), 0, st, x, ld_x, R, K, q, ld_q, s, s_row, s_grp)
-             : launch_pdl(rows_any_kernel<T, U>, dim3(grid), dim3(256), 0, st, x, ld_x, R, K, q, ld_q, s, s_row, s_grp);
+             : launch_pdl(rows_any_kernel<T, 4>, dim3(grid), dim3(256), 0, st, x, ld_x, R, K, q, ld_q, s, s_row, s_grp);
 }
 
 template <typename T>

@@ -312,6 +312,35 @@ def test_grouped_gemm(name, n, k, gather):
         assert (out[live:] == 5).all()  # rows past the last offset are not touched
 
 
+PAIRS = [700, 300, 0, 129, 513, 1]  # 256-row tiles: whole, with an empty second half, with one row in it
+
+
+@pytest.mark.parametrize("gather", [False, True], ids=["sorted", "gathered"])
+@pytest.mark.parametrize("n,k", [(2300, 272), (2056, 1000)])
+def test_grouped_gemm_cta_pairs(n, k, gather):
+    """Enough rows per expert and tiles for the CTA-pair tiles of 256 rows."""
+    c = grouped_case(PAIRS, n, k, gather, n, 3)
+    for dt in (torch.bfloat16, torch.float32):
+        out = torch.full((c["slots"], (n + 7) // 8 * 8), 5.0, dtype=dt, device="cuda")[:, :n]
+        moe.moe_fp8_grouped_gemm(c["a"], c["sa"], c["w"], c["sw"], c["offsets"], c["slots"], gather_ids=c["ids"], out=out,
+                                 c_dtype=dt)
+        live = sum(PAIRS)
+        ref, mags = grouped64(c)
+        assert_product(out[:live], ref[:live], mags[:live], k)
+        assert (out[live:] == 5).all()
+
+
+@pytest.mark.parametrize("gather", [False, True], ids=["sorted", "gathered"])
+@pytest.mark.parametrize("inter,k", [(1024, 400), (1152, 129)])
+def test_swiglu_cta_pairs(inter, k, gather):
+    c = grouped_case(PAIRS, 2 * inter, k, gather, inter + k)
+    q, s = moe.moe_fp8_grouped_gemm_swiglu(c["a"], c["sa"], c["w"], c["sw"], c["offsets"], c["slots"], limit=0.75,
+                                           gather_ids=c["ids"])
+    ref, mags = grouped64(c)
+    act, tol = swiglu64(ref, mags, k, 0.75)
+    assert_quantised(q, s, act, tol)
+
+
 def swiglu64(ref, mags, k, limit):
     inter = ref.shape[1] // 2
     g, u = ref[:, :inter], ref[:, inter:]
