@@ -146,48 +146,94 @@ __global__ void __launch_bounds__(256) rows_vec_kernel(const T* __restrict__ x, 
   }
 }
 
-// Rows of any alignment, 4 consecutive elements to a lane and a warp to a group; U groups of a row in
-// flight per warp.  Codes are stored as words (q is 16-byte aligned with ld_q a multiple of 16).
-template <typename T, int U>
+// Rows of any alignment, 4 consecutive elements to a lane and a warp to a group: four groups of a row at a
+// time, the next four on their way meanwhile.  Codes are stored as words (q is 16-byte aligned with ld_q
+// a multiple of 16); the four groups' scales are worked out by a lane each.
+//
+// The lane's elements are loaded by words: a BF16 row that starts inside one has them in three, of which
+// the second half of the last is the row's next element (none is read past the row: `whole`).
+template <typename T>
+struct Words {
+  static constexpr int N = sizeof(T) == 2 ? 3 : 4;
+  uint32_t w[4][N];
+};
+
+template <typename T>
 __global__ void __launch_bounds__(256) rows_any_kernel(const T* __restrict__ x, int64_t ld_x, int R, int K, uint8_t* q,
                                                        int64_t ld_q, float* s, int64_t s_row, int64_t s_grp) {
   griddep_wait();
   griddep_launch_dependents();
   const int lane = threadIdx.x & 31;
   const int ngrp = (K + G - 1) / G;
-  for (Walk at(gridDim.x * 8, blockIdx.x * 8 + (threadIdx.x >> 5), (ngrp + U - 1) / U); at.row < (uint32_t)R; at.next()) {
-    const int64_t row = at.row;
-    const int g0 = (int)at.piece * U;
-    const T* src = x + row * ld_x;
-    float v[U][4];
+  auto column = [&](const Walk& at, int u) { return ((int)at.piece * 4 + u) * G + lane * 4; };
+  auto odd = [&](const Walk& at) {
+    return sizeof(T) == 2 ? (int)((reinterpret_cast<uintptr_t>(x + at.row * ld_x) >> 1) & 1) : 0;
+  };
+  auto load = [&](const Walk& at, Words<T>& r) {
+    const int o = odd(at);
 #pragma unroll
-    for (int u = 0; u < U; ++u)
+    for (int u = 0; u < 4; ++u) {
+      const int k = column(at, u);
+      const bool whole = at.row < (uint32_t)R && k + 4 + o <= K;
+      const uint32_t* p = reinterpret_cast<const uint32_t*>(x + at.row * ld_x + k - o);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int k = (g0 + u) * G + lane * 4 + i;
-        v[u][i] = k < K ? load1(src + k) : 0.f;
+      for (int i = 0; i < Words<T>::N; ++i)
+        r.w[u][i] = whole && (sizeof(T) == 4 || i < 2 || o) ? __ldg(p + i) : 0;
+    }
+  };
+  Walk at(gridDim.x * 8, blockIdx.x * 8 + (threadIdx.x >> 5), (ngrp + 3) / 4);
+  Words<T> cur, nxt;
+  load(at, cur);
+  while (at.row < (uint32_t)R) {
+    Walk then = at;
+    then.next();
+    load(then, nxt);
+    const int o = odd(at);
+    float v[4][4];
+    uint32_t mine = 0;  // of group lane % 4
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int k = column(at, u);
+      if (k + 4 + o <= K) {
+        if constexpr (sizeof(T) == 2) {
+          const uint32_t lo = o ? __funnelshift_r(cur.w[u][0], cur.w[u][1], 16) : cur.w[u][0];
+          const uint32_t hi = o ? __funnelshift_r(cur.w[u][1], cur.w[u][2], 16) : cur.w[u][1];
+          v[u][0] = bf16_lo(lo);
+          v[u][1] = bf16_hi(lo);
+          v[u][2] = bf16_lo(hi);
+          v[u][3] = bf16_hi(hi);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[u][i] = __uint_as_float(cur.w[u][i]);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[u][i] = k + i < K ? load1(x + at.row * ld_x + k + i) : 0.f;
       }
+      const uint32_t m = __reduce_max_sync(
+          0xffffffffu, max(max(abs_bits(v[u][0]), abs_bits(v[u][1])), max(abs_bits(v[u][2]), abs_bits(v[u][3]))));
+      if ((lane & 3) == u) mine = m;
+    }
+    float scale, inv4;
+    fp8_scale(mine, scale, inv4);
+    const int grp = (int)at.piece * 4 + lane;
+    if (lane < 4 && grp < ngrp) s[at.row * s_row + grp * s_grp] = scale;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (g0 + u >= ngrp) break;
-      uint32_t m = 0;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) m = max(m, abs_bits(v[u][i]));
-      m = __reduce_max_sync(0xffffffffu, m);
-      float scale, inv;
-      fp8_scale(m, scale, inv);
-      const uint32_t w = pack_e4m3x4(v[u][0] * inv, v[u][1] * inv, v[u][2] * inv, v[u][3] * inv);
-      const int k0 = (g0 + u) * G + lane * 4;
-      uint8_t* dst = q + row * ld_q + k0;
-      if (k0 + 4 <= K) {
-        *reinterpret_cast<uint32_t*>(dst) = w;
+    for (int u = 0; u < 4; ++u) {
+      const float inv = __shfl_sync(0xffffffffu, inv4, u);
+      const uint32_t c = pack_e4m3x4(v[u][0] * inv, v[u][1] * inv, v[u][2] * inv, v[u][3] * inv);
+      const int k = column(at, u);
+      uint8_t* dst = q + at.row * ld_q + k;
+      if (k + 4 <= K) {
+        *reinterpret_cast<uint32_t*>(dst) = c;
       } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          if (k0 + i < K) dst[i] = (uint8_t)(w >> (8 * i));
+          if (k + i < K) dst[i] = (uint8_t)(c >> (8 * i));
       }
-      if (lane == 0) s[row * s_row + (g0 + u) * s_grp] = scale;
     }
+    at = then;
+    cur = nxt;
   }
 }
 
@@ -284,10 +330,10 @@ int rows(const T* x, int64_t ld_x, int R, int K, uint8_t* q, int64_t ld_q, float
   const int64_t warps = (int64_t)R * ((ngrp + 3) / 4);  // both kernels give a warp four groups
   if (warps >= (1ll << 31)) return MOE_ERR_UNSUPPORTED_SHAPE;
   static std::atomic<int> vec_per_sm, any_per_sm;
-  const int fit = vec ? per_sm(rows_vec_kernel<T>, vec_per_sm) : per_sm(rows_any_kernel<T, 4>, any_per_sm);
+  const int fit = vec ? per_sm(rows_vec_kernel<T>, vec_per_sm) : per_sm(rows_any_kernel<T>, any_per_sm);
   const int grid = (int)std::min<int64_t>((warps + 7) / 8, (int64_t)nsm * fit);
   return vec ? launch_pdl(rows_vec_kernel<T>, dim3(grid), dim3(256), 0, st, x, ld_x, R, K, q, ld_q, s, s_row, s_grp)
-             : launch_pdl(rows_any_kernel<T, 4>, dim3(grid), dim3(256), 0, st, x, ld_x, R, K, q, ld_q, s, s_row, s_grp);
+             : launch_pdl(rows_any_kernel<T>, dim3(grid), dim3(256), 0, st, x, ld_x, R, K, q, ld_q, s, s_row, s_grp);
 }
 
 template <typename T>
