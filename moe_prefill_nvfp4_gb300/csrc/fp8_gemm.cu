@@ -10,12 +10,22 @@
 // tensor memory.  Sums stay in FP32 throughout; one rounding makes the BF16 output.
 //
 // Two kernels:
-//   wide  token rows are the MMA's M operand (128 per tile, a TMEM lane and an epilogue thread to a
-//         row: its sa is one register), weight rows the N operand (NB blocks of 128, sw uniform
-//         over a block).  Persistent CTAs over all experts' tiles.
+//   wide  token rows are the MMA's M operand (128 per tile, a TMEM lane and two epilogue threads to a
+//         row: its sa is one number), weight rows the N operand (NB blocks of 128, sw uniform over a
+//         block).  Persistent CTAs over all experts' tiles.  Bound by shared memory: a k block of a
+//         128 x 256 tile is 512 cycles of MMA, and 768 of writing its 48 KB there and reading them
+//         back; it takes ~850 (434 ns), 2.9 of the 3.8 PFLOP/s that a library product with one scale
+//         to a tensor reaches.  (CTA pairs, whose tiles need 32 KB to an SM, measured slower: with 256
+//         columns to an accumulator a k block waits for its release across the pair, 19456 x 1536 x
+//         5120 in 123 us against 115; four accumulators of 128 columns take 144.)
 //   few   weight rows are the M operand (two blocks of 128 per tile), up to NT token rows the N
-//         operand: a tile of the wide kernel would be mostly empty rows.  The k blocks of a tile are
-//         split over a cluster whose partial sums meet in shared memory.
+//         operand: a tile of the wide kernel would be mostly empty rows.  Bound by the weights' bytes.
+//
+// Measured on GB300 (GLM sizes: 160 experts, top-8, hidden 5120, intermediate 1536), cold weights:
+//   down product      1 token 14.8 us, 64 tokens 182 us (6.6 TB/s), 8192 tokens 576 us (1.8 PFLOP/s)
+//   gate/up + SwiGLU  4 tokens 80 us, 64 tokens 351 us (6.9 TB/s), 8192 tokens 1172 us (1.8 PFLOP/s; with
+//                     rows that need no gathering 1060)
+//   dense             8192 x 1536 x 5120 59 us (2.2 PFLOP/s), 1 x 5120 x 1536 5.8 us
 //
 // gate/up form: the tile's two blocks are a gate block and the matching up block, and the tile's
 // output is a 128-column group of act = silu(min(g, L)) * clamp(u, -L, L), quantised in the
@@ -347,12 +357,11 @@ struct WideCfg {
   static_assert(SMEM > 232448 / 2 && SMEM <= 232448, "one CTA per SM (it takes all of TMEM)");
 };
 
-// Warp roles: 0 TMA producer, 1 MMA issuer and TMEM owner, 2 the scales of each
-// k block into shared memory (asynchronously and blocks ahead, across tiles too: epilogue threads that
-// loaded their own scales waited for L2 in every block), 4-11 epilogue, 12-15 gathered
-// token rows.  (Epilogue: two warpgroups; warp w
-// reads TMEM lanes 32 (w % 4).., warpgroup g the columns 64 g .. 64 g + 63 of each weight block, so
-// that in the gate/up form a thread holds a gate column and its up column).
+// Warp roles: 0 TMA producer, 1 MMA issuer and TMEM owner, 2 the scales of each k block into shared memory
+// (asynchronously and blocks ahead, across tiles too: epilogue threads that loaded their own scales waited
+// for L2 in every block, 8192 x 1536 x 5120 in 87 us against 60), 4-11 epilogue, 12-15 gathered token rows.
+// Epilogue: warp w reads TMEM lanes 32 (w % 4).., its warpgroup g the columns 64 g .. 64 g + 63 of each
+// weight block, so that in the gate/up form a thread holds gate columns and their up columns.
 template <class C>
 __global__ void __launch_bounds__(C::THREADS, 1)
     wide_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap wmap,
@@ -440,8 +449,11 @@ __global__ void __launch_bounds__(C::THREADS, 1)
               tma_load_3d(st + BLK + h * BLK, &wmap, kb * BK, block_row<NB>(args, t.ng, h), t.e, full(s));
           }
         }
-        if (!ok)  // every copy issued lands before the CTA leaves
-          for (int j = max(0, i - NS); j < i; ++j) mbar_wait_drain(full(j % NS), (j / NS) & 1);
+        // every copy issued lands before the CTA leaves (a stage that misses other arrivals, of gathering
+        // threads that gave up too, is waited for until the limit, by which its copies have landed)
+        if (!ok)
+          for (int j = max(0, i - NS); j < i; ++j)
+            if (!mbar_wait_drain(full(j % NS), (j / NS) & 1)) break;
       }
     } else if (warp == 1) {
       // ---------------------------------------------------------------- MMA issuer
@@ -526,9 +538,9 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   } else if (GATHER && warp >= 12) {
     // ------------------------------------------------------------------ gathered token rows
     // 16-byte cp.async into the swizzled layout (chunk c of row r at c ^ (r % 8)): 8 lanes to a row of
-    // the k block, 4 rows to an instruction, every fourth group of 4 rows to a warp.  (TMA gather4
-    // moved ~12 bytes per cycle and SM where a tile takes ~20.)  Sixteens of rows past the tile's are left as
-    // they are (their accumulator rows are not stored), single rows repeat its last.
+    // the k block, 4 rows to an instruction, every fourth group of 4 rows to a warp (gate/up of 2048 tokens at
+    // 40 experts 298 us; rows gathered by TMA gather4 689, rows that need no gathering 270).  Sixteens of rows
+    // past the tile's are left as they are (their accumulator rows are not stored), single rows repeat its last.
     reg_dec<C::REG_LOW>();
     const int r0 = (warp - 12) * 4 + (lane >> 3);  // rows r0 + 16 j: the same chunk place in all of them
     const int chunk = lane & 7;
@@ -730,9 +742,11 @@ __global__ void __launch_bounds__(C::THREADS, 1)
 // ------------------------------------------------------------------------------------------------
 // few-row kernel
 //
-// Bound by the weights it streams.  Persistent, with loads under way across tiles.  One SM draws 77 GB/s
-// from DRAM at most (44.7 is its share when all of them do), so it pays to have every tile's CTA resident
-// at once: two CTAs to an SM where their stages fit, k split over a cluster where tiles are few.
+// Bound by the weights it streams.  Persistent, with loads under way across tiles: CTAs of one tile each
+// spent ~4 us on their start and end (64 tokens' down product 195 us, persistent 178).  One SM draws 77 GB/s
+// from DRAM at most (44.7 is its share when all of them do), so it pays to have every tile's CTA resident at
+// once: two CTAs to an SM where their stages fit (192 tiles: 41 us; one CTA with twice the stages 49), k
+// split over a cluster where tiles are few.
 
 template <int NT_, int NS_, int PER_SM_>
 struct FewCfg {
@@ -742,7 +756,7 @@ struct FewCfg {
   static constexpr int THREADS = 224;
   static constexpr int STAGE = 2 * BLK + NT * BK;
   // accumulators: a k block of a tile is little work for the MMA and the epilogue, most of its way through
-  // both is latency, which eight on their way hide (with two, one SM could draw 77 GB/s of the 140 or so)
+  // both is latency, which eight on their way hide (3% less time than with two)
   static constexpr int ND = 8;
   static constexpr int TMEM_COLS = ND * 2 * NT;
   static constexpr int PART = NT * 256 * 4;  // a tile's partial sums [NT][256] of a cluster, over the drained stages
@@ -765,9 +779,8 @@ struct FewCfg {
 
 // Warp roles: 0 TMA producer, 1 MMA issuer and TMEM owner, 2-5 epilogue (TMEM lanes 32 (w % 4)..), 6 the
 // scales of each k block, as in the wide kernel.
-// Persistent; CTAs that are a cluster of their own take tiles g, g + CTAs, ...  A cluster of S > 1 has one
-// tile, with the partial sums in shared memory when the last k block is done: CTA
-// `rank` takes its k blocks KB rank / S .. KB (rank + 1) / S.
+// CTAs that are a cluster of their own take tiles g, g + CTAs, ...  A cluster of S > 1 CTAs has one tile:
+// CTA `rank` takes its k blocks KB rank / S .. KB (rank + 1) / S, and the partial sums meet in shared memory.
 template <class C, bool GATHER>
 __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
     few_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap wmap,
@@ -1184,7 +1197,9 @@ int launch_few(const Fp8Gemm& d, int64_t tiles, cudaStream_t st) {
   if (rc != MOE_OK) return rc;
   static std::atomic<int> configured[64];
   if ((rc = configure(few_kernel<C, GATHER>, C::SMEM, configured)) != MOE_OK) return rc;
-  // Split k as far as every CTA is still resident at once and keeps two k blocks.
+  // Split k as far as every CTA is still resident at once and keeps two k blocks (one token's gate/up at 64
+  // experts, 48 tiles: 10.6 us with one CTA to a tile, 8.2 with four; clusters that share several tiles in
+  // turn wait for each other's sums at every one, 64 tokens' down product 269 us against 182).
   const int KB = (d.args.K + BK - 1) / BK;
   int S = 1;
   for (int t = 2; t <= 8 && 2 * t <= KB; ++t)
@@ -1205,15 +1220,22 @@ template <bool GATHER>
 int launch(const Fp8Gemm& d, cudaStream_t st) {
   const Fp8GemmArgs& a = d.args;
   const int groups = a.offsets == nullptr ? 1 : std::min(a.E, a.R);
-  const double rows = (double)a.R / groups;  // per expert
+  const double rows = (double)a.R / groups;  // per expert, on average
   const int64_t ng2 = a.half ? a.half / 128 : (a.N + 255) / 256;
   const int64_t tt = token_tiles(d, 128);
   const int64_t wide_tiles = a.half ? tt * ng2 : tt * ((a.N + 127) / 128);
+  // Few rows per expert: the few-row kernel up to 16 (gate/up of 128 tokens at 64 experts, 16 rows: 40.0 us
+  // against the wide kernel's 45.9; of 512 tokens at 160 experts, 26 rows: 440 against 398).  Busier experts
+  // among them take several of its tiles, each reading the weights again from L2.  And where the wide
+  // kernel's tiles, which do not split k, would leave half of the SMs idle (64 x 1536 x 5120: 8.2 us against
+  // 16.4; 256 rows 13.3 against 16.8).  32 token rows to a tile from 49 rows on (64 rows: 8.2 us against 8.7
+  // with 16; 32 rows: 8.0 against 7.0).
   if (rows <= 16 || (rows <= 256 && 2 * wide_tiles <= device_sm_count())) {
     if (rows <= 48) return launch_few<FewCfg<16, 3, 2>, GATHER>(d, token_tiles(d, 16) * ng2, st);
     return launch_few<FewCfg<32, 5, 1>, GATHER>(d, token_tiles(d, 32) * ng2, st);
   }
   if (a.half) return launch_wide<WideCfg<2, GATHER, true>>(d, tt * ng2, st);
+  // 128 weight rows to a tile where tiles of 256 would not fill the SMs
   if (tt * ng2 < device_sm_count()) return launch_wide<WideCfg<1, GATHER, false>>(d, tt * ((a.N + 127) / 128), st);
   return launch_wide<WideCfg<2, GATHER, false>>(d, tt * ng2, st);
 }

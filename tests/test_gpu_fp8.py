@@ -483,3 +483,40 @@ def test_streams_and_graph():
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(got, want)
+
+
+def test_offsets_past_32_bits():
+    """Codes, scales and outputs whose last elements lie past 2^32 bytes and 2^31 elements."""
+    rows, ld, k, n = 900_000, 5120, 256, 136
+    flat = torch.zeros(rows * ld, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn).view(rows, ld)
+    a = flat[:, ld - k:]
+    x = rand((rows, k), 40)
+    sa = torch.zeros(rows, 2600, device="cuda")[:, 2598:]
+    moe.moe_fp8_quantize_rows(x, out=a, scales=sa)
+    w, sw = weights(2, n, k, 41)
+    some = [0, 1, 127, 128, 450_000, rows - 129, rows - 2, rows - 1]
+    ids = torch.tensor(some, dtype=torch.int32, device="cuda")
+    ref = torch.cat([product64(dequant_rows64(a[i:i + 1], sa[i:i + 1]), dequant_blocks64(w[0], sw[0]))[0] for i in some])
+    mags = torch.cat([product64(dequant_rows64(a[i:i + 1], sa[i:i + 1]), dequant_blocks64(w[0], sw[0]))[1] for i in some])
+    for reps in (1, 20):  # few rows (TMA gather) and many (cp.async)
+        got = moe.moe_fp8_grouped_gemm(a, sa, w, sw, offsets_of([8 * reps, 0]), 8 * reps, gather_ids=ids.repeat(reps),
+                                       c_dtype=torch.float32)
+        assert_product(got, ref.repeat(reps, 1), mags.repeat(reps, 1), k)
+    out = torch.zeros(rows, 2560, dtype=torch.bfloat16, device="cuda")[:, :n]
+    got = moe.moe_fp8_gemm(a, sa, w[0], sw[0], out=out)
+    assert_product(got[ids.long()], ref, mags, k)
+
+
+@pytest.mark.parametrize("first_stride", [1, 0])
+def test_activation_scales_of_any_layout(first_stride):
+    """Row-major, group-major and one scale per group shared by all rows (stride 0)."""
+    r, n, k = 150, 260, 512
+    a, sa = moe.moe_fp8_quantize_rows(rand((r, k), 50))
+    w, sw = moe.moe_fp8_quantize_blocks(rand((n, k), 51))
+    if first_stride == 0:
+        sa = sa[:1].expand(r, 4)
+    else:
+        sa = sa.contiguous()
+    for rows in (5, r):
+        ref, mags = product64(dequant_rows64(a[:rows], sa[:rows]), dequant_blocks64(w, sw))
+        assert_product(moe.moe_fp8_gemm(a[:rows], sa[:rows], w, sw, c_dtype=torch.float32), ref, mags, k)
