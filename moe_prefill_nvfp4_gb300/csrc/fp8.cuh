@@ -27,13 +27,28 @@ MOE_DEV uint32_t pack_e4m3x4(float a, float b, float c, float d) {
   return out;
 }
 
-// silu(min(g, L)) * clamp(u, -L, L) of FP32 sums, NaN kept (fminf and fmaxf would drop it).  The
-// exponential and the division are the hardware approximations (a few FP32 ulp); for g -> -inf the
-// denominator overflows and the quotient is -0, the limit of silu.
+// Minimum and maximum that keep a NaN (fminf and fmaxf drop it), one instruction each.
+MOE_DEV float min_nan(float a, float b) {
+  float d;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+MOE_DEV float max_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+
+// silu(min(g, L)) * clamp(u, -L, L) of FP32 sums, NaN kept.  silu(z) = z / (1 + 2^(-z log2 e)) with the
+// hardware's approximate power of two and reciprocal (2^-22 and 2^-23 relative): the result is rounded to
+// four bits.  For z -> -inf the power overflows, its reciprocal is 0 and the product -0, the limit of silu.
 MOE_DEV float swiglu_keep_nan(float g, float u, float L) {
-  const float gm = g > L ? L : g;
-  const float uc = u > L ? L : (u < -L ? -L : u);
-  return __fdividef(gm, 1.0f + __expf(-gm)) * uc;
+  const float gm = min_nan(g, L);
+  const float uc = max_nan(min_nan(u, L), -L);
+  float e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(gm * -1.44269504f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+  return gm * r * uc;
 }
 
 // Load from the shared memory of CTA `rank` of the cluster, at the offset of local_addr in ours.

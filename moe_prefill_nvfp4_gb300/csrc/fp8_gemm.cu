@@ -645,7 +645,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       if constexpr (C::GATE_UP) {
         const bool live = row < t.cnt;
         // gate (block 0) and up (block 1) columns 64 wg .. of the act group
-        uint32_t m = 0;
+        float high = 0.f;
 #pragma unroll
         for (int j = 0; j < 32; ++j) {
           float g0, g1, u0, u1;
@@ -653,14 +653,16 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           unpack_f32x2(acc[NB - 1][j], u0, u1);
           g0 = swiglu_keep_nan(g0, u0, args.limit);
           g1 = swiglu_keep_nan(g1, u1, args.limit);
-          m = max(m, max(__float_as_uint(g0) & 0x7FFFFFFFu, __float_as_uint(g1) & 0x7FFFFFFFu));
+          high = max_nan(high, max_nan(fabsf(g0), fabsf(g1)));
           acc[0][j] = pack_f32x2(g0, g1);
         }
+        uint32_t m = __float_as_uint(high);
         s_amax[wg * 128 + row] = m;
         named_bar_sync(1, 256);
         m = max(m, s_amax[(wg ^ 1) * 128 + row]);  // (the next tile's write comes after its first barrier)
         float scale, inv;
         fp8_scale(m, scale, inv);
+        const uint64_t inv2 = pack_f32x2(inv, inv);
         uint8_t* dst = args.q + (int64_t)(t.p0 + row) * args.ld_q + t.ng * 128 + wg * 64;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
@@ -668,9 +670,9 @@ __global__ void __launch_bounds__(C::THREADS, 1)
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             float a0, a1, a2, a3;
-            unpack_f32x2(acc[0][c * 8 + 2 * j], a0, a1);
-            unpack_f32x2(acc[0][c * 8 + 2 * j + 1], a2, a3);
-            w[j] = pack_e4m3x4(a0 * inv, a1 * inv, a2 * inv, a3 * inv);
+            unpack_f32x2(mul_f32x2(acc[0][c * 8 + 2 * j], inv2), a0, a1);
+            unpack_f32x2(mul_f32x2(acc[0][c * 8 + 2 * j + 1], inv2), a2, a3);
+            w[j] = pack_e4m3x4(a0, a1, a2, a3);
           }
           if (live) *reinterpret_cast<uint4*>(dst + c * 16) = make_uint4(w[0], w[1], w[2], w[3]);
         }
