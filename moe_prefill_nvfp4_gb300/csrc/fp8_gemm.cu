@@ -335,7 +335,7 @@ struct WideCfg {
   // 7.3 us that a tile of K = 1536 took, the fourth stage is worth 1-2%.
   static constexpr int NS = NB == 1 ? 5 : GATE_UP ? 4 : 3;
   static constexpr int TMEM_COLS = 2 * BN;
-  static constexpr int EPI_WARP = GATE_UP ? 0 : NB * 4096;     // NB boxes of 32 rows x 128 bytes
+  static constexpr int EPI_WARP = GATE_UP ? 2048 : NB * 4096;  // 32 rows x 64 bytes; NB boxes of 32 x 128
   static constexpr int OFF_EPI = NS * STAGE;
   static constexpr int OFF_AMAX = OFF_EPI + 8 * EPI_WARP;      // uint32 [2][128]
   static constexpr int NF = 4;              // k blocks whose scales are held
@@ -663,7 +663,14 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         float scale, inv;
         fp8_scale(m, scale, inv);
         const uint64_t inv2 = pack_f32x2(inv, inv);
-        uint8_t* dst = args.q + (int64_t)(t.p0 + row) * args.ld_q + t.ng * 128 + wg * 64;
+        // This row's 64 codes: a warp's 32 rows leave together through its staging box (16-byte chunk c of
+        // row r at c ^ ((r >> 1) % 4), the 64-byte swizzle), rows where the tile ends each by itself.
+        const int nrow = t.cnt - q * 32, col = t.ng * 128 + wg * 64;
+        if (nrow >= 32) {
+          if (lane == 0) bulk_wait_read();  // the last box has left
+          __syncwarp();
+        }
+        uint8_t* dst = args.q + (int64_t)(t.p0 + row) * args.ld_q + col;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           uint32_t w[4];
@@ -674,7 +681,22 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             unpack_f32x2(mul_f32x2(acc[0][c * 8 + 2 * j + 1], inv2), a2, a3);
             w[j] = pack_e4m3x4(a0, a1, a2, a3);
           }
-          if (live) *reinterpret_cast<uint4*>(dst + c * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+          if (nrow >= 32)
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(stg + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4)),
+                         "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
+                         : "memory");
+          else if (live)
+            *reinterpret_cast<uint4*>(dst + c * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        if (nrow >= 32) {
+          fence_proxy_async_shared();
+          __syncwarp();
+          if (lane == 0) {
+            asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(&cmap),
+                         "r"(col), "r"(t.p0 + q * 32), "r"(stg)
+                         : "memory");
+            bulk_commit();
+          }
         }
         if (live && wg == 0) args.s[(int64_t)(t.p0 + row) * args.s_row + t.ng * args.s_grp] = scale;
       } else {
@@ -730,7 +752,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         }
       }
     }
-    if (!C::GATE_UP && lane == 0) bulk_wait();
+    if (lane == 0) bulk_wait();
   }
 
   tc_fence_before();
@@ -1141,9 +1163,16 @@ int w_map(CUtensorMap* m, const Fp8Gemm& d) {
                      CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-// stores of 32-row boxes, 128 bytes wide
+// stores of 32-row boxes, 128 bytes wide (the gate/up form's codes: 64)
 int c_map(CUtensorMap* m, const Fp8Gemm& d) {
   const Fp8GemmArgs& a = d.args;
+  if (a.half) {
+    const cuuint64_t dims[2] = {(cuuint64_t)a.half, (cuuint64_t)a.R};
+    const cuuint64_t strides[1] = {(cuuint64_t)a.ld_q};
+    const cuuint32_t box[2] = {64, 32};
+    const cuuint32_t estr[2] = {1, 1};
+    return encode_tmap(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, a.q, dims, strides, box, estr, CU_TENSOR_MAP_SWIZZLE_64B);
+  }
   const bool bf16 = a.c_dtype == MOE_DTYPE_BF16;
   const cuuint64_t dims[2] = {(cuuint64_t)a.N, (cuuint64_t)a.R};
   const cuuint64_t strides[1] = {(cuuint64_t)a.ldc * (bf16 ? 2 : 4)};
@@ -1158,7 +1187,7 @@ int launch_wide(const Fp8Gemm& d, int64_t tiles, cudaStream_t st) {
   CUtensorMap am, wm, cm = {};
   int rc = a_map(&am, d, 128);
   if (rc == MOE_OK) rc = w_map(&wm, d);
-  if (rc == MOE_OK && !C::GATE_UP) rc = c_map(&cm, d);
+  if (rc == MOE_OK) rc = c_map(&cm, d);
   if (rc != MOE_OK) return rc;
   static std::atomic<int> configured[64];
   if ((rc = configure(wide_kernel<C>, C::SMEM, configured)) != MOE_OK) return rc;
