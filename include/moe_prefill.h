@@ -322,7 +322,7 @@ typedef struct {
 
 /*
  * Rows to codes and scales: for each group of 128 columns of a row, in FP32,
- *   a = max(max |x|, 2^-100),  s = a / 448,  q = e4m3(x * (448 / a))  (round to nearest even).
+ *   a = max(max |x|, 2^-100),  s = a / 448,  q = e4m3(x * (448 * (1 / a)))  (round to nearest even).
  * A group of zeros gives codes 0; a group holding an infinity or a NaN gives s = NaN and NaN codes.
  *   x     device BF16 or FP32 (x_dtype) [R, ld_x], ld_x >= K; any alignment of its element type
  *         (rows on 16-byte boundaries are read with wide loads)

@@ -8,13 +8,14 @@ namespace moe {
 constexpr uint32_t kFp8AmaxFloorBits = 0x0D800000u;  // 2^-100
 
 // Scale and its reciprocal of a group whose largest magnitude has the bits amax_bits (inf and NaN
-// compare above every number): a = max(amax, 2^-100), scale = a / 448, inv = 448 / a; both NaN
-// for a group with a value that is not finite.
+// compare above every number): a = max(amax, 2^-100), scale = a / 448, inv = 448 (1 / a), the form in which
+// PyTorch evaluates 448 / a, so that its codes are these; both NaN for a group with a value that is not
+// finite.
 MOE_DEV void fp8_scale(uint32_t amax_bits, float& scale, float& inv) {
   const bool finite = amax_bits < 0x7F800000u;
   const float a = __uint_as_float(finite ? max(amax_bits, kFp8AmaxFloorBits) : 0x7FC00000u);
   scale = __fdiv_rn(a, 448.0f);
-  inv = __fdiv_rn(448.0f, a);
+  inv = 448.0f * __frcp_rn(a);
 }
 
 // Four floats to E4M3 codes, round to nearest even, a in the low byte.

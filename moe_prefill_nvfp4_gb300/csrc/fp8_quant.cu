@@ -1,11 +1,11 @@
 // fp8_quant.cu -- quantisation to E4M3 with one FP32 scale per 128 elements of a row (activations)
 // or per 128 x 128 block (weights): the operands of the FP8 products.
 //
-//   a = max(max |x| over the group, 2^-100),  s = a / 448,  q = e4m3(x * (448 / a))
+//   a = max(max |x| over the group, 2^-100),  s = a / 448,  q = e4m3(x * (448 * (1 / a)))
 //
-// in FP32 with correctly rounded division and multiplication; q rounds to nearest even (x * 448/a
-// is at most 448 (1 + 2^-23), which rounds to 448, so nothing saturates).  The floor of a keeps
-// 448 / a and s normal FP32 numbers; a group of zeros gives q = 0.  A group with an infinity or a
+// in FP32, each operation correctly rounded; q rounds to nearest even (the product is at most
+// 448 (1 + 2^-22), which rounds to 448, so nothing saturates).  The floor of a keeps 448 / a and s
+// normal FP32 numbers; a group of zeros gives q = 0.  A group with an infinity or a
 // NaN gives s = NaN and codes NaN: whatever reads it is NaN, no finite value stands for it.
 //
 // Bound by memory: each element is read once (held in registers between the maximum and the

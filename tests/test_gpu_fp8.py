@@ -1,7 +1,8 @@
 """GPU tests of the FP8 (E4M3, one FP32 scale per 128 columns / 128 x 128 block) quantisers and products
 against plain FP64 forms.
 
-Quantisers: bit for bit against numpy's FP32 division and product and torch's CPU cast.
+Quantisers: bit for bit against numpy's FP32 divisions and products and torch's CPU cast, and the codes
+against the same expression in torch on the GPU.
 
 Products: the codes' products are exact in FP32 (4-bit significands).  A k block adds 128 of them in
 the MMA, each addition off by at most 2^-23 of the sum of magnitudes (truncation allowed), the product
@@ -51,7 +52,7 @@ def quantize_ref(x: torch.Tensor, rows_per_scale: int):
                 m = np.abs(part).max()
                 m = np.float32(np.nan) if not np.isfinite(m) else max(m, FLOOR)
                 s[i, j] = np.float32(m) / np.float32(448)
-                v = part * (np.float32(448) / np.float32(m))
+                v = part * (np.float32(448) * (np.float32(1) / np.float32(m)))
                 c = torch.from_numpy(v).to(torch.float8_e4m3fn).view(torch.uint8).numpy()
                 q[i * rows_per_scale:(i + 1) * rows_per_scale, j * BLOCK:(j + 1) * BLOCK] = c
     return q, s
@@ -131,6 +132,16 @@ def test_quantize_rows(r, k, dtype):
     assert_codes(codes(q), qr)
     np.testing.assert_array_equal(s.cpu().numpy(), sr)
     assert q.stride(0) % 16 == 0 or r == 1
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_quantize_equals_the_torch_expression(dtype):
+    """Many groups of BF16 values, whose quotients often lie on a tie between two codes."""
+    x = rand((512, 2048), 77, 3.0, dtype)
+    q, _ = moe.moe_fp8_quantize_rows(x)
+    groups = x.float().view(512, 16, BLOCK)
+    want = (groups * (448.0 / groups.abs().amax(-1, keepdim=True))).to(torch.float8_e4m3fn).view(512, 2048)
+    assert torch.equal(q.view(torch.uint8), want.view(torch.uint8))
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
