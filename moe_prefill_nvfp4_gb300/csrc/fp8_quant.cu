@@ -242,7 +242,7 @@ __global__ void __launch_bounds__(256) rows_any_kernel(const T* __restrict__ x, 
 // Weights: a CTA of 256 threads per 128 x 128 block, 64 elements to a thread (lane: 4 consecutive
 // columns; warp w: rows w, w + 8, ...).  VEC: 4-element loads (rows 4-element aligned).
 template <typename T, bool VEC>
-__global__ void __launch_bounds__(256) blocks_kernel(const T* __restrict__ w, int64_t ld_w, int N, int K, uint8_t* q,
+__global__ void __launch_bounds__(256, 3) blocks_kernel(const T* __restrict__ w, int64_t ld_w, int N, int K, uint8_t* q,
                                                      int64_t ld_q, float* s) {
   __shared__ uint32_t s_max[8];
   griddep_wait();
