@@ -40,12 +40,16 @@ MOE_DEV float max_nan(float a, float b) {
   return d;
 }
 
-// silu(min(g, L)) * clamp(u, -L, L) of FP32 sums, NaN kept.  silu(z) = z / (1 + 2^(-z log2 e)) with the
-// hardware's approximate power of two and reciprocal (2^-22 and 2^-23 relative): the result is rounded to
-// four bits.  For z -> -inf the power overflows, its reciprocal is 0 and the product -0, the limit of silu.
+// silu(min(g, L)) * clamp(u, -L, L) of FP32 sums, NaN kept.  silu(z) = z / (1 + e^-z).  FAST: with the
+// hardware's approximate power of two and reciprocal (2^-22 and 2^-23 relative, against 2^-24 of FP32: the
+// result is rounded to four bits, and one in about a million values then to the other neighbour), for
+// kernels in which the accurate forms' instructions count.  For z -> -inf the power overflows and the
+// quotient is -0, the limit of silu.
+template <bool FAST>
 MOE_DEV float swiglu_keep_nan(float g, float u, float L) {
   const float gm = min_nan(g, L);
   const float uc = max_nan(min_nan(u, L), -L);
+  if (!FAST) return __fdiv_rn(gm, 1.0f + expf(-gm)) * uc;
   float e, r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(gm * -1.44269504f));
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));

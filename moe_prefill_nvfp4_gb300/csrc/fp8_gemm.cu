@@ -12,7 +12,8 @@
 // Two kernels:
 //   wide  token rows are the MMA's M operand (128 per tile, a TMEM lane and two epilogue threads to a
 //         row: its sa is one number), weight rows the N operand (NB blocks of 128, sw uniform over a
-//         block).  Persistent CTAs over all experts' tiles.  Bound by shared memory: a k block of a
+//         block).  Persistent CTAs over all experts' tiles (or one tile to a cluster that shares its k
+//         blocks, where tiles are few and long).  Bound by shared memory: a k block of a
 //         128 x 256 tile is 512 cycles of MMA, and 768 of writing its 48 KB there and reading them
 //         back; it takes ~850 (434 ns), 2.9 of the 3.8 PFLOP/s that a library product with one scale
 //         to a tensor reaches.  (CTA pairs, whose tiles need 32 KB to an SM, measured slower: with 256
@@ -115,6 +116,12 @@ MOE_DEV uint64_t mul_f32x2(uint64_t a, uint64_t b) {
   return d;
 }
 
+MOE_DEV uint64_t add_f32x2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
 template <uint32_t N>
 MOE_DEV void reg_inc() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
@@ -162,6 +169,11 @@ MOE_DEV void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memo
 template <int N>
 MOE_DEV void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// ... on a barrier that CTAs of the cluster arrive on (acquire at cluster scope)
+MOE_DEV bool warp_wait_cluster(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* err) {
+  return __all_sync(0xffffffffu, mbar_wait_cluster(bar, parity, abort_flag, err));
 }
 
 // named_bar_sync that tells every thread whether any of them had pred set.
@@ -321,11 +333,12 @@ MOE_DEV void bulk_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memor
 // ------------------------------------------------------------------------------------------------
 // wide kernel
 
-template <int NB_, bool GATHER_, bool GATE_UP_>
+template <int NB_, bool GATHER_, bool GATE_UP_, bool SPLIT_ = false>
 struct WideCfg {
   static constexpr int NB = NB_;           // weight blocks of 128 per tile
   static constexpr bool GATE_UP = GATE_UP_;
   static constexpr bool GATHER = GATHER_;  // token rows through gather ids
+  static constexpr bool SPLIT = SPLIT_;    // a tile's k blocks shared by a cluster of 2 or 4 CTAs
   static constexpr int BN = NB * 128;
   // warpgroup 0: TMA, MMA, scales; 1 and 2: epilogue; 3: gathering
   static constexpr int THREADS = GATHER ? 512 : 384;
@@ -344,8 +357,8 @@ struct WideCfg {
   static constexpr int OFF_OFFS = OFF_F + NF * F_SLOT * 4;
   static constexpr int OFF_TBASE = OFF_OFFS + (MAX_E + 1) * 4;
   static constexpr int OFF_BAR = (OFF_TBASE + (MAX_E + 1) * 4 + 7) & ~7;
-  // full[NS] empty[NS] d_full[2] d_empty[2] drain
-  static constexpr int NBAR = 2 * NS + 5;
+  // full[NS] empty[NS] d_full[2] d_empty[2] drain j
+  static constexpr int NBAR = 2 * NS + 6;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
   static constexpr int BYTES = OFF_MISC + 16;
   static constexpr int SMEM = BYTES + 1024;
@@ -353,6 +366,9 @@ struct WideCfg {
   static constexpr int REG_LAUNCH = GATHER ? 128 : 168;
   static constexpr int REG_LOW = NB == 1 ? REG_LAUNCH - 32 : GATHER ? 56 : 72;
   static constexpr int REG_HIGH = NB == 1 ? REG_LAUNCH + (GATHER ? 32 : 16) : GATHER ? 200 : 216;
+  // partial sums for the cluster's other CTAs, 64-bit words [epilogue warp][32][lane], over the drained stages
+  static constexpr int PART_WARP = 32 * 32 * 8;
+  static_assert(!SPLIT || (NB == 1 && !GATE_UP && 8 * PART_WARP <= NS * STAGE), "partial sums");
   static_assert((THREADS - 256) * REG_LOW + 256 * REG_HIGH <= THREADS * REG_LAUNCH, "register split");
   static_assert(SMEM > 232448 / 2 && SMEM <= 232448, "one CTA per SM (it takes all of TMEM)");
 };
@@ -378,7 +394,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   auto empty = [&](int s) { return bar0 + 8u * (NS + s); };
   auto d_full = [&](int d) { return bar0 + 8u * (2 * NS + d); };
   auto d_empty = [&](int d) { return bar0 + 8u * (2 * NS + 2 + d); };
-  const uint32_t drain_bar = bar0 + 8u * (2 * NS + 4);
+  const uint32_t drain_bar = bar0 + 8u * (2 * NS + 4), j_bar = drain_bar + 8;
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
   volatile int* s_abort = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
   float* s_f = reinterpret_cast<float*>(smem + C::OFF_F);
@@ -386,6 +402,10 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint64_t limit = args.wait_ns;
   int* err = args.err;
+  // tiles first, first + step, ...; with SPLIT one tile to a cluster of S CTAs
+  const int S = C::SPLIT ? (int)cluster_nctarank() : 1, rank = C::SPLIT ? (int)cluster_ctarank() : 0;
+  const int first = C::SPLIT ? (int)cluster_id_x() : (int)blockIdx.x;
+  const int step = C::SPLIT ? (int)cluster_count_x() : (int)gridDim.x;
 
   if (tid == 0) {
     for (int s = 0; s < NS; ++s) {
@@ -397,6 +417,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       mbar_init(d_empty(d), 8);  // the epilogue warps
     }
     mbar_init(drain_bar, 1);
+    if (C::SPLIT) mbar_init(j_bar, S);  // the CTAs whose partial sums are written
     *s_abort = 0;
     fence_barrier_init();
   }
@@ -404,6 +425,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     tmem_alloc(smem_u32(s_tmem), C::TMEM_COLS);
     tmem_relinquish();
   }
+  if (C::SPLIT) cluster_sync_all();  // the barriers exist before other CTAs arrive on them
   griddep_wait();
   griddep_launch_dependents();
   const int NG = C::GATE_UP ? args.half / 128 : (args.N + C::BN - 1) / C::BN;
@@ -423,6 +445,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   const uint32_t tmem_base = *s_tmem;
   const int KB = (args.K + BK - 1) / BK;
   const int total = s_tbase[args.E];
+  // this CTA's k blocks
+  const int kb0 = C::SPLIT ? KB * rank / S : 0, kb1 = C::SPLIT ? KB * (rank + 1) / S : KB;
 
   if (warp < 4) {
     reg_dec<C::REG_LOW>();
@@ -433,9 +457,9 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         prefetch_tmap(&wmap);
         int i = 0;
         bool ok = true;
-        for (int g = blockIdx.x; ok && g < total; g += gridDim.x) {
+        for (int g = first; ok && g < total; g += step) {
           const Tile t = decode_tile(g, args, s_offs, s_tbase, 128, NG);
-          for (int kb = 0; kb < KB; ++kb, ++i) {
+          for (int kb = kb0; kb < kb1; ++kb, ++i) {
             const int s = i % NS;
             if (!wait_bounded(empty(s), ((i / NS) & 1) ^ 1, s_abort, err, limit)) {
               ok = false;
@@ -460,8 +484,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       constexpr uint32_t idesc = make_idesc_e4m3(128, C::BN);
       int i = 0;
       bool ok = true;
-      for (int g = blockIdx.x; ok && g < total; g += gridDim.x) {
-        for (int kb = 0; kb < KB; ++kb, ++i) {
+      for (int g = first; ok && g < total; g += step) {
+        for (int kb = kb0; kb < kb1; ++kb, ++i) {
           const int s = i % NS, db = i & 1;
           // (the operands are usually there first: the accumulator's release is what an MMA waits for)
           if (!warp_wait(full(s), (i / NS) & 1, s_abort, err, limit)) {
@@ -497,14 +521,14 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       // accumulator buffer of block i is free its arrival joins the MMA's commit.
       const float* sa[4];
       const float* sw = nullptr;
-      int g = blockIdx.x, kb = 0, n = 0;  // the next block to copy
+      int g = first, kb = kb0, n = 0;  // the next block to copy
       auto copy_next = [&]() {
         if (g < total) {
-          if (kb == 0) {
+          if (kb == kb0) {
             const Tile t = decode_tile(g, args, s_offs, s_tbase, 128, NG);
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-              sa[j] = args.sa + (int64_t)source_row(args, t.p0 + min(32 * j + lane, t.cnt - 1)) * args.sa_row;
+              sa[j] = args.sa + (int64_t)source_row(args, t.p0 + min(32 * j + lane, t.cnt - 1)) * args.sa_row + kb0 * args.sa_grp;
             // lane h < NB: block h's (past N: any scale, the block's columns are not stored)
             const int blk = min(block_row<NB>(args, t.ng, min(lane, NB - 1)) >> 7, args.nblk - 1);
             sw = args.sw + ((int64_t)t.e * args.nblk + blk) * KB;
@@ -516,9 +540,9 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             sa[j] += args.sa_grp;
           }
           if (lane < NB) cp_async4(dst + 512u, sw + kb);
-          if (++kb == KB) {
-            kb = 0;
-            g += gridDim.x;
+          if (++kb == kb1) {
+            kb = kb0;
+            g += step;
           }
           ++n;
         }
@@ -547,13 +571,13 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     const uint32_t dst = sbase + (uint32_t)(r0 * BK + ((chunk ^ (r0 & 7)) << 4));
     int i = 0;
     bool ok = true;
-    for (int g = blockIdx.x; ok && g < total; g += gridDim.x) {
+    for (int g = first; ok && g < total; g += step) {
       const Tile t = decode_tile(g, args, s_offs, s_tbase, 128, NG);
       const uint8_t* src[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j)
-        src[j] = args.A + source_row(args, t.p0 + min(r0 + 16 * j, t.cnt - 1)) * args.lda + chunk * 16;
-      for (int kb = 0; kb < KB; ++kb, ++i) {
+        src[j] = args.A + source_row(args, t.p0 + min(r0 + 16 * j, t.cnt - 1)) * args.lda + kb0 * BK + chunk * 16;
+      for (int kb = kb0; kb < kb1; ++kb, ++i) {
         const int s = i % NS;
         if (!warp_wait(empty(s), ((i / NS) & 1) ^ 1, s_abort, err, limit)) {
           ok = false;
@@ -588,14 +612,14 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     if (total >= 0) zero_absent(args, s_offs, (int64_t)blockIdx.x * 256 + (tid - 128), (int64_t)gridDim.x * 256);
     int i = 0;
     bool ok = true;
-    for (int g = blockIdx.x; ok && g < total; g += gridDim.x) {
+    for (int g = first; ok && g < total; g += step) {
       const Tile t = decode_tile(g, args, s_offs, s_tbase, 128, NG);
       uint64_t acc[NB][32];
 #pragma unroll
       for (int h = 0; h < NB; ++h)
 #pragma unroll
         for (int j = 0; j < 32; ++j) acc[h][j] = 0;
-      for (int kb = 0; kb < KB; ++kb, ++i) {
+      for (int kb = kb0; kb < kb1; ++kb, ++i) {
         const int db = i & 1;
         if (!warp_wait(d_full(db), (i >> 1) & 1, s_abort, err, limit)) {
           ok = false;
@@ -638,7 +662,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         }
       }
       // (the gate/up form's warps exchange maxima below: all of them leave the loop at the same tile)
-      if (C::GATE_UP ? named_bar_any(1, 256, !ok) : !ok) {
+      if (C::GATE_UP || C::SPLIT ? named_bar_any(1, 256, !ok) : !ok) {
         ok = false;
         break;
       }
@@ -651,8 +675,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           float g0, g1, u0, u1;
           unpack_f32x2(acc[0][j], g0, g1);
           unpack_f32x2(acc[NB - 1][j], u0, u1);
-          g0 = swiglu_keep_nan(g0, u0, args.limit);
-          g1 = swiglu_keep_nan(g1, u1, args.limit);
+          g0 = swiglu_keep_nan<true>(g0, u0, args.limit);
+          g1 = swiglu_keep_nan<true>(g1, u1, args.limit);
           high = max_nan(high, max_nan(fabsf(g0), fabsf(g1)));
           acc[0][j] = pack_f32x2(g0, g1);
         }
@@ -699,6 +723,62 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           }
         }
         if (live && wg == 0) args.s[(int64_t)(t.p0 + row) * args.s_row + t.ng * args.s_grp] = scale;
+      } else if constexpr (C::SPLIT) {
+        // Of each thread's 64 columns, sixteens 4 rank / S .. are this CTA's to sum and store: the others'
+        // go to shared memory (the stages are drained: every accumulator has been read).
+        const uint32_t part = sbase + (uint32_t)((warp - 4) * C::PART_WARP + lane * 8);
+#pragma unroll
+        for (int b = 0; b < 4; ++b)
+          if (b * S / 4 != rank)
+#pragma unroll
+            for (int j = 8 * b; j < 8 * b + 8; ++j)
+              asm volatile("st.shared.b64 [%0], %1;" ::"r"(part + (uint32_t)(j * 256)), "l"(acc[0][j]) : "memory");
+        named_bar_sync(1, 256);
+        if (tid == 128)
+          for (int c = 0; c < S; ++c) mbar_arrive_remote(j_bar, (uint32_t)c);
+        if (!warp_wait_cluster(j_bar, 0, s_abort, err)) break;
+        const bool live = row < t.cnt;
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          if (b * S / 4 != rank) continue;
+          for (int c = 0; c < S; ++c) {  // in the order of the ranks, this CTA's own first
+            if (c == rank) continue;
+            uint32_t at;
+            asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(part), "r"(c));
+            uint64_t v[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              asm volatile("ld.shared::cluster.b64 %0, [%1];" : "=l"(v[j]) : "r"(at + (uint32_t)((8 * b + j) * 256)));
+#pragma unroll
+            for (int j = 0; j < 8; ++j) acc[0][8 * b + j] = add_f32x2(acc[0][8 * b + j], v[j]);
+          }
+          const int col = block_row<NB>(args, t.ng, 0) + wg * 64 + 16 * b;
+          float o[16];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) unpack_f32x2(acc[0][8 * b + j], o[2 * j], o[2 * j + 1]);
+          const int64_t at = (int64_t)(t.p0 + row) * args.ldc + col;
+          if (!live) {
+          } else if (col + 16 > args.N) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              if (col + j < args.N) {
+                if (args.c_dtype == MOE_DTYPE_BF16)
+                  static_cast<__nv_bfloat16*>(args.C)[at + j] = __float2bfloat16_rn(o[j]);
+                else
+                  static_cast<float*>(args.C)[at + j] = o[j];
+              }
+          } else if (args.c_dtype == MOE_DTYPE_BF16) {
+            uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(args.C) + at);
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+              dst[j] = make_uint4(pack_bf16x2(o[8 * j], o[8 * j + 1]), pack_bf16x2(o[8 * j + 2], o[8 * j + 3]),
+                                  pack_bf16x2(o[8 * j + 4], o[8 * j + 5]), pack_bf16x2(o[8 * j + 6], o[8 * j + 7]));
+          } else {
+            float4* dst = reinterpret_cast<float4*>(static_cast<float*>(args.C) + at);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) dst[j] = make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+          }
+        }
       } else {
         const int nrow = min(32, t.cnt - q * 32);
         const int64_t row0 = t.p0 + q * 32;
@@ -752,11 +832,16 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         }
       }
     }
-    if (lane == 0) bulk_wait();
+    if (!C::SPLIT && lane == 0) bulk_wait();
   }
 
   tc_fence_before();
-  __syncthreads();
+  if (C::SPLIT) {
+    __syncwarp();
+    cluster_sync_all();  // the other CTAs have read this one's sums
+  } else {
+    __syncthreads();
+  }
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem_base, C::TMEM_COLS);
@@ -882,7 +967,7 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
   auto store = [&](const Tile& t, int n, float v0, float v1, uint32_t* amax) {
     const int64_t p = t.p0 + n;
     if (args.half) {
-      const float act = swiglu_keep_nan(v0, v1, args.limit);
+      const float act = swiglu_keep_nan<false>(v0, v1, args.limit);
       const uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(act) & 0x7FFFFFFFu);
       if (lane == 0) amax[n * 4 + q] = m;
       return act;
@@ -1182,24 +1267,10 @@ int c_map(CUtensorMap* m, const Fp8Gemm& d) {
                      strides, box, estr, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-template <class C>
-int launch_wide(const Fp8Gemm& d, int64_t tiles, cudaStream_t st) {
-  CUtensorMap am, wm, cm = {};
-  int rc = a_map(&am, d, 128);
-  if (rc == MOE_OK) rc = w_map(&wm, d);
-  if (rc == MOE_OK) rc = c_map(&cm, d);
-  if (rc != MOE_OK) return rc;
-  static std::atomic<int> configured[64];
-  if ((rc = configure(wide_kernel<C>, C::SMEM, configured)) != MOE_OK) return rc;
-  const int grid = (int)std::min<int64_t>(tiles, device_sm_count());
-  return launch_pdl(wide_kernel<C>, dim3(grid), dim3(C::THREADS), C::SMEM, st, am, wm, cm, d.args);
-}
-
-// Clusters of S CTAs of this kernel that the device holds at once (they do not cross its groups of SMs, so
+// Clusters of S CTAs of a kernel that the device holds at once (they do not cross its groups of SMs, so
 // fewer than the CTAs would suggest), asked once for each S.
-template <class C, bool GATHER>
-int resident_clusters(int S) {
-  static std::atomic<int> known[64][9];
+template <class K>
+int resident_clusters(K kernel, int threads, int smem, int S, std::atomic<int> (*known)[9]) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
   int n = known[dev][S].load(std::memory_order_relaxed);
@@ -1211,13 +1282,34 @@ int resident_clusters(int S) {
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   cfg.gridDim = dim3(S);
-  cfg.blockDim = dim3(C::THREADS);
-  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaOccupancyMaxActiveClusters(&n, few_kernel<C, GATHER>, &cfg) != cudaSuccess) return 0;
+  if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) return 0;
   known[dev][S].store(n, std::memory_order_relaxed);
   return n;
+}
+
+template <class C>
+int launch_wide(const Fp8Gemm& d, int64_t tiles, cudaStream_t st) {
+  CUtensorMap am, wm, cm = {};
+  int rc = a_map(&am, d, 128);
+  if (rc == MOE_OK) rc = w_map(&wm, d);
+  if (rc == MOE_OK) rc = c_map(&cm, d);
+  if (rc != MOE_OK) return rc;
+  static std::atomic<int> configured[64];
+  if ((rc = configure(wide_kernel<C>, C::SMEM, configured)) != MOE_OK) return rc;
+  if constexpr (C::SPLIT) {
+    static std::atomic<int> known[64][9];
+    int S = 1;
+    for (int t = 2; t <= 4; t *= 2)
+      if (tiles <= resident_clusters(wide_kernel<C>, C::THREADS, C::SMEM, t, known)) S = t;
+    return launch_pdl_cluster(wide_kernel<C>, dim3((unsigned)(tiles * S)), dim3(C::THREADS), C::SMEM, st, S, am, wm, cm,
+                              d.args);
+  }
+  const int grid = (int)std::min<int64_t>(tiles, device_sm_count());
+  return launch_pdl(wide_kernel<C>, dim3(grid), dim3(C::THREADS), C::SMEM, st, am, wm, cm, d.args);
 }
 
 template <class C, bool GATHER>
@@ -1233,8 +1325,9 @@ int launch_few(const Fp8Gemm& d, int64_t tiles, cudaStream_t st) {
   // turn wait for each other's sums at every one, 64 tokens' down product 269 us against 182).
   const int KB = (d.args.K + BK - 1) / BK;
   int S = 1;
+  static std::atomic<int> known[64][9];
   for (int t = 2; t <= 8 && 2 * t <= KB; ++t)
-    if (tiles <= resident_clusters<C, GATHER>(t)) S = t;
+    if (tiles <= resident_clusters(few_kernel<C, GATHER>, C::THREADS, C::SMEM, t, known)) S = t;
   const int64_t grid = S > 1 ? tiles * S : std::min<int64_t>(tiles, device_sm_count() * C::PER_SM);
   return launch_pdl_cluster(few_kernel<C, GATHER>, dim3((unsigned)grid), dim3(C::THREADS), C::SMEM, st, S, am, wm,
                             d.args);
@@ -1257,14 +1350,19 @@ int launch(const Fp8Gemm& d, cudaStream_t st) {
   const int64_t wide_tiles = a.half ? tt * ng2 : tt * ((a.N + 127) / 128);
   // Few rows per expert: the few-row kernel up to 16 (gate/up of 128 tokens at 64 experts, 16 rows: 40.0 us
   // against the wide kernel's 45.9; of 512 tokens at 160 experts, 26 rows: 440 against 398).  Busier experts
-  // among them take several of its tiles, each reading the weights again from L2.  And where the wide
-  // kernel's tiles, which do not split k, would leave half of the SMs idle (64 x 1536 x 5120: 8.2 us against
-  // 16.4; 256 rows 13.3 against 16.8).  32 token rows to a tile from 49 rows on (64 rows: 8.2 us against 8.7
-  // with 16; 32 rows: 8.0 against 7.0).
-  if (rows <= 16 || (rows <= 256 && 2 * wide_tiles <= device_sm_count())) {
-    if (rows <= 48) return launch_few<FewCfg<16, 3, 2>, GATHER>(d, token_tiles(d, 16) * ng2, st);
+  // among them take several of its tiles, each reading the weights again from L2.  And up to 128 where the
+  // wide kernel's tiles would leave half of the SMs idle (64 x 1536 x 5120: 8.2 us against 16.4, with its k
+  // split 10.6; 200 rows 14.0 against 11.4 split; gate/up of one expert, 128 rows: 20.1 against 21.2, 200
+  // rows 27.7 against 21.4).  32 token rows to a tile from 33 rows on (64 rows: 8.2 us against 8.7 with 16;
+  // 32 rows: 8.0 against 7.0).
+  const bool idle = 2 * wide_tiles <= device_sm_count();
+  if (rows <= 16 || (rows <= 128 && idle)) {
+    if (rows <= 32) return launch_few<FewCfg<16, 3, 2>, GATHER>(d, token_tiles(d, 16) * ng2, st);
     return launch_few<FewCfg<32, 5, 1>, GATHER>(d, token_tiles(d, 32) * ng2, st);
   }
+  // The plain form's k blocks shared by a cluster where tiles leave half of the SMs idle and are long (333 x
+  // 1536 x 5120: 11.8 us against 16.9; 333 x 1536 x 2048, 16 k blocks: 9.9 against 9.4)
+  if (!a.half && idle && a.K > 23 * BK) return launch_wide<WideCfg<1, GATHER, false, true>>(d, wide_tiles, st);
   if (a.half) return launch_wide<WideCfg<2, GATHER, true>>(d, tt * ng2, st);
   // 128 weight rows to a tile where tiles of 256 would not fill the SMs
   if (tt * ng2 < device_sm_count()) return launch_wide<WideCfg<1, GATHER, false>>(d, tt * ((a.N + 127) / 128), st);

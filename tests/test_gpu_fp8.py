@@ -196,7 +196,8 @@ def test_quantize_no_rows():
 # few-row tiles of 16 and 32, wide tiles of 128 and 256 weight rows; k tails, weight-row tails, one of each
 DENSE = [(1, 1, 1), (1, 128, 128), (1, 5120, 1536), (2, 300, 129), (5, 130, 257), (12, 256, 2048), (13, 513, 384),
          (16, 257, 640), (32, 1000, 100), (40, 385, 1111), (41, 128, 128), (64, 200, 300), (127, 640, 256),
-         (129, 255, 640), (300, 520, 200), (333, 1500, 2000), (1300, 4000, 272), (2000, 2560, 520)]
+         (129, 255, 640), (300, 520, 200), (333, 1500, 2000), (1300, 4000, 272), (2000, 2560, 520),
+         (130, 300, 3000), (257, 1013, 4100), (600, 1280, 3200)]  # long and few tiles: k shared by a cluster
 
 
 @pytest.mark.parametrize("c_dtype", [torch.bfloat16, torch.float32])
@@ -212,6 +213,20 @@ def test_gemm(r, n, k, c_dtype):
     assert_product(got, ref, mags, k)
     assert (flat[0] == 3).all() and (flat[r + 1] == 3).all() and (flat[:, :8] == 3).all() and (flat[:, 8 + n:] == 3).all()
     assert torch.equal(moe.moe_fp8_gemm(a, sa, w, sw, c_dtype=c_dtype), got)  # the same sums in the same order
+
+
+@pytest.mark.parametrize("gather", [False, True], ids=["sorted", "gathered"])
+def test_grouped_gemm_long_k_few_tiles(gather):
+    """Two experts with a long K: the wide kernel's k blocks are shared by a cluster."""
+    counts, n, k = [150, 0, 131], 270, 3200
+    c = grouped_case(counts, n, k, gather, 61, 2)
+    for dt in (torch.bfloat16, torch.float32):
+        out = torch.full((c["slots"], 272), 5.0, dtype=dt, device="cuda")[:, :n]
+        moe.moe_fp8_grouped_gemm(c["a"], c["sa"], c["w"], c["sw"], c["offsets"], c["slots"], gather_ids=c["ids"], out=out,
+                                 c_dtype=dt)
+        ref, mags = grouped64(c)
+        assert_product(out[:281], ref[:281], mags[:281], k)
+        assert (out[281:] == 5).all()
 
 
 @pytest.mark.parametrize("r", [1, 16, 31, 100, 1280])
