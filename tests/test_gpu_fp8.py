@@ -546,3 +546,65 @@ def test_activation_scales_of_any_layout(first_stride):
     for rows in (5, r):
         ref, mags = product64(dequant_rows64(a[:rows], sa[:rows]), dequant_blocks64(w, sw))
         assert_product(moe.moe_fp8_gemm(a[:rows], sa[:rows], w, sw, c_dtype=torch.float32), ref, mags, k)
+
+
+@pytest.mark.parametrize("heavy", [0, 40], ids=["few-rows", "wide-tiles"])
+def test_as_many_experts_as_there_may_be(heavy):
+    """512 experts, most of them without a row; the last has some."""
+    e, n, k = moe.MOE_FP8_MAX_EXPERTS, 136, 144
+    g = torch.Generator().manual_seed(heavy)
+    counts = [int(c) + heavy for c in torch.randint(0, 3, (e,), generator=g) * torch.randint(0, 2, (e,), generator=g)]
+    counts[-1] = 5
+    c = grouped_case(counts, n, k, True, 70 + heavy)
+    got = moe.moe_fp8_grouped_gemm(c["a"], c["sa"], c["w"], c["sw"], c["offsets"], c["slots"], gather_ids=c["ids"],
+                                   c_dtype=torch.float32)
+    ref, mags = grouped64(c)
+    assert_product(got, ref, mags, k)
+
+
+def test_bad_gather_index_in_the_few_row_kernel():
+    c = grouped_case(COUNTS["empty-ends"], 256, 256, True, 80)
+    ids = c["ids"].clone()
+    ids[3], ids[c["slots"] - 1] = 1 << 30, -5
+    got = moe.moe_fp8_grouped_gemm(c["a"], c["sa"], c["w"], c["sw"], c["offsets"], c["slots"], gather_ids=ids)
+    assert moe.moe_get_device_error() == 5
+    ids[3] = ids[c["slots"] - 1] = 0
+    want = moe.moe_fp8_grouped_gemm(c["a"], c["sa"], c["w"], c["sw"], c["offsets"], c["slots"], gather_ids=ids)
+    assert torch.equal(got, want)
+
+
+def test_binding_refuses_on_the_gpu():
+    """Shapes, types and strides that the binding checks before it calls the library."""
+    a, sa = moe.moe_fp8_quantize_rows(rand((4, 256), 90))
+    w, sw = moe.moe_fp8_quantize_blocks(rand((128, 256), 91))
+    ok = moe.moe_fp8_gemm(a, sa, w, sw)
+    assert ok.shape == (4, 128) and ok.dtype == torch.bfloat16
+    for bad in (
+        lambda: moe.moe_fp8_gemm(a[:, :128], sa, w, sw),                       # columns
+        lambda: moe.moe_fp8_gemm(a, sa[:3], w, sw),                            # scales of other rows
+        lambda: moe.moe_fp8_gemm(a, sa.double(), w, sw),
+        lambda: moe.moe_fp8_gemm(a, sa, w, sw[:, :1]),
+        lambda: moe.moe_fp8_gemm(a, sa, w.t(), sw),                            # column stride
+        lambda: moe.moe_fp8_gemm(a, sa, w, sw, c_dtype=torch.float16),
+        lambda: moe.moe_fp8_gemm(a, sa, w, sw, out=torch.empty(4, 127, dtype=torch.bfloat16, device="cuda")),
+        lambda: moe.moe_fp8_gemm(a, sa, w, sw, out=torch.empty(4, 128, device="cuda")),
+        lambda: moe.moe_fp8_gemm(a, sa, w[None], sw[None]),
+        lambda: moe.moe_fp8_quantize_rows(rand((4, 256), 1).half()),
+        lambda: moe.moe_fp8_quantize_rows(rand((4, 256), 1).t()),
+        lambda: moe.moe_fp8_grouped_gemm(a, sa, w[None], sw[None], torch.zeros(2, device="cuda"), 4),
+        lambda: moe.moe_fp8_grouped_gemm(a, sa, w[None], sw[None], offsets_of([4]), 4, gather_ids=offsets_of([4])),
+        lambda: moe.moe_fp8_grouped_gemm(a, sa, w[None], sw[None], offsets_of([4]), -1),
+    ):
+        with pytest.raises(ValueError):
+            bad()
+    for bad in (
+        lambda: moe.moe_fp8_grouped_gemm(a, sa, w[None], sw[None], offsets_of([4]), 5),           # rows of A
+        lambda: moe.moe_fp8_grouped_gemm(a, sa, w[None], sw[None], offsets_of([4]), 4, first=1),
+        lambda: moe.moe_fp8_grouped_gemm_swiglu(a, sa, w[None], sw[None], offsets_of([4]), 4),    # I = 64
+        lambda: moe.moe_fp8_grouped_gemm_swiglu(a, sa, w[None], sw[None], offsets_of([4]), 4, limit=0.0),
+        lambda: moe.moe_fp8_gemm(a, sa, w, sw, out=torch.empty(4, 130, dtype=torch.bfloat16, device="cuda")[:, :128]),
+    ):
+        with pytest.raises(moe.MoeError):
+            bad()
+    with pytest.raises(TypeError):
+        moe.moe_fp8_grouped_gemm(a, sa, w[None], sw[None], offsets_of([4]), "four")
