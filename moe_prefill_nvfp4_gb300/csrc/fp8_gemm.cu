@@ -24,8 +24,8 @@
 //
 // Measured on GB300 (GLM sizes: 160 experts, top-8, hidden 5120, intermediate 1536), cold weights:
 //   down product      1 token 14.8 us, 64 tokens 182 us (6.6 TB/s), 8192 tokens 576 us (1.8 PFLOP/s)
-//   gate/up + SwiGLU  4 tokens 80 us, 64 tokens 351 us (6.9 TB/s), 8192 tokens 1172 us (1.8 PFLOP/s; with
-//                     rows that need no gathering 1060)
+//   gate/up + SwiGLU  4 tokens 80 us, 64 tokens 351 us (6.9 TB/s), 8192 tokens 1100 us (1.9 PFLOP/s; with
+//                     rows that need no gathering 1020)
 //   dense             8192 x 1536 x 5120 59 us (2.2 PFLOP/s), 1 x 5120 x 1536 5.8 us
 //
 // gate/up form: the tile's two blocks are a gate block and the matching up block, and the tile's
@@ -262,27 +262,23 @@ MOE_DEV int block_row(const Fp8GemmArgs& a, int ng, int h) {
 }
 
 // Rows of experts outside W (expert parallelism: other ranks' experts) read as zeros: sorted rows
-// [0, offs[e_first]) and [offs[e_first + e_count], offs[E]).  `tid` of `nthreads` threads of the grid.
-MOE_DEV void zero_absent(const Fp8GemmArgs& a, const int* s_offs, int64_t tid, int64_t nthreads) {
+// [0, offs[e_first]) and [offs[e_first + e_count], offs[E]), a warp to a row; this one is `warp` of
+// `warps` of the grid.
+MOE_DEV void zero_absent(const Fp8GemmArgs& a, const int* s_offs, int warp, int warps) {
+  const int lane = lane_id();
   const int lo = s_offs[a.e_first], hi = s_offs[a.e_first + a.e_count];
-  const int64_t rows = (int64_t)lo + (s_offs[a.E] - hi);
-  if (rows <= 0) return;
-  const int cols = a.half ? a.half : a.N;
-  for (int64_t i = tid; i < rows * cols; i += nthreads) {
-    const int64_t r = i / cols;
-    const int c = (int)(i - r * cols);
+  const int rows = lo + (s_offs[a.E] - hi);
+  const int esz = a.half ? 1 : a.c_dtype == MOE_DTYPE_BF16 ? 2 : 4;
+  const int64_t bytes = (int64_t)(a.half ? a.half : a.N) * esz;
+  for (int r = warp; r < rows; r += warps) {
     const int64_t p = r < lo ? r : hi + (r - lo);
+    uint8_t* out = a.half ? a.q + p * a.ld_q : static_cast<uint8_t*>(a.C) + p * a.ldc * esz;
+    for (int64_t b = lane * 16; b + 16 <= bytes; b += 512) *reinterpret_cast<uint4*>(out + b) = make_uint4(0, 0, 0, 0);
+    for (int64_t b = (bytes & ~15ll) + lane; b < bytes; b += 32) out[b] = 0;
     if (a.half) {
-      a.q[p * a.ld_q + c] = 0;
-      if ((c & 127) == 0) {
-        float s, inv;
-        fp8_scale(0, s, inv);
-        a.s[p * a.s_row + (c >> 7) * a.s_grp] = s;
-      }
-    } else if (a.c_dtype == MOE_DTYPE_BF16) {
-      static_cast<uint16_t*>(a.C)[p * a.ldc + c] = 0;
-    } else {
-      static_cast<float*>(a.C)[p * a.ldc + c] = 0.f;
+      float scale, inv;
+      fp8_scale(0, scale, inv);
+      for (int g = lane; g < a.half / 128; g += 32) a.s[p * a.s_row + g * a.s_grp] = scale;
     }
   }
 }
@@ -563,7 +559,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     // ------------------------------------------------------------------ gathered token rows
     // 16-byte cp.async into the swizzled layout (chunk c of row r at c ^ (r % 8)): 8 lanes to a row of
     // the k block, 4 rows to an instruction, every fourth group of 4 rows to a warp (gate/up of 2048 tokens at
-    // 40 experts 298 us; rows gathered by TMA gather4 689, rows that need no gathering 270).  Sixteens of rows
+    // 40 experts 284 us; rows gathered by TMA gather4 689, rows that need no gathering 260).  Sixteens of rows
     // past the tile's are left as they are (their accumulator rows are not stored), single rows repeat its last.
     reg_dec<C::REG_LOW>();
     const int r0 = (warp - 12) * 4 + (lane >> 3);  // rows r0 + 16 j: the same chunk place in all of them
@@ -609,7 +605,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     uint32_t* s_amax = reinterpret_cast<uint32_t*>(smem + C::OFF_AMAX);
     const uint32_t lane_base = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(wg * 64);
     const int row = q * 32 + lane;  // of the tile
-    if (total >= 0) zero_absent(args, s_offs, (int64_t)blockIdx.x * 256 + (tid - 128), (int64_t)gridDim.x * 256);
+    if (total >= 0) zero_absent(args, s_offs, (int)blockIdx.x * 8 + warp - 4, (int)gridDim.x * 8);
     int i = 0;
     bool ok = true;
     for (int g = first; ok && g < total; g += step) {
@@ -1179,7 +1175,7 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
     }
   }
   if (total >= 0)
-    zero_absent(args, s_offs, (int64_t)blockIdx.x * C::THREADS + tid, (int64_t)gridDim.x * C::THREADS);
+    zero_absent(args, s_offs, (int)blockIdx.x * (C::THREADS / 32) + warp, (int)gridDim.x * (C::THREADS / 32));
 
   if (S > 1) {
     __syncwarp();
