@@ -197,7 +197,8 @@ def test_quantize_no_rows():
 DENSE = [(1, 1, 1), (1, 128, 128), (1, 5120, 1536), (2, 300, 129), (5, 130, 257), (12, 256, 2048), (13, 513, 384),
          (16, 257, 640), (32, 1000, 100), (40, 385, 1111), (41, 128, 128), (64, 200, 300), (127, 640, 256),
          (129, 255, 640), (300, 520, 200), (333, 1500, 2000), (1300, 4000, 272), (2000, 2560, 520),
-         (130, 300, 3000), (257, 1013, 4100), (600, 1280, 3200)]  # long and few tiles: k shared by a cluster
+         (130, 300, 3000), (257, 1013, 4100), (600, 1280, 3200),  # long and few tiles: k shared by a cluster
+         (200, 1, 300), (700, 5, 130), (333, 2, 4000), (40000, 7, 33)]  # narrow outputs of wide tiles
 
 
 @pytest.mark.parametrize("c_dtype", [torch.bfloat16, torch.float32])
