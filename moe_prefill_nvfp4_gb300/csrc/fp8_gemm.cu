@@ -1317,13 +1317,16 @@ int launch_few(const Fp8Gemm& d, int64_t tiles, cudaStream_t st) {
   static std::atomic<int> configured[64];
   if ((rc = configure(few_kernel<C, GATHER>, C::SMEM, configured)) != MOE_OK) return rc;
   // Split k as far as every CTA is still resident at once and keeps two k blocks (one token's gate/up at 64
-  // experts, 48 tiles: 10.6 us with one CTA to a tile, 8.2 with four; clusters that share several tiles in
-  // turn wait for each other's sums at every one, 64 tokens' down product 269 us against 182).
+  // experts, 48 tiles: 11.9 us with one CTA to a tile, 9.4 with four; at 160 experts, 96 tiles: 27.5 with one,
+  // 25.6 with two, 31.9 with four, which no longer fit; clusters that share several tiles in turn wait for
+  // each other's sums at every one, 64 tokens' down product 269 us against 182).  The query counts one CTA of
+  // these kernels per SM whatever they use; PER_SM of them run (192 tiles of two CTAs per SM take 41 us, one
+  // and a third rounds of one per SM 49).
   const int KB = (d.args.K + BK - 1) / BK;
   int S = 1;
   static std::atomic<int> known[64][9];
   for (int t = 2; t <= 8 && 2 * t <= KB; ++t)
-    if (tiles <= resident_clusters(few_kernel<C, GATHER>, C::THREADS, C::SMEM, t, known)) S = t;
+    if (tiles <= C::PER_SM * resident_clusters(few_kernel<C, GATHER>, C::THREADS, C::SMEM, t, known)) S = t;
   const int64_t grid = S > 1 ? tiles * S : std::min<int64_t>(tiles, device_sm_count() * C::PER_SM);
   return launch_pdl_cluster(few_kernel<C, GATHER>, dim3((unsigned)grid), dim3(C::THREADS), C::SMEM, st, S, am, wm,
                             d.args);
