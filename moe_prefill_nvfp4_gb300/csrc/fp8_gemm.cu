@@ -1347,15 +1347,17 @@ int launch(const Fp8Gemm& d, cudaStream_t st) {
   const int64_t ng2 = a.half ? a.half / 128 : (a.N + 255) / 256;
   const int64_t tt = token_tiles(d, 128);
   const int64_t wide_tiles = a.half ? tt * ng2 : tt * ((a.N + 127) / 128);
-  // Few rows per expert: the few-row kernel up to 16 (gate/up of 128 tokens at 64 experts, 16 rows: 40.0 us
-  // against the wide kernel's 45.9; of 512 tokens at 160 experts, 26 rows: 440 against 398).  Busier experts
-  // among them take several of its tiles, each reading the weights again from L2.  And up to 128 where the
+  // Few rows per expert: the few-row kernel up to 8 (at 64 experts the down product of 64 tokens, 8 rows,
+  // takes 21.1 us against the wide kernel's 23.9 and gate/up 40.5 against 40.1; at 160 experts gate/up of 64
+  // tokens, 3.2 rows, 352 against 369, of 256 tokens, 12.8 rows, 393 against 375).  Busier experts among them
+  // take several of its tiles, each reading the weights again from L2: routed by a Zipf(1.2) law, 1280 rows
+  // over 160 experts take 315 us against 305, 2560 rows 425 against 359.  And up to 128 rows where the
   // wide kernel's tiles would leave half of the SMs idle (64 x 1536 x 5120: 8.2 us against 16.4, with its k
   // split 10.6; 200 rows 14.0 against 11.4 split; gate/up of one expert, 128 rows: 20.1 against 21.2, 200
   // rows 27.7 against 21.4).  32 token rows to a tile from 33 rows on (64 rows: 8.2 us against 8.7 with 16;
   // 32 rows: 8.0 against 7.0).
   const bool idle = 2 * wide_tiles <= device_sm_count();
-  if (rows <= 16 || (rows <= 128 && idle)) {
+  if (rows <= 8 || (rows <= 128 && idle)) {
     if (rows <= 32) return launch_few<FewCfg<16, 3, 2>, GATHER>(d, token_tiles(d, 16) * ng2, st);
     return launch_few<FewCfg<32, 5, 1>, GATHER>(d, token_tiles(d, 32) * ng2, st);
   }
