@@ -12,6 +12,7 @@ runs one chunk of random weights and prints its time and its distance from the s
 
 from __future__ import annotations
 
+import contextlib
 from typing import Optional
 
 import torch
@@ -19,6 +20,22 @@ import torch
 from . import _lib as moe
 
 __all__ = ["Fp8Weight", "Fp8SharedExpert", "Fp8Experts"]
+
+
+def _on(stream):
+    """Context in which torch's own operations and allocations belong to `stream` too, as the calls that are
+    given it do: what a forward drops on return is then handed out again behind its last use."""
+    if stream is None:
+        return contextlib.nullcontext()
+    return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream)
+                             else torch.cuda.ExternalStream(stream.cuda_stream))
+
+
+def _result(t: torch.Tensor, stream) -> torch.Tensor:
+    """A result allocated on `stream`, for the current stream to use (and to drop) once it has waited for it."""
+    if stream is not None:
+        t.record_stream(torch.cuda.current_stream())
+    return t
 
 
 class Fp8Weight:
@@ -47,11 +64,14 @@ class Fp8SharedExpert:
         self.gate_up, self.down, self.limit = gate_up, down, limit
 
     def forward(self, q: torch.Tensor, s: torch.Tensor, stream=None) -> torch.Tensor:
-        """BF16 [T, H] of quantised rows.  The gate/up product runs as one expert that has every row."""
-        rows = torch.arange(0, 2 * q.shape[0], q.shape[0], dtype=torch.int32, device=q.device)  # [0, T]
-        act = moe.moe_fp8_grouped_gemm_swiglu(q, s, self.gate_up.q[None], self.gate_up.s[None], rows, q.shape[0],
-                                              limit=self.limit, stream=stream)
-        return moe.moe_fp8_gemm(*act, self.down.q, self.down.s, stream=stream)
+        """BF16 [T, H] of quantised rows.  The gate/up product runs as one expert that has every row.
+        ``stream``: as for ``Fp8Experts.forward``."""
+        with _on(stream):
+            rows = torch.arange(0, 2 * q.shape[0], q.shape[0], dtype=torch.int32, device=q.device)  # [0, T]
+            act = moe.moe_fp8_grouped_gemm_swiglu(q, s, self.gate_up.q[None], self.gate_up.s[None], rows, q.shape[0],
+                                                  limit=self.limit, stream=stream)
+            y = moe.moe_fp8_gemm(*act, self.down.q, self.down.s, stream=stream)
+        return _result(y, stream)
 
 
 class Fp8Experts:
@@ -68,13 +88,22 @@ class Fp8Experts:
 
     def forward(self, x: torch.Tensor, w_router: Optional[torch.Tensor] = None, logits: Optional[torch.Tensor] = None,
                 router_bias: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
-        """BF16 [T, H] of a chunk x BF16 [T, H], routed by ``logits`` FP32 [T, E] or by ``w_router`` BF16 [E, H]."""
+        """BF16 [T, H] of a chunk x BF16 [T, H], routed by ``logits`` FP32 [T, E] or by ``w_router`` BF16 [E, H].
+
+        With ``stream`` everything runs on it, temporaries and a new result are allocated on it, and nothing waits
+        for the current stream: the caller has the inputs ready on ``stream``, keeps them until it is done, and
+        waits for it before it uses the result elsewhere."""
         if (w_router is None) == (logits is None):
             raise ValueError("forward: exactly one of w_router and logits")
-        if logits is None:
-            logits = moe.moe_router_logits(x, w_router, stream=stream)
-        if logits.shape != (x.shape[0], self.num_experts):
-            raise ValueError(f"logits: need {(x.shape[0], self.num_experts)}, got {tuple(logits.shape)}")
+        with _on(stream):
+            if logits is None:
+                logits = moe.moe_router_logits(x, w_router, stream=stream)
+            if logits.shape != (x.shape[0], self.num_experts):
+                raise ValueError(f"logits: need {(x.shape[0], self.num_experts)}, got {tuple(logits.shape)}")
+            y = self._chunk(x, logits, router_bias, out, stream)
+        return y if out is not None else _result(y, stream)
+
+    def _chunk(self, x, logits, router_bias, out, stream) -> torch.Tensor:
         ids, wts = moe.moe_route_topk(logits, self.top_k, router_bias, self.renormalize, self.routed_scale, stream=stream)
         order = moe.moe_sort_by_expert(ids, self.num_experts, stream=stream)
         slots = ids.numel()
