@@ -77,11 +77,13 @@ class Fp8SharedExpert:
 class Fp8Experts:
     """E routed experts, gate_up [count, 2I, H] and down [count, H, I]: all of them, or the ``count`` experts
     from ``first`` on of ``num_experts`` (expert parallelism: the others' part of the result is zero, and the
-    caller adds the ranks' results)."""
+    caller adds the ranks' results; the shared expert, which is in one of them only, goes with expert 0)."""
 
     def __init__(self, gate_up: Fp8Weight, down: Fp8Weight, top_k: int, num_experts: Optional[int] = None, first: int = 0,
                  limit: float = 7.0, renormalize: bool = True, routed_scale: float = 1.0,
                  shared: Optional[Fp8SharedExpert] = None):
+        if shared is not None and first != 0:
+            raise ValueError(f"shared: the results of all parts are added, only the one with first = 0 has it (got {first})")
         self.gate_up, self.down, self.top_k, self.first, self.limit = gate_up, down, top_k, first, limit
         self.num_experts = gate_up.q.shape[0] if num_experts is None else num_experts
         self.renormalize, self.routed_scale, self.shared = renormalize, routed_scale, shared

@@ -87,3 +87,13 @@ def test_everything_of_the_shared_expert_is_on_its_stream(calls):
     shared = fp8.Fp8SharedExpert(weight(256, 64), weight(64, 128))
     shared.forward(torch.zeros(3, 64).to(torch.float8_e4m3fn), torch.ones(3, 1), Side.current)
     assert len(calls) >= 2 and all(current for _, _, current in calls), calls
+
+
+def test_shared_expert_is_in_one_part_only():
+    """The parts' results are added: a shared expert in each of them would count as often."""
+    shared = fp8.Fp8SharedExpert(weight(256, 64), weight(64, 128))
+    parts = weight(4, 256, 64), weight(4, 64, 128)
+    with pytest.raises(ValueError, match="shared"):
+        fp8.Fp8Experts(*parts, top_k=2, num_experts=8, first=4, shared=shared)
+    assert fp8.Fp8Experts(*parts, top_k=2, num_experts=8, first=0, shared=shared).shared is shared
+    assert fp8.Fp8Experts(*parts, top_k=2, num_experts=8, first=4).shared is None
