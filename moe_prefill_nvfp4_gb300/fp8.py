@@ -39,14 +39,16 @@ def _result(t: torch.Tensor, stream) -> torch.Tensor:
 
 
 class Fp8Weight:
-    """Codes [..., N, K] (E4M3) and scales [..., ceil(N/128), ceil(K/128)] of a weight or of one weight
-    per expert.  ``quantise`` makes them from BF16 or FP32, at load."""
+    """Codes (E4M3) and scales of a weight, [N, K] and [ceil(N/128), ceil(K/128)], or of one weight per expert,
+    both with the experts in front.  ``quantise`` makes them from BF16 or FP32, at load."""
 
     def __init__(self, q: torch.Tensor, s: torch.Tensor):
         self.q, self.s = q, s
 
     @classmethod
     def quantise(cls, w: torch.Tensor) -> "Fp8Weight":
+        if w.dim() not in (2, 3):
+            raise ValueError(f"w: need [N, K] or [experts, N, K], got {tuple(w.shape)}")
         lead, (n, k) = w.shape[:-2], w.shape[-2:]
         q = torch.empty(*lead, n, -(-k // 16) * 16, dtype=torch.float8_e4m3fn, device=w.device)[..., :k]
         s = torch.empty(*lead, -(-n // 128), -(-k // 128), dtype=torch.float32, device=w.device)

@@ -97,3 +97,9 @@ def test_shared_expert_is_in_one_part_only():
         fp8.Fp8Experts(*parts, top_k=2, num_experts=8, first=4, shared=shared)
     assert fp8.Fp8Experts(*parts, top_k=2, num_experts=8, first=0, shared=shared).shared is shared
     assert fp8.Fp8Experts(*parts, top_k=2, num_experts=8, first=4).shared is None
+
+
+@pytest.mark.parametrize("shape", [(128,), (2, 3, 128, 128), (1, 1, 2, 128, 128)])
+def test_weight_of_another_rank_is_refused(shape):
+    with pytest.raises(ValueError, match="w: need"):
+        fp8.Fp8Weight.quantise(torch.zeros(shape))
