@@ -40,6 +40,7 @@
 #include <algorithm>
 #include <atomic>
 
+#include "expert_rows.h"
 #include "fp8.cuh"
 #include "internal.h"
 
@@ -210,11 +211,12 @@ MOE_DEV void build_tiles(const Fp8GemmArgs& a, const int* s_offs, int* s_tbase, 
   int sum = 0;
   bool bad = false;
   for (int e = e0; e < e1; ++e) {
-    const int m = s_offs[e + 1] - s_offs[e];
-    if (m < 0) bad = true;
-    if (m > 0 && (unsigned)(e - a.e_first) < (unsigned)a.e_count) sum += NG * ((m + BT - 1) / BT);
+    if (!expert_rows_ok(s_offs[e], s_offs[e + 1], a.R))
+      bad = true;
+    else if ((unsigned)(e - a.e_first) < (unsigned)a.e_count)
+      sum += NG * tiles_of_rows(s_offs[e + 1] - s_offs[e], BT);
   }
-  if (lane == 0 && (s_offs[0] != 0 || s_offs[a.E] > a.R)) bad = true;
+  if (lane == 0 && s_offs[0] != 0) bad = true;
   bad = __any_sync(0xffffffffu, bad);
   if (bad && lane == 0) set_error(a.err, MOE_DEVERR_BAD_OFFSETS);
   int incl = sum;
@@ -226,8 +228,7 @@ MOE_DEV void build_tiles(const Fp8GemmArgs& a, const int* s_offs, int* s_tbase, 
   int run = incl - sum;
   for (int e = e0; e < e1; ++e) {
     s_tbase[e] = bad ? 0 : run;
-    const int m = s_offs[e + 1] - s_offs[e];
-    if (m > 0 && (unsigned)(e - a.e_first) < (unsigned)a.e_count) run += NG * ((m + BT - 1) / BT);
+    if (!bad && (unsigned)(e - a.e_first) < (unsigned)a.e_count) run += NG * tiles_of_rows(s_offs[e + 1] - s_offs[e], BT);
   }
   if (lane == 31) s_tbase[a.E] = bad ? -1 : incl;
 }
@@ -1335,7 +1336,7 @@ int launch_few(const Fp8Gemm& d, int64_t tiles, cudaStream_t st) {
 // Upper bound of the number of token tiles of BT rows: experts with rows plus their full tiles.
 int64_t token_tiles(const Fp8Gemm& d, int BT) {
   const Fp8GemmArgs& a = d.args;
-  if (a.offsets == nullptr) return (a.R + BT - 1) / BT;
+  if (a.offsets == nullptr) return tiles_of_rows(a.R, BT);
   return std::min<int64_t>(a.R, std::min<int64_t>(a.R, a.e_count) + a.R / BT);
 }
 
