@@ -49,6 +49,7 @@
 #include <atomic>
 
 #include "common.cuh"
+#include "expert_rows.h"
 #include "internal.h"
 
 namespace moe {
@@ -246,11 +247,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     int sum = 0;
     bool bad = false;
     for (int e = e0; e < e1; ++e) {
-      const int m = s_offs[e + 1] - s_offs[e];
-      if (m < 0) bad = true;
-      if (m > 0 && args.packed[e] != nullptr) sum += NBG * ((m + C::BN_MAX - 1) / C::BN_MAX);
+      if (!expert_rows_ok(s_offs[e], s_offs[e + 1], args.R))
+        bad = true;
+      else if (args.packed[e] != nullptr)
+        sum += NBG * tiles_of_rows(s_offs[e + 1] - s_offs[e], C::BN_MAX);
     }
-    if (lane == 0 && (s_offs[0] != 0 || s_offs[E] > args.R || s_offs[E] < 0)) bad = true;
+    if (lane == 0 && s_offs[0] != 0) bad = true;
     bad = __any_sync(0xffffffffu, bad);
     int incl = sum;
 #pragma unroll
@@ -261,8 +263,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     int run = incl - sum;
     for (int e = e0; e < e1; ++e) {
       s_tbase[e] = bad ? 0 : run;
-      const int m = s_offs[e + 1] - s_offs[e];
-      if (m > 0 && args.packed[e] != nullptr) run += NBG * ((m + C::BN_MAX - 1) / C::BN_MAX);
+      if (!bad && args.packed[e] != nullptr) run += NBG * tiles_of_rows(s_offs[e + 1] - s_offs[e], C::BN_MAX);
     }
     if (lane == 31) s_tbase[E] = bad ? 0 : incl;
     if (lane == 0) *s_bad = bad ? 1 : 0;

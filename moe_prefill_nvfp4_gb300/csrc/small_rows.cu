@@ -12,6 +12,7 @@
 #include <cuda_bf16.h>
 
 #include "common.cuh"
+#include "expert_rows.h"
 #include "internal.h"
 
 namespace moe {
@@ -152,13 +153,13 @@ __global__ void __launch_bounds__(SR_WARPS * 32, 2)
   for (long long it = blockIdx.x * SR_WARPS + (threadIdx.x >> 5); it < items; it += nwarps) {
     const int e = (int)(it / groups);
     const int n0 = (int)(it - (long long)e * groups) * NOUT;
-    const int p0 = offsets[e];
-    const int m = offsets[e + 1] - p0;
-    if (m <= 0) continue;
-    if (p0 < 0 || p0 + m > R) {
+    const int p0 = offsets[e], p1 = offsets[e + 1];
+    if (p1 <= p0) continue;
+    if (!expert_rows_ok(p0, p1, R)) {
       if (lane == 0 && n0 == 0) set_error(err, MOE_DEVERR_BAD_OFFSETS);
       continue;
     }
+    const int m = p1 - p0;
     if (m > SR_MAXM) {
       if (lane == 0 && n0 == 0) set_error(err, MOE_DEVERR_SMALL_ROWS);
       continue;
