@@ -475,7 +475,8 @@ def _fp8():
         # the current stream's handle without making a Stream object, where torch offers it
         raw = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
             lambda index: torch.cuda.current_stream(index).cuda_stream)
-        m.init(MoeError, torch.empty_strided, torch.float8_e4m3fn, torch.bfloat16, torch.float32, torch.int32, raw)
+        device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+        m.init(MoeError, torch.empty_strided, torch.float8_e4m3fn, torch.bfloat16, torch.float32, torch.int32, raw, device)
         _FP8 = m
     return _FP8
 

@@ -12,9 +12,10 @@
 #include "moe_prefill.h"
 
 /* set by init() */
-static PyObject *g_error, *g_empty, *g_f8, *g_bf16, *g_f32, *g_i32, *g_raw_stream;
+static PyObject *g_error, *g_empty, *g_f8, *g_bf16, *g_f32, *g_i32, *g_raw_stream, *g_current_device;
+static PyObject* g_no_text; /* "" */
 /* interned names */
-static PyObject *n_dtype, *n_is_cuda, *n_shape, *n_stride, *n_data_ptr, *n_device, *n_get_device, *n_cuda_stream;
+static PyObject *n_dtype, *n_shape, *n_stride, *n_data_ptr, *n_device, *n_get_device, *n_cuda_stream;
 static PyObject* kw_empty; /* ("dtype", "device") */
 
 typedef struct {
@@ -35,15 +36,24 @@ static int ints(PyObject* tuple, int64_t* out) {
 
 static int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-/* Reads a CUDA tensor of nd dimensions and one of two element types (d1 may be NULL). */
-static int read_tensor(PyObject* t, const char* name, int nd, PyObject* d0, PyObject* d1, Tensor* out) {
-  PyObject *dtype = PyObject_GetAttr(t, n_dtype), *cuda = NULL, *shape = NULL, *stride = NULL, *ptr = NULL;
+/* Reads a CUDA tensor of nd dimensions and one of two element types (d1 may be NULL).  *gpu is the GPU of the
+ * call's tensors, -1 before the first: the kernel runs on one GPU and gets every pointer. */
+static int read_tensor(PyObject* t, const char* name, int nd, PyObject* d0, PyObject* d1, Tensor* out, int* gpu) {
+  PyObject *dtype = PyObject_GetAttr(t, n_dtype), *index = NULL, *shape = NULL, *stride = NULL, *ptr = NULL;
   int ok = 0;
   if (dtype == NULL) return 0;
-  if ((cuda = PyObject_GetAttr(t, n_is_cuda)) == NULL || (shape = PyObject_GetAttr(t, n_shape)) == NULL) goto done;
-  if ((dtype != d0 && dtype != d1) || cuda != Py_True || !PyTuple_Check(shape) || PyTuple_GET_SIZE(shape) != nd) {
-    PyErr_Format(PyExc_ValueError, "%s: need a CUDA tensor of %d dimensions and type %R%s%R, got %R %R%s", name, nd, d0,
-                 d1 ? " or " : ", not ", d1 ? d1 : cuda, dtype, shape, cuda == Py_True ? "" : " not on a GPU");
+  if ((index = PyObject_CallMethodNoArgs(t, n_get_device)) == NULL || (shape = PyObject_GetAttr(t, n_shape)) == NULL)
+    goto done;
+  const long device = PyLong_AsLong(index); /* -1: not on a GPU */
+  if (device == -1 && PyErr_Occurred()) goto done;
+  if ((dtype != d0 && dtype != d1) || device < 0 || !PyTuple_Check(shape) || PyTuple_GET_SIZE(shape) != nd) {
+    PyErr_Format(PyExc_ValueError, "%s: need a CUDA tensor of %d dimensions and type %R%s%S, got %R %R%s", name, nd, d0,
+                 d1 ? " or " : "", d1 ? d1 : g_no_text, dtype, shape, device < 0 ? " not on a GPU" : "");
+    goto done;
+  }
+  if (*gpu < 0) *gpu = (int)device;
+  if (device != *gpu) {
+    PyErr_Format(PyExc_ValueError, "%s: on GPU %ld, the tensors before it are on GPU %d", name, device, *gpu);
     goto done;
   }
   if ((stride = PyObject_CallMethodNoArgs(t, n_stride)) == NULL || (ptr = PyObject_CallMethodNoArgs(t, n_data_ptr)) == NULL)
@@ -55,7 +65,7 @@ static int read_tensor(PyObject* t, const char* name, int nd, PyObject* d0, PyOb
   ok = !PyErr_Occurred();
 done:
   Py_XDECREF(dtype);
-  Py_XDECREF(cuda);
+  Py_XDECREF(index);
   Py_XDECREF(shape);
   Py_XDECREF(stride);
   Py_XDECREF(ptr);
@@ -86,9 +96,9 @@ static int same_shape(const Tensor* t, const char* name, int64_t rows, int64_t c
 /* A new reference to `given` (checked: an E4M3, BF16 or FP32 matrix of that shape), or a new tensor with
  * the strides (ld, 1) or, by_column, (1, rows). */
 static PyObject* output(PyObject* given, const char* name, PyObject* dtype, PyObject* device, int64_t rows, int64_t cols,
-                        int64_t ld, int by_column, Tensor* out) {
+                        int64_t ld, int by_column, Tensor* out, int* gpu) {
   if (given != Py_None) {
-    if (!read_tensor(given, name, 2, dtype, NULL, out) || !same_shape(out, name, rows, cols)) return NULL;
+    if (!read_tensor(given, name, 2, dtype, NULL, out, gpu) || !same_shape(out, name, rows, cols)) return NULL;
     return Py_NewRef(given);
   }
   PyObject* size = Py_BuildValue("(LL)", (long long)rows, (long long)cols);
@@ -116,36 +126,42 @@ static PyObject* output(PyObject* given, const char* name, PyObject* dtype, PyOb
 }
 
 static PyObject* codes_out(PyObject* given, const char* name, PyObject* device, int64_t rows, int64_t cols, Tensor* out,
-                           int64_t* ld) {
-  PyObject* t = output(given, name, g_f8, device, rows, cols, ceil_div(cols, 16) * 16, 0, out);
+                           int64_t* ld, int* gpu) {
+  PyObject* t = output(given, name, g_f8, device, rows, cols, ceil_div(cols, 16) * 16, 0, out, gpu);
   if (t != NULL && !unit_columns(out, name)) Py_CLEAR(t);
   *ld = t ? row_stride(out, 16) : 0;
   return t;
 }
 
 static PyObject* product_out(PyObject* given, PyObject* c_dtype, PyObject* device, int64_t rows, int64_t cols, Tensor* out,
-                             int64_t* ld, int* code) {
+                             int64_t* ld, int* code, int* gpu) {
   if (c_dtype != g_bf16 && c_dtype != g_f32) {
     PyErr_SetString(PyExc_ValueError, "c_dtype: torch.bfloat16 or torch.float32");
     return NULL;
   }
   *code = c_dtype == g_bf16 ? MOE_DTYPE_BF16 : MOE_DTYPE_F32;
-  PyObject* t = output(given, "out", c_dtype, device, rows, cols, ceil_div(cols, 8) * 8, 0, out);
+  PyObject* t = output(given, "out", c_dtype, device, rows, cols, ceil_div(cols, 8) * 8, 0, out, gpu);
   if (t != NULL && !unit_columns(out, "out")) Py_CLEAR(t);
   *ld = t ? row_stride(out, 8) : 0;
   return t;
 }
 
-/* the stream handle: `stream`'s, or the current one of the tensor's device */
-static int stream_of(PyObject* stream, PyObject* tensor, void** out) {
+/* The stream handle: `stream`'s, or the current one of the tensors' GPU, which has to be the current GPU: the
+ * library launches there, and the default stream's handle is the same on all of them. */
+static int stream_of(PyObject* stream, int gpu, void** out) {
+  PyObject* now = PyObject_CallNoArgs(g_current_device);
+  if (now == NULL) return 0;
+  const long current = PyLong_AsLong(now);
   PyObject* h = NULL;
-  if (stream != Py_None) {
+  if (current == -1 && PyErr_Occurred()) {
+  } else if (current != gpu) {
+    PyErr_Format(PyExc_ValueError, "tensors on GPU %d, the current one is GPU %ld", gpu, current);
+  } else if (stream != Py_None) {
     h = PyObject_GetAttr(stream, n_cuda_stream);
   } else {
-    PyObject* dev = PyObject_CallMethodNoArgs(tensor, n_get_device);
-    if (dev != NULL) h = PyObject_CallOneArg(g_raw_stream, dev);
-    Py_XDECREF(dev);
+    h = PyObject_CallOneArg(g_raw_stream, now);
   }
+  Py_DECREF(now);
   if (h == NULL) return 0;
   *out = PyLong_AsVoidPtr(h);
   Py_DECREF(h);
@@ -186,15 +202,16 @@ static PyObject* quantize(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   Tensor x, q, s;
   int64_t ld_q;
   void* st;
-  if (!want(n, 5) || !read_tensor(a[0], "x", 2, g_bf16, g_f32, &x) || !unit_columns(&x, "x") || !fits(x.shape[0], "rows") ||
-      !fits(x.shape[1], "columns") || !stream_of(a[3], a[0], &st))
+  int gpu = -1;
+  if (!want(n, 5) || !read_tensor(a[0], "x", 2, g_bf16, g_f32, &x, &gpu) || !unit_columns(&x, "x") || !fits(x.shape[0], "rows") ||
+      !fits(x.shape[1], "columns") || !stream_of(a[3], gpu, &st))
     return NULL;
   const int blocks = a[4] == Py_True;
   const int64_t R = x.shape[0], K = x.shape[1], G = ceil_div(K, 128), SR = blocks ? ceil_div(R, 128) : R;
   PyObject* device = PyObject_GetAttr(a[0], n_device);
   if (device == NULL) return NULL;
-  PyObject *tq = codes_out(a[1], "out", device, R, K, &q, &ld_q), *ts = NULL;
-  if (tq != NULL) ts = output(a[2], "scales", g_f32, device, SR, G, G, !blocks, &s);
+  PyObject *tq = codes_out(a[1], "out", device, R, K, &q, &ld_q, &gpu), *ts = NULL;
+  if (tq != NULL) ts = output(a[2], "scales", g_f32, device, SR, G, G, !blocks, &s, &gpu);
   Py_DECREF(device);
   if (ts != NULL && blocks && s.shape[0] * s.shape[1] > 1 && ((s.stride[1] != 1 && G > 1) || (s.stride[0] != G && SR > 1))) {
     PyErr_SetString(PyExc_ValueError, "scales: need a contiguous tensor");
@@ -215,10 +232,10 @@ static PyObject* quantize(PyObject* self, PyObject* const* a, Py_ssize_t n) {
 }
 
 /* activation rows [rows, K] with their scales and a weight [N, K] (nd 2) or [experts, N, K] (nd 3) with its */
-static int operands(PyObject* const* a, int nd, int64_t first, moe_fp8_rows* A, moe_fp8_weight* W) {
+static int operands(PyObject* const* a, int nd, int64_t first, moe_fp8_rows* A, moe_fp8_weight* W, int* gpu) {
   Tensor q, s, w, ws;
-  if (!read_tensor(a[0], "A", 2, g_f8, NULL, &q) || !read_tensor(a[1], "a_scales", 2, g_f32, NULL, &s) ||
-      !read_tensor(a[2], "W", nd, g_f8, NULL, &w) || !read_tensor(a[3], "w_scales", nd, g_f32, NULL, &ws))
+  if (!read_tensor(a[0], "A", 2, g_f8, NULL, &q, gpu) || !read_tensor(a[1], "a_scales", 2, g_f32, NULL, &s, gpu) ||
+      !read_tensor(a[2], "W", nd, g_f8, NULL, &w, gpu) || !read_tensor(a[3], "w_scales", nd, g_f32, NULL, &ws, gpu))
     return 0;
   const int64_t N = w.shape[nd - 2], K = w.shape[nd - 1], G = ceil_div(K, 128), NB = ceil_div(N, 128);
   if (q.shape[1] != K) {
@@ -262,12 +279,12 @@ static PyObject* gemm(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   moe_fp8_weight W;
   Tensor c;
   int64_t ld;
-  int code;
+  int code, gpu = -1;
   void* st;
-  if (!want(n, 7) || !operands(a, 2, 0, &A, &W) || !stream_of(a[6], a[0], &st)) return NULL;
+  if (!want(n, 7) || !operands(a, 2, 0, &A, &W, &gpu) || !stream_of(a[6], gpu, &st)) return NULL;
   PyObject* device = PyObject_GetAttr(a[0], n_device);
   if (device == NULL) return NULL;
-  PyObject* out = product_out(a[4], a[5], device, A.rows, W.N, &c, &ld, &code);
+  PyObject* out = product_out(a[4], a[5], device, A.rows, W.N, &c, &ld, &code, &gpu);
   Py_DECREF(device);
   if (out == NULL || A.rows == 0) return out;
   const int rc = moe_fp8_gemm(&A, &W, c.ptr, ld, code, st);
@@ -277,12 +294,12 @@ static PyObject* gemm(PyObject* self, PyObject* const* a, Py_ssize_t n) {
 }
 
 /* expert_offsets [E + 1] and gather_ids [>= R] (or None): contiguous int32 */
-static int groups(PyObject* offsets, PyObject* gather, int64_t R, Tensor* off, const void** ids) {
+static int groups(PyObject* offsets, PyObject* gather, int64_t R, Tensor* off, const void** ids, int* gpu) {
   Tensor g;
   *ids = NULL;
-  if (!read_tensor(offsets, "expert_offsets", 1, g_i32, NULL, off) || !unit_columns(off, "expert_offsets")) return 0;
+  if (!read_tensor(offsets, "expert_offsets", 1, g_i32, NULL, off, gpu) || !unit_columns(off, "expert_offsets")) return 0;
   if (gather == Py_None) return 1;
-  if (!read_tensor(gather, "gather_ids", 1, g_i32, NULL, &g) || !unit_columns(&g, "gather_ids")) return 0;
+  if (!read_tensor(gather, "gather_ids", 1, g_i32, NULL, &g, gpu) || !unit_columns(&g, "gather_ids")) return 0;
   if (g.shape[0] < R) {
     PyErr_Format(PyExc_ValueError, "gather_ids: need %lld entries, got %lld", (long long)R, (long long)g.shape[0]);
     return 0;
@@ -298,16 +315,16 @@ static PyObject* grouped(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   Tensor off, c;
   const void* ids;
   int64_t ld;
-  int code;
+  int code, gpu = -1;
   void* st;
   if (!want(n, 11)) return NULL;
   const int64_t R = PyLong_AsLongLong(a[5]), first = PyLong_AsLongLong(a[7]);
-  if (PyErr_Occurred() || !fits(R, "R") || !operands(a, 3, first, &A, &W) || !groups(a[4], a[6], R, &off, &ids) ||
-      !stream_of(a[10], a[0], &st))
+  if (PyErr_Occurred() || !fits(R, "R") || !operands(a, 3, first, &A, &W, &gpu) ||
+      !groups(a[4], a[6], R, &off, &ids, &gpu) || !stream_of(a[10], gpu, &st))
     return NULL;
   PyObject* device = PyObject_GetAttr(a[0], n_device);
   if (device == NULL) return NULL;
-  PyObject* out = product_out(a[8], a[9], device, R, W.N, &c, &ld, &code);
+  PyObject* out = product_out(a[8], a[9], device, R, W.N, &c, &ld, &code, &gpu);
   Py_DECREF(device);
   if (out == NULL || R == 0) return out;
   const int rc = moe_fp8_grouped_gemm(&A, ids, &W, off.ptr, (int)off.shape[0] - 1, (int)R, c.ptr, ld, code, st);
@@ -323,18 +340,19 @@ static PyObject* grouped_swiglu(PyObject* self, PyObject* const* a, Py_ssize_t n
   Tensor off, q, s;
   const void* ids;
   int64_t ld;
+  int gpu = -1;
   void* st;
   if (!want(n, 12)) return NULL;
   const int64_t R = PyLong_AsLongLong(a[5]), first = PyLong_AsLongLong(a[8]);
   const double limit = PyFloat_AsDouble(a[6]);
-  if (PyErr_Occurred() || !fits(R, "R") || !operands(a, 3, first, &A, &W) || !groups(a[4], a[7], R, &off, &ids) ||
-      !stream_of(a[11], a[0], &st))
+  if (PyErr_Occurred() || !fits(R, "R") || !operands(a, 3, first, &A, &W, &gpu) ||
+      !groups(a[4], a[7], R, &off, &ids, &gpu) || !stream_of(a[11], gpu, &st))
     return NULL;
   const int64_t I = W.N / 2;
   PyObject* device = PyObject_GetAttr(a[0], n_device);
   if (device == NULL) return NULL;
-  PyObject *tq = codes_out(a[9], "out", device, R, I, &q, &ld), *ts = NULL;
-  if (tq != NULL) ts = output(a[10], "scales", g_f32, device, R, ceil_div(I, 128), 0, 1, &s);
+  PyObject *tq = codes_out(a[9], "out", device, R, I, &q, &ld, &gpu), *ts = NULL;
+  if (tq != NULL) ts = output(a[10], "scales", g_f32, device, R, ceil_div(I, 128), 0, 1, &s, &gpu);
   Py_DECREF(device);
   if (ts == NULL) {
     Py_XDECREF(tq);
@@ -347,11 +365,12 @@ static PyObject* grouped_swiglu(PyObject* self, PyObject* const* a, Py_ssize_t n
   return pair_or_fail(rc, "moe_fp8_grouped_gemm_swiglu", tq, ts);
 }
 
-/* init(MoeError, torch.empty_strided, float8_e4m3fn, bfloat16, float32, int32, device index -> stream handle) */
+/* init(MoeError, torch.empty_strided, float8_e4m3fn, bfloat16, float32, int32, device index -> stream handle,
+ * current device index) */
 static PyObject* init(PyObject* self, PyObject* const* a, Py_ssize_t n) {
-  PyObject** to[7] = {&g_error, &g_empty, &g_f8, &g_bf16, &g_f32, &g_i32, &g_raw_stream};
-  if (!want(n, 7)) return NULL;
-  for (int i = 0; i < 7; ++i) Py_XSETREF(*to[i], Py_NewRef(a[i]));
+  PyObject** to[8] = {&g_error, &g_empty, &g_f8, &g_bf16, &g_f32, &g_i32, &g_raw_stream, &g_current_device};
+  if (!want(n, 8)) return NULL;
+  for (int i = 0; i < 8; ++i) Py_XSETREF(*to[i], Py_NewRef(a[i]));
   Py_RETURN_NONE;
 }
 
@@ -368,7 +387,7 @@ static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_fp8_call", NULL, -1
 
 PyMODINIT_FUNC PyInit__fp8_call(void) {
   n_dtype = PyUnicode_InternFromString("dtype");
-  n_is_cuda = PyUnicode_InternFromString("is_cuda");
+  g_no_text = PyUnicode_InternFromString("");
   n_shape = PyUnicode_InternFromString("shape");
   n_stride = PyUnicode_InternFromString("stride");
   n_data_ptr = PyUnicode_InternFromString("data_ptr");
