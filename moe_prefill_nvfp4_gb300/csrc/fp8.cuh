@@ -40,19 +40,27 @@ MOE_DEV float max_nan(float a, float b) {
   return d;
 }
 
-// silu(min(g, L)) * clamp(u, -L, L) of FP32 sums, NaN kept.  silu(z) = z / (1 + e^-z).  FAST: with the
-// hardware's approximate power of two and reciprocal (2^-22 and 2^-23 relative, against 2^-24 of FP32: the
-// result is rounded to four bits, and one in about a million values then to the other neighbour), for
-// kernels in which the accurate forms' instructions count.  For z -> -inf the power overflows and the
-// quotient is -0, the limit of silu.
+// silu(min(g, L)) * clamp(u, -L, L) of FP32 sums, NaN kept.  silu(z) = z / (1 + e^-z).
+//
+// FAST: e^-z by the hardware's approximate power of two (2^-22 relative) and the quotient by its approximate
+// reciprocal (2^-23), for the wide kernel, whose epilogue nothing hides: with the accurate forms the gate/up
+// product of 256 tokens at 64 experts takes 65.8 us against 41.9, of 2048 tokens at 40 experts 326 against 287.
+// The power's argument t = fl(-z log2 e) is off by up to 2^-24 |t|, which alone would make 2^-18 of e^-z at
+// z = -64 (41.1 and 284 us).  What it misses, x = -z - t ln 2, is exact to 2^-28 |t| in one FMA (ln 2
+// rounded), and e^-z = 2^t (1 + x) to within x^2 / 2 < 2^-35: in all 2^-20 of the result, 2^-21 with the
+// accurate forms.  t is kept within +-127, so that neither 2^t nor x overflows: where it is more, 2^t (1 + x)
+// is past 2^126 and its reciprocal is flushed to zero (the result to a zero, the limit of silu), where it is
+// less, 2^t is flushed and the reciprocal 1.
 template <bool FAST>
 MOE_DEV float swiglu_keep_nan(float g, float u, float L) {
   const float gm = min_nan(g, L);
   const float uc = max_nan(min_nan(u, L), -L);
   if (!FAST) return __fdiv_rn(gm, 1.0f + expf(-gm)) * uc;
+  const float t = fmaxf(fminf(gm * -1.44269504f, 127.0f), -127.0f);
+  const float x = __fmaf_rn(t, -0.693147181f, -gm);
   float e, r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(gm * -1.44269504f));
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(t));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(__fmaf_rn(e, x, 1.0f + e)));
   return gm * r * uc;
 }
 
