@@ -68,9 +68,10 @@ class Fp8SharedExpert:
     def forward(self, q: torch.Tensor, s: torch.Tensor, stream=None) -> torch.Tensor:
         """BF16 [T, H] of quantised rows.  The gate/up product runs as one expert that has every row.
         ``stream``: as for ``Fp8Experts.forward``."""
+        tokens = q.shape[0]
         with _on(stream):
-            rows = torch.arange(0, 2 * q.shape[0], q.shape[0], dtype=torch.int32, device=q.device)  # [0, T]
-            act = moe.moe_fp8_grouped_gemm_swiglu(q, s, self.gate_up.q[None], self.gate_up.s[None], rows, q.shape[0],
+            rows = torch.arange(0, 2 * tokens, max(tokens, 1), dtype=torch.int32, device=q.device)  # [0, T]
+            act = moe.moe_fp8_grouped_gemm_swiglu(q, s, self.gate_up.q[None], self.gate_up.s[None], rows, tokens,
                                                   limit=self.limit, stream=stream)
             y = moe.moe_fp8_gemm(*act, self.down.q, self.down.s, stream=stream)
         return _result(y, stream)

@@ -103,3 +103,9 @@ def test_shared_expert_is_in_one_part_only():
 def test_weight_of_another_rank_is_refused(shape):
     with pytest.raises(ValueError, match="w: need"):
         fp8.Fp8Weight.quantise(torch.zeros(shape))
+
+
+def test_shared_expert_without_tokens(calls):
+    Side.current = None
+    shared = fp8.Fp8SharedExpert(weight(256, 64), weight(64, 128))
+    assert shared.forward(torch.zeros(0, 64).to(torch.float8_e4m3fn), torch.ones(0, 1)).shape == (0, 64)

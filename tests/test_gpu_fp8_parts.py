@@ -33,3 +33,11 @@ def test_parts_with_a_shared_expert_add_up():
     assert ((total - whole).abs() <= 2.0 ** -8 * (mags + whole.abs())).all()
     assert float((whole - routed).norm() / whole.norm()) > 0.3  # the shared expert is a good part of it
     assert moe.moe_get_device_error() == 0
+
+
+def test_shared_expert_without_tokens():
+    sg, sd = make(1, 256, 128, 70)
+    shared = fp8.Fp8SharedExpert(fp8.Fp8Weight.quantise(sg[0]), fp8.Fp8Weight.quantise(sd[0]))
+    y = shared.forward(*moe.moe_fp8_quantize_rows(rand((0, 256), 1)))
+    assert y.shape == (0, 256) and y.dtype == torch.bfloat16
+    assert moe.moe_get_device_error() == 0
