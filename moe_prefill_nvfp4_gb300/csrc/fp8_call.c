@@ -78,12 +78,9 @@ static int unit_columns(const Tensor* t, const char* name) {
   return 0;
 }
 
-/* Row stride; a single row's, which torch leaves arbitrary, counts as whole pieces of `piece` elements. */
+/* Row stride; a single row has none, whatever its tensor says: it counts as whole pieces of `piece` elements. */
 static int64_t row_stride(const Tensor* t, int64_t piece) {
-  const int64_t ld = t->stride[t->nd - 2], cols = t->shape[t->nd - 1];
-  if (t->shape[t->nd - 2] > 1) return ld;
-  const int64_t least = ceil_div(cols, piece) * piece;
-  return ld > least ? ld : least;
+  return t->shape[t->nd - 2] > 1 ? t->stride[t->nd - 2] : ceil_div(t->shape[t->nd - 1], piece) * piece;
 }
 
 static int same_shape(const Tensor* t, const char* name, int64_t rows, int64_t cols) {
