@@ -468,7 +468,7 @@ def _fp8():
         lib()
         path = _build.call_path()
         if not os.path.exists(path):
-            raise FileNotFoundError(f"call module not built: {path}")
+            _build.build_call_module()  # (another interpreter's build, or one that could not make it: why)
         spec = importlib.util.spec_from_file_location("_fp8_call", path)
         m = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(m)

@@ -3,9 +3,12 @@
 Each ``csrc/*.cu`` file is compiled in parallel (``-gencode arch=compute_103a,code=sm_103a``),
 then linked into one shared library against the shared CUDA runtime (the same libcudart that
 PyTorch loads, so streams and the primary context are shared) and nothing else: every product,
-the shared expert's dense ones included, runs in this library's own kernels.  No cmake, no torch extension machinery: the library exports a plain C ABI
-(``include/moe_prefill.h``).  ``csrc/fp8_call.c``, the FP8 calls' argument marshalling, becomes the
-extension module ``lib/_fp8_call.so`` beside it (the host compiler and Python's own headers, no others).
+the shared expert's dense ones included, runs in this library's own kernels.  No cmake, no torch
+extension machinery: the library exports a plain C ABI (``include/moe_prefill.h``).
+``csrc/fp8_call.c``, the FP8 calls' argument marshalling, becomes the extension module
+``lib/_fp8_call<suffix>.so`` beside it, one for each interpreter that built it (the host compiler
+and Python's own headers, no others).  Where it cannot be built the library still is:
+``build`` warns, and the FP8 calls, which need it, fail with the compiler's message.
 """
 
 from __future__ import annotations
@@ -16,6 +19,7 @@ import shutil
 import subprocess
 import sys
 import sysconfig
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -41,24 +45,61 @@ def lib_path() -> str:
 
 
 def call_path() -> str:
-    return os.path.join(LIBDIR, "_fp8_call.so")
+    return os.path.join(LIBDIR, "_fp8_call" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
 
 
-def _newest_input() -> float:
-    files = sources() + [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h", ".c"))]
-    files.append(os.path.join(ROOT, "include", "moe_prefill.h"))
-    files.append(os.path.abspath(__file__))
-    return max(os.path.getmtime(f) for f in files)
+CALL_SOURCE = os.path.join(CSRC, "fp8_call.c")
+HEADER = os.path.join(ROOT, "include", "moe_prefill.h")
+
+
+def _newer(path: str, inputs) -> bool:
+    return os.path.exists(path) and os.path.getmtime(path) >= max(os.path.getmtime(f) for f in inputs)
+
+
+def _library_up_to_date() -> bool:
+    headers = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))]
+    return _newer(lib_path(), sources() + headers + [HEADER, os.path.abspath(__file__)])
+
+
+def _call_up_to_date() -> bool:
+    return _newer(call_path(), [CALL_SOURCE, HEADER, os.path.abspath(__file__)])
 
 
 def up_to_date() -> bool:
-    return all(os.path.exists(p) and os.path.getmtime(p) >= _newest_input() for p in (lib_path(), call_path()))
+    return _library_up_to_date() and _call_up_to_date()
+
+
+def build_call_module() -> str:
+    """Compiles the FP8 calls' argument marshalling for this interpreter; raises with the compiler's message."""
+    tmp = call_path() + ".tmp"
+    cmd = [os.environ.get("CC", "gcc"), "-O2", "-fPIC", "-shared", "-I", sysconfig.get_paths()["include"], "-I",
+           os.path.join(ROOT, "include"), CALL_SOURCE, "-o", tmp, "-L", LIBDIR, "-l:" + LIBNAME, "-Wl,-rpath,$ORIGIN"]
+    try:
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        failed = r.stderr if r.returncode != 0 else None
+    except OSError as e:
+        failed = str(e)
+    if failed is not None:
+        if os.path.exists(call_path()):  # (of older sources)
+            os.remove(call_path())
+        raise RuntimeError(f"building the FP8 calls' module failed:\n{failed}")
+    os.replace(tmp, call_path())
+    return call_path()
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = False) -> str:
-    """Compile and link; returns the library path.  Rebuilds only when a source is newer."""
-    if not force and up_to_date():
-        return lib_path()
+    """Compile and link; returns the library path.  Rebuilds only what has a newer source."""
+    if force or not _library_up_to_date():
+        _build_library(verbose, ptxas_verbose)
+    if force or not _call_up_to_date():
+        try:
+            build_call_module()
+        except RuntimeError as e:
+            warnings.warn(f"no FP8 calls: {e}", RuntimeWarning)
+    return lib_path()
+
+
+def _build_library(verbose: bool, ptxas_verbose: bool) -> None:
     nvcc = nvcc_path()
     objdir = os.path.join(LIBDIR, "obj")
     os.makedirs(objdir, exist_ok=True)
@@ -89,15 +130,6 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stderr}")
     os.replace(tmp, lib_path())
-    tmp = call_path() + ".tmp"
-    cmd = [os.environ.get("CC", "gcc"), "-O2", "-fPIC", "-shared", "-I", sysconfig.get_paths()["include"], "-I",
-           os.path.join(ROOT, "include"), os.path.join(CSRC, "fp8_call.c"), "-o", tmp, "-L", LIBDIR,
-           "-l:" + LIBNAME, "-Wl,-rpath,$ORIGIN"]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"building the call module failed:\n{r.stderr}")
-    os.replace(tmp, call_path())
-    return lib_path()
 
 
 if __name__ == "__main__":
