@@ -177,6 +177,14 @@ def _stream(stream=None):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+def _used_on(t: torch.Tensor, stream):
+    """`t`, a workspace of this call alone, is dropped on return: its memory may be handed out again behind its
+    use on `stream` only (None: the current stream, whose allocations are ordered behind it anyway)."""
+    if stream is not None:
+        t.record_stream(stream if isinstance(stream, torch.cuda.Stream)
+                        else torch.cuda.ExternalStream(stream.cuda_stream))
+
+
 def _need(t: torch.Tensor, dtype, name: str):
     if not t.is_cuda or t.dtype != dtype or not t.is_contiguous():
         raise ValueError(f"{name}: need a contiguous CUDA {dtype} tensor, got {t.dtype} on {t.device}")
@@ -263,6 +271,7 @@ def moe_sort_by_expert(ids: torch.Tensor, E: int, ws: Optional[torch.Tensor] = N
     need = moe_sort_workspace_bytes(T, k, E)
     if ws is None:
         ws = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
+        _used_on(ws, stream)
     _check(lib().moe_sort_by_expert(_ptr(ids), T, k, E, _ptr(out["sorted_token_ids"]), _ptr(out["sorted_expert_ids"]),
                                     _ptr(out["expert_offsets"]), _ptr(out["token_to_perm"]), _ptr(ws), ws.numel(),
                                     _stream(stream)), "moe_sort_by_expert")
@@ -446,6 +455,7 @@ def moe_shared_expert_forward(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch
     I = w_gate.shape[0]
     if ws is None:
         ws = torch.empty(max(moe_shared_expert_workspace_bytes(T, H, I), 1), dtype=torch.uint8, device=x.device)
+        _used_on(ws, stream)
     if out is None:
         out = torch.empty(T, H, dtype=torch.bfloat16, device=x.device)
     _check(lib().moe_shared_expert_forward(_ptr(x), T, H, I, _ptr(w_gate), _ptr(w_up), _ptr(w_down), limit, _ptr(ws),
