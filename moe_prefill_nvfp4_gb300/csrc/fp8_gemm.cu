@@ -1362,9 +1362,12 @@ int launch(const Fp8Gemm& d, cudaStream_t st) {
     if (rows <= 32) return launch_few<FewCfg<16, 3, 2>, GATHER>(d, token_tiles(d, 16) * ng2, st);
     return launch_few<FewCfg<32, 5, 1>, GATHER>(d, token_tiles(d, 32) * ng2, st);
   }
-  // The plain form's k blocks shared by a cluster where tiles leave half of the SMs idle and are long (333 x
-  // 1536 x 5120: 11.8 us against 16.9; 333 x 1536 x 2048, 16 k blocks: 9.9 against 9.4)
-  if (!a.half && idle && a.K > 23 * BK) return launch_wide<WideCfg<1, GATHER, false, true>>(d, wide_tiles, st);
+  // The plain form's k blocks shared by a cluster where tiles leave half of the SMs idle and are long: from 18 k
+  // blocks on, where both cluster sizes cross the time of a CTA alone.  Four CTAs to a tile (333 x 1536): K =
+  // 2176 9.46 us against 9.40, 2304 9.46 against 9.74, 2944 9.86 against 11.29, 5120 11.5 against 16.9; two
+  // (1100 x 1024): 2176 9.85 against 9.58, 2304 9.92 against 9.92, 2944 10.9 against 11.6.  (Very few tiles
+  // cross earlier: 140 x 256, K = 2048 8.17 against 8.93, 1536 7.86 against 7.70.)
+  if (!a.half && idle && a.K > 17 * BK) return launch_wide<WideCfg<1, GATHER, false, true>>(d, wide_tiles, st);
   if (a.half) return launch_wide<WideCfg<2, GATHER, true>>(d, tt * ng2, st);
   // 128 weight rows to a tile where tiles of 256 would not fill the SMs
   if (tt * ng2 < device_sm_count()) return launch_wide<WideCfg<1, GATHER, false>>(d, tt * ((a.N + 127) / 128), st);
