@@ -366,7 +366,8 @@ int moe_fp8_grouped_gemm(const moe_fp8_rows* A, const int32_t* gather_ids, const
  *   act[p, j] = silu(min(g, L)) * clamp(u, -L, L)  of the FP32 sums g = C[p, j], u = C[p, I + j]
  * is quantised per row and 128 columns as by moe_fp8_quantize_rows (its FP32 values, no BF16
  * rounding between): act device E4M3 [R, ld_act], act_s its scales -- the A of the down product.
- * A NaN sum gives a NaN act.  Rows of experts W does not hold are quantised zeros.
+ * A NaN sum gives a NaN act.  L > 0; an infinite L clamps nothing.  The activation is within 2^-20 of its
+ * formula on the sums.  Rows of experts W does not hold are quantised zeros.
  */
 int moe_fp8_grouped_gemm_swiglu(const moe_fp8_rows* A, const int32_t* gather_ids, const moe_fp8_weight* W,
                                 const int32_t* expert_offsets, int E, int R, float limit, uint8_t* act, int64_t ld_act,

@@ -1,9 +1,10 @@
 /* fp8_call.c -- Python argument marshalling of the FP8 calls (module _fp8_call), the part of the binding
  * whose own time counts: one token's product takes a few microseconds on the GPU, and the same marshalling
  * in Python (tensor attributes, ctypes structures, checks) took longer than that (row quantiser 9.8 us a
- * call, dense product 12.5 us; here 8.6 both, of which 2.9 and 4.1 remain when outputs are given).  It reads tensors through their Python attributes, so it
- * depends on no PyTorch header, allocates outputs with torch.empty_strided, and calls the C ABI
- * (include/moe_prefill.h), which repeats every check that matters to the device.
+ * call, dense product 12.5 us; here 8.6 both, of which 3.1 and 4.3 remain when outputs are given).  It
+ * reads tensors through their Python attributes, so it depends on no PyTorch header, allocates outputs with
+ * torch.empty_strided, and calls the C ABI (include/moe_prefill.h), which repeats every check that matters
+ * to the device, but for the GPU that the pointers belong to, which is checked here alone.
  */
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>

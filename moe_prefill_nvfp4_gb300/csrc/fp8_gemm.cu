@@ -22,11 +22,14 @@
 //   few   weight rows are the M operand (two blocks of 128 per tile), up to NT token rows the N
 //         operand: a tile of the wide kernel would be mostly empty rows.  Bound by the weights' bytes.
 //
-// Measured on GB300 (GLM sizes: 160 experts, top-8, hidden 5120, intermediate 1536), cold weights:
-//   down product      1 token 14.8 us, 64 tokens 182 us (6.6 TB/s), 8192 tokens 576 us (1.8 PFLOP/s)
-//   gate/up + SwiGLU  4 tokens 80 us, 64 tokens 351 us (6.9 TB/s), 8192 tokens 1100 us (1.9 PFLOP/s; with
-//                     rows that need no gathering 1020)
-//   dense             8192 x 1536 x 5120 59 us (2.2 PFLOP/s), 1 x 5120 x 1536 5.8 us
+// Measured on GB300 (GLM sizes: 160 experts, top-8, hidden 5120, intermediate 1536), cold weights, the kernels
+// alone (in CUDA graphs of 12 launches, some 20 ms of them):
+//   down product      1 token 15.1 us, 64 tokens 182 us (6.6 TB/s), 8192 tokens 577 us (1.8 PFLOP/s)
+//   gate/up + SwiGLU  4 tokens 81 us, 64 tokens 352 us (6.9 TB/s), 8192 tokens 1102 us (1.9 PFLOP/s; with
+//                     rows that need no gathering 1014)
+//   dense             8192 x 1536 x 5120 58 us (2.2 PFLOP/s), 1 x 5120 x 1536 5.8 us
+// In a loop of seconds the power limit takes the SM clock from 2.07 to 1.68 GHz and the 8192-token products
+// to 607 and 1215 us.
 //
 // gate/up form: the tile's two blocks are a gate block and the matching up block, and the tile's
 // output is a 128-column group of act = silu(min(g, L)) * clamp(u, -L, L), quantised in the
@@ -560,7 +563,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     // ------------------------------------------------------------------ gathered token rows
     // 16-byte cp.async into the swizzled layout (chunk c of row r at c ^ (r % 8)): 8 lanes to a row of
     // the k block, 4 rows to an instruction, every fourth group of 4 rows to a warp (gate/up of 2048 tokens at
-    // 40 experts 284 us; rows gathered by TMA gather4 689, rows that need no gathering 260).  Sixteens of rows
+    // 40 experts 286 us; rows gathered by TMA gather4 689, rows that need no gathering 260).  Sixteens of rows
     // past the tile's are left as they are (their accumulator rows are not stored), single rows repeat its last.
     reg_dec<C::REG_LOW>();
     const int r0 = (warp - 12) * 4 + (lane >> 3);  // rows r0 + 16 j: the same chunk place in all of them
@@ -1349,13 +1352,13 @@ int launch(const Fp8Gemm& d, cudaStream_t st) {
   const int64_t tt = token_tiles(d, 128);
   const int64_t wide_tiles = a.half ? tt * ng2 : tt * ((a.N + 127) / 128);
   // Few rows per expert: the few-row kernel up to 8 (at 64 experts the down product of 64 tokens, 8 rows,
-  // takes 21.1 us against the wide kernel's 23.9 and gate/up 40.5 against 40.1; at 160 experts gate/up of 64
-  // tokens, 3.2 rows, 352 against 369, of 256 tokens, 12.8 rows, 393 against 375).  Busier experts among them
+  // takes 21.2 us against the wide kernel's 24.0 and gate/up 40.5 against 41.0; at 160 experts gate/up of 64
+  // tokens, 3.2 rows, 352 against 370, of 256 tokens, 12.8 rows, 391 against 377).  Busier experts among them
   // take several of its tiles, each reading the weights again from L2: routed by a Zipf(1.2) law, 1280 rows
-  // over 160 experts take 315 us against 305, 2560 rows 425 against 359.  And up to 128 rows where the
+  // over 160 experts take 325 us against 306, 2560 rows 422 against 360.  And up to 128 rows where the
   // wide kernel's tiles would leave half of the SMs idle (64 x 1536 x 5120: 8.2 us against 16.4, with its k
-  // split 10.6; 200 rows 14.0 against 11.4 split; gate/up of one expert, 128 rows: 20.1 against 21.2, 200
-  // rows 27.7 against 21.4).  32 token rows to a tile from 33 rows on (64 rows: 8.2 us against 8.7 with 16;
+  // split 10.6; 200 rows 14.0 against 11.4 split; gate/up of one expert, 128 rows: 22.9 against 23.8, 200
+  // rows 33.6 against 23.9).  32 token rows to a tile from 33 rows on (64 rows: 8.2 us against 8.7 with 16;
   // 32 rows: 8.0 against 7.0).
   const bool idle = 2 * wide_tiles <= device_sm_count();
   if (rows <= 8 || (rows <= 128 && idle)) {

@@ -60,7 +60,7 @@ class Fp8Weight:
 
 
 class Fp8SharedExpert:
-    """A dense SwiGLU MLP: gate_up [2I, H] (gate rows first), down [H, I]."""
+    """A dense SwiGLU MLP: gate_up [2I, H] (gate rows first), down [H, I].  ``limit``: as for ``Fp8Experts``."""
 
     def __init__(self, gate_up: Fp8Weight, down: Fp8Weight, limit: float = 7.0):
         self.gate_up, self.down, self.limit = gate_up, down, limit
@@ -80,7 +80,8 @@ class Fp8SharedExpert:
 class Fp8Experts:
     """E routed experts, gate_up [count, 2I, H] and down [count, H, I]: all of them, or the ``count`` experts
     from ``first`` on of ``num_experts`` (expert parallelism: the others' part of the result is zero, and the
-    caller adds the ranks' results; the shared expert, which is in one of them only, goes with expert 0)."""
+    caller adds the ranks' results; the shared expert, which is in one of them only, goes with expert 0).
+    Gates are clamped to at most ``limit`` and ups to +-``limit`` before the SwiGLU; float("inf") clamps nothing."""
 
     def __init__(self, gate_up: Fp8Weight, down: Fp8Weight, top_k: int, num_experts: Optional[int] = None, first: int = 0,
                  limit: float = 7.0, renormalize: bool = True, routed_scale: float = 1.0,

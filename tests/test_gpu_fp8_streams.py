@@ -95,3 +95,24 @@ def test_out_on_a_stream_that_is_not_current():
     assert layer.forward(x, logits=logits, out=out, stream=side) is out
     side.synchronize()
     assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("given", [False, True], ids=["current", "given"])
+def test_captured_on_a_stream(given):
+    """A forward with a shared expert captured into a graph, the stream current or given as well."""
+    gu, dn = make(4, 512, 128, 13)
+    sg, sd = make(1, 512, 128, 21)
+    shared = fp8.Fp8SharedExpert(fp8.Fp8Weight.quantise(sg[0]), fp8.Fp8Weight.quantise(sd[0]))
+    layer = fp8.Fp8Experts(fp8.Fp8Weight.quantise(gu), fp8.Fp8Weight.quantise(dn), 2, shared=shared)
+    x, logits = rand((40, 512), 9), rand((40, 4), 10, 1.0, torch.float32)
+    want = layer.forward(x, logits=logits)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        got = layer.forward(x, logits=logits, stream=side if given else None)
+    for _ in range(2):
+        got.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
