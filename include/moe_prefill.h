@@ -336,6 +336,26 @@ int moe_fp8_quantize_blocks(const void* w, int w_dtype, int64_t ld_w, int N, int
                             void* stream);
 
 /*
+ * The step in front of the experts: residual addition, root-mean-square norm, and the row quantiser on its result,
+ *   h = x + r,  y = h / sqrt(sum_k h^2 / K + eps) * w,  (q, s) = moe_fp8_quantize_rows of y,
+ * in FP32 without rounding in between: y is made of the unrounded h, the codes of the unrounded y.
+ *   x     device BF16 or FP32 (x_dtype) [R, ld_x]
+ *   r     NULL (h = x, not stored), or device BF16 or FP32 (r_dtype) [R, ld_r]
+ *   w     device BF16 or FP32 (w_dtype) [K]
+ *   h     device [R, ld_h] of r_dtype (output); may be r itself, or x itself where the types are the same
+ *   y     NULL, or device BF16 [R, ld_y] (output): the router's operand, and the NVFP4 experts'; may be x itself
+ *         where that is BF16
+ *   q, s  device outputs, laid out as above
+ * Any alignment of the element types (operands whose rows all start on 16-byte boundaries take the wide loads).
+ * A NaN in h makes the whole row NaN; an infinity is NaN itself, and the row's others zeros.  Squares are FP32:
+ * an |h| above 2^56 may overflow them, to the same effect.  R = 0 does nothing.
+ * Requirements: 1 <= K <= 32768, eps >= 0 and finite.
+ */
+int moe_fp8_add_rms_norm(const void* x, int x_dtype, int64_t ld_x, const void* r, int r_dtype, int64_t ld_r,
+                         const void* w, int w_dtype, float eps, int R, int K, void* h, int64_t ld_h, uint16_t* y,
+                         int64_t ld_y, uint8_t* q, int64_t ld_q, float* s, int64_t s_row, int64_t s_grp, void* stream);
+
+/*
  * Dense product: C[r, n] = sum_k A[r, k] W[n, k] over the dequantised values, as
  *   sum over groups g of sa[r, g] * sw[n/128, g] * (sum over k in g of the codes' products),
  * the inner sums by FP8 tensor-core MMAs with FP32 accumulation, the outer in FP32; C is BF16
@@ -397,6 +417,59 @@ typedef struct {
  * "Module forward_prefill_gemm", "Layout compatibility": remote experts as NULL table entries,
  * the caller all-reducing out), where this library keeps multicast out; results are identical. */
 #define MOE_FWD_NO_MULTICAST 4
+
+/* ---------------------------------------------------------------- few tokens */
+/*
+ * The whole layer for at most MOE_FEW_MAX_TOKENS tokens (a decode batch, drafted tokens to verify), in two
+ * launches: routing, gate/up products with the clamped SwiGLU, down products and the weighted sum,
+ *   out[t] = sum_s wts[t, s] * W_dn[e] act(W_gu[e] x[t])  (+ shared),  e = ids[t, s],
+ * with ids and wts as moe_route_topk gives them.  Bound by the bytes of the picked experts' weights; nothing
+ * but them is large.  Logits, sums, activations and the down products are FP32; out is rounded to BF16 once.
+ * The order of every sum depends on sizes alone: the same call gives the same bits.
+ *
+ * cfg: hidden, moe_intermediate, num_experts (<= MOE_FEW_MAX_EXPERTS), top_k (<= 32), swiglu_limit (> 0, infinity
+ * clamps nothing), renormalize, routed_scale; flags 0 or MOE_FWD_NO_MULTICAST (there is none to leave out).
+ *   x          device BF16 [T, H], 1 <= T <= MOE_FEW_MAX_TOKENS
+ *   w_router   device BF16 [E, H] or NULL; logits device FP32 [T, E] or NULL (exactly one of them);
+ *   router_bias device FP32 [E] or NULL (selection only)
+ *   ws         device workspace of moe_few_workspace_bytes, 256-byte aligned; its contents need not be kept or
+ *              cleared between calls, and calls that can overlap need one each
+ *   out        device BF16 [T, H]
+ * No host round trip: capturable.  A call that shares the GPU with another kernel waits for no CTA that is not
+ * running.
+ *
+ * moe_fp8_few_forward: experts in block-scaled FP8 (see FP8 experts), with activations quantised per row and 128
+ * columns as the chunk path does it.
+ *   rows       NULL: x is quantised as by moe_fp8_quantize_rows; or T rows already quantised, any scale layout
+ *              (moe_fp8_add_rms_norm's), and x is the router's operand alone (NULL with logits)
+ *   gate_up, down  [count][2 I, H] and [count][H, I], both the experts first .. first + count - 1; slots of
+ *              experts held elsewhere add nothing
+ *   shared_gate_up, shared_down  NULL, or a shared expert [2 Is, H] and [H, Is] (count 1; first is not read) with
+ *              its own clamp shared_limit; it goes with first = 0
+ * Requirements: H, I and Is multiples of 128.
+ *
+ * moe_w4a16_few_forward: experts in NVFP4 tables (absent ones add nothing).  The weights are exact (E2M1 x E4M3
+ * in FP16, scale2 on the FP32 sums), x and the activations FP16 times a power of two per 128 columns: x exactly
+ * down to 2^-31 of its group's largest magnitude (and to 2^-39 of that below), the activations to 2^-12 of their
+ * value.  g and u are not rounded to BF16 (as in the small-row products).
+ *   shared_out device BF16 [T, H] or NULL, added to out
+ * Requirements: H and I multiples of 256.
+ */
+#define MOE_FEW_MAX_TOKENS 16
+#define MOE_FEW_MAX_EXPERTS 512
+
+/* fp8: 1 for moe_fp8_few_forward (shared_intermediate Is, 0 without), 0 for moe_w4a16_few_forward; 0 bytes on bad
+ * sizes. */
+size_t moe_few_workspace_bytes(const moe_prefill_config* cfg, int fp8, int shared_intermediate, int T);
+int moe_fp8_few_forward(const moe_prefill_config* cfg, const uint16_t* x, const moe_fp8_rows* rows, int T,
+                        const uint16_t* w_router, const float* logits, const float* router_bias,
+                        const moe_fp8_weight* gate_up, const moe_fp8_weight* down, const moe_fp8_weight* shared_gate_up,
+                        const moe_fp8_weight* shared_down, float shared_limit, void* ws, size_t ws_bytes, uint16_t* out,
+                        void* stream);
+int moe_w4a16_few_forward(const moe_prefill_config* cfg, const uint16_t* x, int T, const uint16_t* w_router,
+                          const float* logits, const float* router_bias, const moe_expert_table* w_gate_up,
+                          const moe_expert_table* w_down, const uint16_t* shared_out, void* ws, size_t ws_bytes,
+                          uint16_t* out, void* stream);
 
 /* Workspace bytes for moe_prefill_forward with up to max_rows rows (0 on a bad config). */
 size_t moe_workspace_bytes(const moe_prefill_config* cfg, int max_rows);

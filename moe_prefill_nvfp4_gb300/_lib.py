@@ -31,7 +31,8 @@ __all__ = [
     "moe_debug_set_gemm_kernel", "moe_debug_set_wait_limit_ns", "MOE_GEMM_KERNEL_AUTO", "MOE_GEMM_KERNEL_SINGLE",
     "MOE_GEMM_KERNEL_PAIR", "gemm_kernel", "moe_debug_grouped_gemm_after",
     "moe_fp8_quantize_rows", "moe_fp8_quantize_blocks", "moe_fp8_gemm", "moe_fp8_grouped_gemm",
-    "moe_fp8_grouped_gemm_swiglu", "MOE_FP8_BLOCK", "MOE_FP8_MAX_EXPERTS",
+    "moe_fp8_grouped_gemm_swiglu", "MOE_FP8_BLOCK", "MOE_FP8_MAX_EXPERTS", "moe_fp8_add_rms_norm",
+    "moe_few_workspace_bytes", "moe_fp8_few_forward", "moe_w4a16_few_forward", "MOE_FEW_MAX_TOKENS",
 ]
 
 HEADER = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include", "moe_prefill.h")
@@ -49,6 +50,7 @@ MOE_GEMM_KERNEL_SINGLE = 1  # the single-CTA kernel
 MOE_GEMM_KERNEL_PAIR = 2  # the CTA-pair kernel only (other shapes are refused)
 MOE_FP8_BLOCK = 128  # elements per scale of the FP8 formats (rows: 128 columns, weights: 128 x 128)
 MOE_FP8_MAX_EXPERTS = 512
+MOE_FEW_MAX_TOKENS = 16  # tokens of moe_fp8_few_forward and moe_w4a16_few_forward
 STATUS = {0: "MOE_OK", 1: "MOE_ERR_INVALID_ARG", 2: "MOE_ERR_UNSUPPORTED_SHAPE", 3: "MOE_ERR_WORKSPACE_TOO_SMALL",
           4: "MOE_ERR_CUDA", 5: "MOE_ERR_DEVICE", 6: "MOE_ERR_NOT_BUILT_FOR_DEVICE", 7: "MOE_ERR_SCRATCH_LIMIT"}
 DEVERR = {0: "none", 1: "bad expert id", 2: "bad expert offsets", 3: "pipeline wait timeout", 4: "NaN logit",
@@ -123,6 +125,13 @@ _SIGS = {
                                   _P]),
     "moe_fp8_grouped_gemm_swiglu": (_I, [ctypes.POINTER(Fp8Rows), _P, ctypes.POINTER(Fp8Weight), _P, _I, _I, _F, _P,
                                          _I64, _P, _I64, _I64, _P]),
+    "moe_fp8_add_rms_norm": (_I, [_P, _I, _I64, _P, _I, _I64, _P, _I, _F, _I, _I, _P, _I64, _P, _I64, _P, _I64, _P, _I64,
+                                  _I64, _P]),
+    "moe_few_workspace_bytes": (_SZ, [ctypes.POINTER(MoePrefillConfig), _I, _I, _I]),
+    "moe_fp8_few_forward": (_I, [ctypes.POINTER(MoePrefillConfig), _P, ctypes.POINTER(Fp8Rows), _I, _P, _P, _P,
+                                 ctypes.POINTER(Fp8Weight), ctypes.POINTER(Fp8Weight), ctypes.POINTER(Fp8Weight),
+                                 ctypes.POINTER(Fp8Weight), _F, _P, _SZ, _P, _P]),
+    "moe_w4a16_few_forward": (_I, [ctypes.POINTER(MoePrefillConfig), _P, _I, _P, _P, _P, _P, _P, _P, _P, _SZ, _P, _P]),
     "moe_get_device_error": (_I, [_P, ctypes.POINTER(_I)]),
     "moe_debug_set_gemm_kernel": (_I, [_I]),
     "moe_debug_set_wait_limit_ns": (ctypes.c_ulonglong, [ctypes.c_ulonglong]),
@@ -530,6 +539,62 @@ def moe_fp8_grouped_gemm_swiglu(A: torch.Tensor, a_scales: torch.Tensor, W: torc
     (E4M3 [R, I], FP32 [R, I/128]), the operands of the down product."""
     return (_FP8 or _fp8()).grouped_swiglu(A, a_scales, W, w_scales, expert_offsets, R, limit, gather_ids, first, out,
                                            scales, stream)
+
+
+def moe_fp8_add_rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Tensor] = None,
+                         eps: float = 1e-6, normed=False, residual_out: Optional[torch.Tensor] = None,
+                         out: Optional[torch.Tensor] = None, scales: Optional[torch.Tensor] = None, stream=None):
+    """h = x + residual, y = h / sqrt(mean(h^2) + eps) * weight and the row quantiser of y in one pass:
+    (E4M3 [R, K], FP32 [R, ceil(K/128)], h or None without a residual, BF16 y or None).  x, residual and weight
+    are BF16 or FP32 each, of any row stride; h has the residual's type, in ``residual_out`` (which may be the
+    residual itself) or a new tensor.  ``normed``: True for y, or the tensor it goes to."""
+    return (_FP8 or _fp8()).add_rms_norm(x, weight, residual, eps, normed, residual_out, out, scales, stream)
+
+
+# ------------------------------------------------------------------------------------------ few tokens
+
+
+def moe_few_workspace_bytes(cfg: MoePrefillConfig, T: int, fp8: bool, shared_intermediate: int = 0) -> int:
+    return int(lib().moe_few_workspace_bytes(ctypes.byref(cfg), int(fp8), shared_intermediate, T))
+
+
+def _few_ws(cfg: MoePrefillConfig, T: int, fp8: bool, shared_intermediate: int, device, stream) -> torch.Tensor:
+    ws = torch.empty(max(moe_few_workspace_bytes(cfg, T, fp8, shared_intermediate), 1), dtype=torch.uint8, device=device)
+    _used_on(ws, stream)
+    return ws
+
+
+def moe_fp8_few_forward(x: Optional[torch.Tensor], w_gate_up: torch.Tensor, s_gate_up: torch.Tensor, w_down: torch.Tensor,
+                        s_down: torch.Tensor, top_k: int, w_router: Optional[torch.Tensor] = None,
+                        logits: Optional[torch.Tensor] = None, router_bias: Optional[torch.Tensor] = None,
+                        limit: float = 7.0, renormalize: bool = True, routed_scale: float = 1.0,
+                        num_experts: Optional[int] = None, first: int = 0, shared: Optional[tuple] = None,
+                        shared_limit: Optional[float] = None, rows: Optional[tuple] = None,
+                        ws: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """A whole layer of FP8 experts for up to ``MOE_FEW_MAX_TOKENS`` tokens: BF16 [T, H].  The weights are those of
+    the grouped products, [experts, 2I, H] and [experts, H, I] from expert ``first`` on of ``num_experts``.
+    ``rows``: the tokens' codes and scales where they are quantised already; x is then only the router's (None
+    with ``logits``).  ``shared``: (gate_up, its scales, down, its scales) of a shared expert, clamped at
+    ``shared_limit`` (default: limit).  ``ws``: a workspace of this call's own, of any contents."""
+    if ws is None and stream is not None and w_down.dim() == 3:
+        t = x if x is not None else rows[0]
+        cfg = MoePrefillConfig(t.shape[1], w_down.shape[2], num_experts or w_down.shape[0], top_k)
+        ws = _few_ws(cfg, t.shape[0], True, shared[2].shape[1] if shared is not None else 0, t.device, stream)
+    return (_FP8 or _fp8()).few_fp8(x, w_gate_up, s_gate_up, w_down, s_down, top_k, w_router, logits, router_bias, limit,
+                                    renormalize, routed_scale, num_experts, first, shared,
+                                    limit if shared_limit is None else shared_limit, rows, ws, out, stream)
+
+
+def moe_w4a16_few_forward(cfg: MoePrefillConfig, x: torch.Tensor, w_gate_up: ExpertTable, w_down: ExpertTable,
+                          w_router: Optional[torch.Tensor] = None, logits: Optional[torch.Tensor] = None,
+                          router_bias: Optional[torch.Tensor] = None, shared_out: Optional[torch.Tensor] = None,
+                          ws: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """A whole layer of NVFP4 experts for up to ``MOE_FEW_MAX_TOKENS`` tokens x BF16 [T, H]: BF16 [T, H], plus
+    ``shared_out`` BF16 [T, H].  ``ws``: a workspace of this call's own, of any contents."""
+    if ws is None and stream is not None:
+        ws = _few_ws(cfg, x.shape[0], False, 0, x.device, stream)
+    return (_FP8 or _fp8()).few_w4(cfg, x, w_gate_up.handle, w_down.handle, w_router, logits, router_bias, shared_out, ws, out,
+                                   stream)
 
 
 def moe_get_device_error(stream=None) -> int:

@@ -104,6 +104,12 @@ int device_sm_count() {
   return d < 0 ? 0 : g_sm_count[d];
 }
 
+int current_device_index() { return current_device(); }
+
+ExpertTableView expert_table_view(const moe_expert_table* t) {
+  return ExpertTableView{t->E, t->N, t->K, t->device, t->d_packed, t->d_scales, t->d_scale2};
+}
+
 int* device_error_word() {
   const int d = current_device();
   return d < 0 ? nullptr : g_err_addr[d];

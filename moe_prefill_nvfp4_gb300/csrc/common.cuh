@@ -128,6 +128,8 @@ MOE_DEV void counter_add_release(int* p, int v) {
 // Orders this thread's earlier generic-proxy accesses (e.g. an acquire of data that other threads
 // stored) before its later async-proxy (TMA) accesses of global memory.
 MOE_DEV void fence_proxy_async_global() { asm volatile("fence.proxy.async.global;" ::: "memory"); }
+// The same for shared memory of the CTA.
+MOE_DEV void fence_proxy_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 // Cluster-scope mbarrier operations on the barrier at the same shared offset in CTA `rank`:
 // arrive with release (orders this thread's earlier st.shared::cluster), and a local wait with

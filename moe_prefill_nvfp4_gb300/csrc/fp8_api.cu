@@ -101,6 +101,46 @@ int moe_fp8_quantize_blocks(const void* w, int w_dtype, int64_t ld_w, int N, int
   return fp8_quantize_blocks_launch(w, w_dtype, ld_w, N, K, q, ld_q, s, as_stream(stream));
 }
 
+int moe_fp8_add_rms_norm(const void* x, int x_dtype, int64_t ld_x, const void* r, int r_dtype, int64_t ld_r,
+                         const void* w, int w_dtype, float eps, int R, int K, void* h, int64_t ld_h, uint16_t* y,
+                         int64_t ld_y, uint8_t* q, int64_t ld_q, float* s, int64_t s_row, int64_t s_grp, void* stream) {
+  if (x == nullptr || w == nullptr || q == nullptr || s == nullptr || !dtype_ok(x_dtype) || !dtype_ok(w_dtype))
+    return MOE_ERR_INVALID_ARG;
+  if (r != nullptr && (h == nullptr || !dtype_ok(r_dtype))) return MOE_ERR_INVALID_ARG;
+  if (!(eps >= 0.f) || eps > 3.402823466e38f) return MOE_ERR_INVALID_ARG;
+  if (R < 0 || K < 1 || K > kRmsNormMaxK || ld_x < K || (r != nullptr && (ld_r < K || ld_h < K)) ||
+      (y != nullptr && ld_y < K))
+    return MOE_ERR_UNSUPPORTED_SHAPE;
+  auto at = [](const void* p, int dtype) { return aligned(p, dtype == MOE_DTYPE_BF16 ? 2 : 4); };
+  if (!codes_ok(q, ld_q, K) || !aligned(s, 4) || !at(x, x_dtype) || !at(w, w_dtype) || !aligned(y, 2) ||
+      (r != nullptr && (!at(r, r_dtype) || !at(h, r_dtype))))
+    return MOE_ERR_INVALID_ARG;
+  const int rc = ensure_device();
+  if (rc != MOE_OK || R == 0) return rc;
+  RmsNormArgs a = {};
+  a.x = x;
+  a.r = r;
+  a.w = w;
+  a.h = h;
+  a.y = y;
+  a.q = q;
+  a.s = s;
+  a.ld_x = ld_x;
+  a.ld_r = ld_r;
+  a.ld_h = ld_h;
+  a.ld_y = ld_y;
+  a.ld_q = ld_q;
+  a.s_row = s_row;
+  a.s_grp = s_grp;
+  a.R = R;
+  a.K = K;
+  a.eps = eps;
+  a.x_bf16 = x_dtype == MOE_DTYPE_BF16;
+  a.r_bf16 = r_dtype == MOE_DTYPE_BF16;
+  a.w_bf16 = w_dtype == MOE_DTYPE_BF16;
+  return rms_norm_launch(a, as_stream(stream));
+}
+
 int moe_fp8_gemm(const moe_fp8_rows* A, const moe_fp8_weight* W, void* C, int64_t ldc, int c_dtype, void* stream) {
   if (A == nullptr || W == nullptr) return MOE_ERR_INVALID_ARG;
   if (W->first != 0 || W->count != 1) return MOE_ERR_UNSUPPORTED_SHAPE;

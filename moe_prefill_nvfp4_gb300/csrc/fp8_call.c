@@ -229,37 +229,38 @@ static PyObject* quantize(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   return pair_or_fail(rc, blocks ? "moe_fp8_quantize_blocks" : "moe_fp8_quantize_rows", tq, ts);
 }
 
-/* activation rows [rows, K] with their scales and a weight [N, K] (nd 2) or [experts, N, K] (nd 3) with its */
-static int operands(PyObject* const* a, int nd, int64_t first, moe_fp8_rows* A, moe_fp8_weight* W, int* gpu) {
-  Tensor q, s, w, ws;
-  if (!read_tensor(a[0], "A", 2, g_f8, NULL, &q, gpu) || !read_tensor(a[1], "a_scales", 2, g_f32, NULL, &s, gpu) ||
-      !read_tensor(a[2], "W", nd, g_f8, NULL, &w, gpu) || !read_tensor(a[3], "w_scales", nd, g_f32, NULL, &ws, gpu))
-    return 0;
-  const int64_t N = w.shape[nd - 2], K = w.shape[nd - 1], G = ceil_div(K, 128), NB = ceil_div(N, 128);
-  if (q.shape[1] != K) {
-    PyErr_Format(PyExc_ValueError, "A, W: %lld and %lld columns", (long long)q.shape[1], (long long)K);
-    return 0;
-  }
-  if (!unit_columns(&q, "A") || !unit_columns(&w, "W") || !same_shape(&s, "a_scales", q.shape[0], G) ||
-      !same_shape(&ws, "w_scales", NB, G))
-    return 0;
-  const int64_t count = nd == 3 ? w.shape[0] : 1;
-  if (nd == 3 && ws.shape[0] != count) {
-    PyErr_Format(PyExc_ValueError, "w_scales: need %lld experts, got %lld", (long long)count, (long long)ws.shape[0]);
-    return 0;
-  }
-  if ((G > 1 && ws.stride[nd - 1] != 1) || (NB > 1 && ws.stride[nd - 2] != G) || (count > 1 && ws.stride[0] != NB * G)) {
-    PyErr_SetString(PyExc_ValueError, "w_scales: need a contiguous tensor");
-    return 0;
-  }
-  if (!fits(q.shape[0], "rows") || !fits(N, "N") || !fits(K, "K") || !fits(count, "experts") || !fits(first, "first"))
-    return 0;
+/* activation rows [rows, K] with their scales */
+static int read_rows(PyObject* tq, PyObject* ts, const char* nq, const char* ns, moe_fp8_rows* A, int64_t* K, int* gpu) {
+  Tensor q, s;
+  if (!read_tensor(tq, nq, 2, g_f8, NULL, &q, gpu) || !read_tensor(ts, ns, 2, g_f32, NULL, &s, gpu)) return 0;
+  *K = q.shape[1];
+  if (!unit_columns(&q, nq) || !same_shape(&s, ns, q.shape[0], ceil_div(*K, 128)) || !fits(q.shape[0], "rows")) return 0;
   A->q = q.ptr;
   A->ld = row_stride(&q, 16);
   A->s = s.ptr;
   A->s_row = s.stride[0];
   A->s_grp = s.stride[1];
   A->rows = (int)q.shape[0];
+  return 1;
+}
+
+/* a weight [N, K] (nd 2) or [experts, N, K] (nd 3) with its scales */
+static int read_weight(PyObject* tq, PyObject* ts, const char* nq, const char* ns, int nd, int64_t first,
+                       moe_fp8_weight* W, int* gpu) {
+  Tensor w, ws;
+  if (!read_tensor(tq, nq, nd, g_f8, NULL, &w, gpu) || !read_tensor(ts, ns, nd, g_f32, NULL, &ws, gpu)) return 0;
+  const int64_t N = w.shape[nd - 2], K = w.shape[nd - 1], G = ceil_div(K, 128), NB = ceil_div(N, 128);
+  if (!unit_columns(&w, nq) || !same_shape(&ws, ns, NB, G)) return 0;
+  const int64_t count = nd == 3 ? w.shape[0] : 1;
+  if (nd == 3 && ws.shape[0] != count) {
+    PyErr_Format(PyExc_ValueError, "%s: need %lld experts, got %lld", ns, (long long)count, (long long)ws.shape[0]);
+    return 0;
+  }
+  if ((G > 1 && ws.stride[nd - 1] != 1) || (NB > 1 && ws.stride[nd - 2] != G) || (count > 1 && ws.stride[0] != NB * G)) {
+    PyErr_Format(PyExc_ValueError, "%s: need a contiguous tensor", ns);
+    return 0;
+  }
+  if (!fits(N, "N") || !fits(K, "K") || !fits(count, "experts") || !fits(first, "first")) return 0;
   W->q = w.ptr;
   W->ld = row_stride(&w, 16);
   W->expert_stride = count > 1 ? w.stride[0] : 0;
@@ -269,6 +270,17 @@ static int operands(PyObject* const* a, int nd, int64_t first, moe_fp8_rows* A, 
   W->N = (int)N;
   W->K = (int)K;
   return 1;
+}
+
+/* the operands of a product: rows, their scales, a weight, its scales */
+static int operands(PyObject* const* a, int nd, int64_t first, moe_fp8_rows* A, moe_fp8_weight* W, int* gpu) {
+  int64_t K;
+  if (!read_rows(a[0], a[1], "A", "a_scales", A, &K, gpu) ||
+      !read_weight(a[2], a[3], "W", "w_scales", nd, first, W, gpu))
+    return 0;
+  if (K == W->K) return 1;
+  PyErr_Format(PyExc_ValueError, "A, W: %lld and %lld columns", (long long)K, (long long)W->K);
+  return 0;
 }
 
 /* gemm(A, a_scales, W, w_scales, out, c_dtype, stream) */
@@ -363,6 +375,269 @@ static PyObject* grouped_swiglu(PyObject* self, PyObject* const* a, Py_ssize_t n
   return pair_or_fail(rc, "moe_fp8_grouped_gemm_swiglu", tq, ts);
 }
 
+/* add_rms_norm(x, weight, residual, eps, normed, residual_out, out, scales, stream) -> (q, s, h or None, y or None) */
+static PyObject* add_rms_norm(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  Tensor x, w, r = {0}, h = {0}, y = {0}, q, s;
+  int64_t ld_q;
+  void* st;
+  int gpu = -1;
+  if (!want(n, 9)) return NULL;
+  const double eps = PyFloat_AsDouble(a[3]);
+  if (PyErr_Occurred() || !read_tensor(a[0], "x", 2, g_bf16, g_f32, &x, &gpu) || !unit_columns(&x, "x") ||
+      !read_tensor(a[1], "weight", 1, g_bf16, g_f32, &w, &gpu) || !unit_columns(&w, "weight") ||
+      !fits(x.shape[0], "rows") || !fits(x.shape[1], "columns"))
+    return NULL;
+  const int64_t R = x.shape[0], K = x.shape[1];
+  if (w.shape[0] != K) {
+    PyErr_Format(PyExc_ValueError, "weight: need [%lld], got [%lld]", (long long)K, (long long)w.shape[0]);
+    return NULL;
+  }
+  const int add = a[2] != Py_None;
+  if (add && (!read_tensor(a[2], "residual", 2, g_bf16, g_f32, &r, &gpu) || !same_shape(&r, "residual", R, K) ||
+              !unit_columns(&r, "residual")))
+    return NULL;
+  if (!add && a[5] != Py_None) {
+    PyErr_SetString(PyExc_ValueError, "residual_out: there is no residual");
+    return NULL;
+  }
+  if (!stream_of(a[8], gpu, &st)) return NULL;
+  PyObject* device = PyObject_GetAttr(a[0], n_device);
+  if (device == NULL) return NULL;
+  PyObject *tq = NULL, *ts = NULL, *th = NULL, *ty = NULL, *result = NULL;
+  tq = codes_out(a[6], "out", device, R, K, &q, &ld_q, &gpu);
+  if (tq != NULL) ts = output(a[7], "scales", g_f32, device, R, ceil_div(K, 128), 0, 1, &s, &gpu);
+  if (ts != NULL)
+    th = add ? output(a[5], "residual_out", r.dtype, device, R, K, K, 0, &h, &gpu) : Py_NewRef(Py_None);
+  if (th != NULL && add && !unit_columns(&h, "residual_out")) Py_CLEAR(th);
+  if (th != NULL) {
+    if (a[4] == Py_None || a[4] == Py_False)
+      ty = Py_NewRef(Py_None);
+    else
+      ty = output(a[4] == Py_True ? Py_None : a[4], "normed", g_bf16, device, R, K, K, 0, &y, &gpu);
+    if (ty != NULL && ty != Py_None && !unit_columns(&y, "normed")) Py_CLEAR(ty);
+  }
+  Py_DECREF(device);
+  if (ty != NULL) {
+    int rc = MOE_OK;
+    if (R > 0)
+      rc = moe_fp8_add_rms_norm(x.ptr, x.dtype == g_bf16 ? MOE_DTYPE_BF16 : MOE_DTYPE_F32, row_stride(&x, 1),
+                                add ? r.ptr : NULL, add && r.dtype == g_f32 ? MOE_DTYPE_F32 : MOE_DTYPE_BF16,
+                                add ? row_stride(&r, 1) : 0, w.ptr, w.dtype == g_bf16 ? MOE_DTYPE_BF16 : MOE_DTYPE_F32,
+                                (float)eps, (int)R, (int)K, add ? h.ptr : NULL, add ? row_stride(&h, 1) : 0,
+                                ty != Py_None ? y.ptr : NULL, ty != Py_None ? row_stride(&y, 1) : 0, q.ptr, ld_q, s.ptr,
+                                s.stride[0], s.stride[1], st);
+    result = rc == MOE_OK ? PyTuple_Pack(4, tq, ts, th, ty) : fail(rc, "moe_fp8_add_rms_norm");
+  }
+  Py_XDECREF(tq);
+  Py_XDECREF(ts);
+  Py_XDECREF(th);
+  Py_XDECREF(ty);
+  return result;
+}
+
+/* A contiguous tensor of `nd` dimensions or None (*ptr NULL). */
+static int read_plain(PyObject* t, const char* name, int nd, PyObject* dtype, int64_t d0, int64_t d1, const void** ptr,
+                      int* gpu) {
+  Tensor v;
+  *ptr = NULL;
+  if (t == Py_None) return 1;
+  if (!read_tensor(t, name, nd, dtype, NULL, &v, gpu)) return 0;
+  if (v.shape[0] != d0 || (nd == 2 && v.shape[1] != d1)) {
+    PyErr_Format(PyExc_ValueError, nd == 2 ? "%s: need [%lld, %lld]" : "%s: need [%lld]", name, (long long)d0, (long long)d1);
+    return 0;
+  }
+  if (!unit_columns(&v, name)) return 0;
+  if (nd == 2 && d0 > 1 && v.stride[0] != d1) {
+    PyErr_Format(PyExc_ValueError, "%s: need a contiguous tensor", name);
+    return 0;
+  }
+  *ptr = v.ptr;
+  return 1;
+}
+
+/* The workspace: `given` (a tensor of bytes), or a new one. */
+static PyObject* workspace(PyObject* given, PyObject* device, size_t bytes, void** ptr, size_t* have, int* gpu) {
+  Tensor v;
+  if (given != Py_None) {
+    PyObject *count = NULL, *at = NULL, *index = PyObject_CallMethodNoArgs(given, n_get_device);
+    const long where = index != NULL ? PyLong_AsLong(index) : -1;
+    Py_XDECREF(index);
+    if (PyErr_Occurred()) return NULL;
+    if (where != *gpu) {
+      PyErr_Format(PyExc_ValueError, "ws: on GPU %ld, the tensors before it are on GPU %d", where, *gpu);
+      return NULL;
+    }
+    PyObject* whole = PyObject_CallMethod(given, "is_contiguous", NULL);
+    if (whole == NULL) return NULL;
+    const int ok = whole == Py_True;
+    Py_DECREF(whole);
+    if (!ok) {
+      PyErr_SetString(PyExc_ValueError, "ws: need a contiguous tensor");
+      return NULL;
+    }
+    count = PyObject_GetAttrString(given, "nbytes");
+    if (count != NULL) at = PyObject_CallMethodNoArgs(given, n_data_ptr);
+    if (at != NULL) {
+      *have = PyLong_AsSize_t(count);
+      *ptr = PyLong_AsVoidPtr(at);
+    }
+    Py_XDECREF(count);
+    Py_XDECREF(at);
+    return PyErr_Occurred() ? NULL : Py_NewRef(given);
+  }
+  *have = bytes;
+  PyObject* t = output(Py_None, "ws", g_f8, device, 1, (int64_t)bytes, (int64_t)bytes, 0, &v, gpu);
+  *ptr = t != NULL ? v.ptr : NULL;
+  return t;
+}
+
+/* few_fp8(x, gate_up, its scales, down, its scales, top_k, w_router, logits, router_bias, limit, renormalize,
+ * routed_scale, num_experts, first, shared, shared_limit, rows, ws, out, stream) */
+static PyObject* few_fp8(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  Tensor x = {0}, o;
+  moe_fp8_weight gu, dn, sgu, sdn;
+  moe_fp8_rows rows;
+  const void *router, *logits, *bias;
+  void *st, *ws;
+  size_t have;
+  int gpu = -1;
+  if (!want(n, 20)) return NULL;
+  moe_prefill_config c = {0};
+  const int64_t top_k = PyLong_AsLongLong(a[5]), first = PyLong_AsLongLong(a[13]);
+  c.swiglu_limit = (float)PyFloat_AsDouble(a[9]);
+  c.renormalize = PyObject_IsTrue(a[10]);
+  c.routed_scale = (float)PyFloat_AsDouble(a[11]);
+  const float shared_limit = (float)PyFloat_AsDouble(a[15]);
+  if (PyErr_Occurred() || !fits(top_k, "top_k")) return NULL;
+  const int by_rows = a[16] != Py_None, with_shared = a[14] != Py_None;
+  if (by_rows && (!PyTuple_Check(a[16]) || PyTuple_GET_SIZE(a[16]) != 2)) {
+    PyErr_SetString(PyExc_ValueError, "rows: need a tuple of codes and scales");
+    return NULL;
+  }
+  if (with_shared && (!PyTuple_Check(a[14]) || PyTuple_GET_SIZE(a[14]) != 4)) {
+    PyErr_SetString(PyExc_ValueError, "shared: need a tuple of gate_up, its scales, down, its scales");
+    return NULL;
+  }
+  if (a[0] == Py_None && (!by_rows || a[6] != Py_None)) {
+    PyErr_SetString(PyExc_ValueError, "x: needed for the router, and where there are no rows");
+    return NULL;
+  }
+  int64_t T = 0, H = 0;
+  if (a[0] != Py_None) {
+    if (!read_tensor(a[0], "x", 2, g_bf16, NULL, &x, &gpu)) return NULL;
+    T = x.shape[0];
+    H = x.shape[1];
+    if (!unit_columns(&x, "x") || (T > 1 && x.stride[0] != H)) {
+      if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "x: need a contiguous tensor");
+      return NULL;
+    }
+  }
+  if (by_rows) {
+    int64_t K;
+    if (!read_rows(PyTuple_GET_ITEM(a[16], 0), PyTuple_GET_ITEM(a[16], 1), "rows", "rows' scales", &rows, &K, &gpu)) return NULL;
+    if (a[0] == Py_None) {
+      T = rows.rows;
+      H = K;
+    }
+    if (rows.rows != T || K != H) {
+      PyErr_Format(PyExc_ValueError, "rows: need [%lld, %lld], got [%d, %lld]", (long long)T, (long long)H, rows.rows, (long long)K);
+      return NULL;
+    }
+  }
+  if (!read_weight(a[1], a[2], "w_gate_up", "s_gate_up", 3, first, &gu, &gpu) ||
+      !read_weight(a[3], a[4], "w_down", "s_down", 3, first, &dn, &gpu))
+    return NULL;
+  if (with_shared && (!read_weight(PyTuple_GET_ITEM(a[14], 0), PyTuple_GET_ITEM(a[14], 1), "shared gate_up",
+                                   "its scales", 2, 0, &sgu, &gpu) ||
+                      !read_weight(PyTuple_GET_ITEM(a[14], 2), PyTuple_GET_ITEM(a[14], 3), "shared down", "its scales", 2,
+                                   0, &sdn, &gpu)))
+    return NULL;
+  const int64_t E = a[12] == Py_None ? gu.count : PyLong_AsLongLong(a[12]);
+  if (PyErr_Occurred() || !fits(E, "num_experts") || !fits(T, "tokens") || !fits(H, "columns")) return NULL;
+  if (!read_plain(a[6], "w_router", 2, g_bf16, E, H, &router, &gpu) ||
+      !read_plain(a[7], "logits", 2, g_f32, T, E, &logits, &gpu) ||
+      !read_plain(a[8], "router_bias", 1, g_f32, E, 0, &bias, &gpu) || !stream_of(a[19], gpu, &st))
+    return NULL;
+  c.hidden = (int)H;
+  c.moe_intermediate = dn.K;
+  c.num_experts = (int)E;
+  c.top_k = (int)top_k;
+  PyObject* device = PyObject_GetAttr(a[1], n_device);
+  if (device == NULL) return NULL;
+  PyObject *tws = NULL, *out = output(a[18], "out", g_bf16, device, T, H, H, 0, &o, &gpu);
+  if (out != NULL && (!unit_columns(&o, "out") || row_stride(&o, 1) != H)) {
+    if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "out: need a contiguous tensor");
+    Py_CLEAR(out);
+  }
+  if (out != NULL && T > 0) {
+    tws = workspace(a[17], device, moe_few_workspace_bytes(&c, 1, with_shared ? sdn.K : 0, (int)T), &ws, &have, &gpu);
+    if (tws == NULL) Py_CLEAR(out);
+  }
+  Py_DECREF(device);
+  if (out == NULL || T == 0) return out;
+  const int rc = moe_fp8_few_forward(&c, x.ptr, by_rows ? &rows : NULL, (int)T, router, logits, bias, &gu, &dn,
+                                     with_shared ? &sgu : NULL, with_shared ? &sdn : NULL, shared_limit, ws, have, o.ptr, st);
+  Py_DECREF(tws);
+  if (rc == MOE_OK) return out;
+  Py_DECREF(out);
+  return fail(rc, "moe_fp8_few_forward");
+}
+
+/* few_w4(cfg, x, gate_up's handle, down's handle, w_router, logits, router_bias, shared_out, ws, out, stream) */
+static PyObject* few_w4(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  Tensor x, o;
+  const void *router, *logits, *bias, *shared;
+  void *st, *ws, *tables[2];
+  size_t have;
+  int gpu = -1;
+  moe_prefill_config c;
+  Py_buffer view;
+  if (!want(n, 11) || PyObject_GetBuffer(a[0], &view, PyBUF_SIMPLE) < 0) return NULL;
+  const int whole = view.len == sizeof c;
+  if (whole) c = *(const moe_prefill_config*)view.buf;
+  PyBuffer_Release(&view);
+  if (!whole) {
+    PyErr_SetString(PyExc_ValueError, "cfg: need a MoePrefillConfig");
+    return NULL;
+  }
+  for (int i = 0; i < 2; ++i) {
+    PyObject* v = PyObject_GetAttrString(a[2 + i], "value");
+    if (v == NULL) return NULL;
+    tables[i] = v != Py_None ? PyLong_AsVoidPtr(v) : NULL;
+    Py_DECREF(v);
+    if (PyErr_Occurred()) return NULL;
+  }
+  if (!read_tensor(a[1], "x", 2, g_bf16, NULL, &x, &gpu)) return NULL;
+  const int64_t T = x.shape[0], H = x.shape[1], E = c.num_experts;
+  if (!unit_columns(&x, "x") || (T > 1 && x.stride[0] != H) || H != c.hidden) {
+    if (!PyErr_Occurred()) PyErr_Format(PyExc_ValueError, "x: need a contiguous tensor of %d columns", c.hidden);
+    return NULL;
+  }
+  if (!fits(T, "tokens") || !read_plain(a[4], "w_router", 2, g_bf16, E, H, &router, &gpu) ||
+      !read_plain(a[5], "logits", 2, g_f32, T, E, &logits, &gpu) ||
+      !read_plain(a[6], "router_bias", 1, g_f32, E, 0, &bias, &gpu) ||
+      !read_plain(a[7], "shared_out", 2, g_bf16, T, H, &shared, &gpu) || !stream_of(a[10], gpu, &st))
+    return NULL;
+  PyObject* device = PyObject_GetAttr(a[1], n_device);
+  if (device == NULL) return NULL;
+  PyObject *tws = NULL, *out = output(a[9], "out", g_bf16, device, T, H, H, 0, &o, &gpu);
+  if (out != NULL && (!unit_columns(&o, "out") || row_stride(&o, 1) != H)) {
+    if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "out: need a contiguous tensor");
+    Py_CLEAR(out);
+  }
+  if (out != NULL && T > 0) {
+    tws = workspace(a[8], device, moe_few_workspace_bytes(&c, 0, 0, (int)T), &ws, &have, &gpu);
+    if (tws == NULL) Py_CLEAR(out);
+  }
+  Py_DECREF(device);
+  if (out == NULL || T == 0) return out;
+  const int rc = moe_w4a16_few_forward(&c, x.ptr, (int)T, router, logits, bias, tables[0], tables[1], shared, ws, have, o.ptr, st);
+  Py_DECREF(tws);
+  if (rc == MOE_OK) return out;
+  Py_DECREF(out);
+  return fail(rc, "moe_w4a16_few_forward");
+}
+
 /* init(MoeError, torch.empty_strided, float8_e4m3fn, bfloat16, float32, int32, device index -> stream handle,
  * current device index) */
 static PyObject* init(PyObject* self, PyObject* const* a, Py_ssize_t n) {
@@ -378,6 +653,9 @@ static PyMethodDef methods[] = {
     {"gemm", (PyCFunction)(void (*)(void))gemm, METH_FASTCALL, NULL},
     {"grouped", (PyCFunction)(void (*)(void))grouped, METH_FASTCALL, NULL},
     {"grouped_swiglu", (PyCFunction)(void (*)(void))grouped_swiglu, METH_FASTCALL, NULL},
+    {"add_rms_norm", (PyCFunction)(void (*)(void))add_rms_norm, METH_FASTCALL, NULL},
+    {"few_fp8", (PyCFunction)(void (*)(void))few_fp8, METH_FASTCALL, NULL},
+    {"few_w4", (PyCFunction)(void (*)(void))few_w4, METH_FASTCALL, NULL},
     {NULL, NULL, 0, NULL},
 };
 

@@ -155,7 +155,6 @@ MOE_DEV bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, 
 }
 
 // Orders generic-proxy accesses of shared memory before later asynchronous ones (TMA, MMA).
-MOE_DEV void fence_proxy_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 // Asynchronous 16-byte copy to shared memory, the first `bytes` of it from global memory, zeros after.
 MOE_DEV void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {

@@ -62,6 +62,15 @@ int encode_tmap(CUtensorMap* map, CUtensorMapDataType dtype, int rank, void* bas
 int ensure_device();
 int device_sm_count();
 int* device_error_word();  // device address of the current device's error word
+int current_device_index();  // -1 where there is none
+// What kernels need of an NVFP4 table: device arrays by expert (packed NULL: absent).
+struct ExpertTableView {
+  int E, N, K, device;
+  const void* const* packed;
+  const void* const* scales;
+  const float* scale2;
+};
+ExpertTableView expert_table_view(const moe_expert_table* t);
 
 int grouped_gemm_launch(const GemmArgs& args, const void* A, int a_rows, int lda, cudaStream_t stream);
 // The CTA-pair kernel (pair_gemm.cu): N a multiple of 256 (gate/up with the fused SwiGLU: N = 2I,
@@ -161,6 +170,21 @@ int fp8_quantize_rows_launch(const void* x, int x_dtype, int64_t ld_x, int R, in
                              int64_t s_row, int64_t s_grp, cudaStream_t st);
 int fp8_quantize_blocks_launch(const void* w, int w_dtype, int64_t ld_w, int N, int K, uint8_t* q, int64_t ld_q,
                                float* s, cudaStream_t st);
+
+// Residual addition, RMS norm and row quantiser (rms_norm.cu), arguments checked; K <= kRmsNormMaxK
+constexpr int kRmsNormMaxK = 32768;
+struct RmsNormArgs {
+  const void *x, *r, *w;  // [R, K], [R, K] or NULL, [K]; BF16 or FP32 each
+  void* h;                // x + r in r's type (r not NULL)
+  void* y;                // NULL, or BF16 [R, K]
+  uint8_t* q;
+  float* s;
+  int64_t ld_x, ld_r, ld_h, ld_y, ld_q, s_row, s_grp;
+  int R, K;
+  float eps;
+  bool x_bf16, r_bf16, w_bf16;
+};
+int rms_norm_launch(const RmsNormArgs& a, cudaStream_t st);
 
 // FP8 products (fp8_gemm.cu)
 struct Fp8GemmArgs {
