@@ -1,6 +1,7 @@
 // few.h -- arguments of the few-token layers (few_tokens.cu).
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <stddef.h>
 #include <stdint.h>
@@ -14,7 +15,7 @@ struct FewFp8Weight {  // codes [experts][N, ld], scales [experts][N / 128][K / 
 };
 struct FewW4Weight {  // by expert (an expert table's arrays)
   const void* const* packed;
-  const void* const* scales;
+  const CUtensorMap* maps;  // [E][2]: packed weights (16 rows x 4 lines of 128 bytes), scales (16 rows x 64 bytes)
   const float* scale2;
 };
 
@@ -37,7 +38,7 @@ struct FewArgs {
   int* err;
   // workspace
   int *counters, *ready, *group_done, *tile_done;
-  int n_counters, groups_max, x_chunks;
+  int n_counters, groups_max;
   float* logits_ws;
   uint8_t *x_rec, *act_rec, *act_rec_shared;
   float *act, *act_shared, *Y;

@@ -133,8 +133,8 @@ int moe_w4a16_few_forward(const moe_prefill_config* cfg, const uint16_t* x, int 
     return MOE_ERR_INVALID_ARG;
   if ((rc = ensure_device()) != MOE_OK) return rc;
   if (current_device_index() != gu.device || current_device_index() != dn.device) return MOE_ERR_INVALID_ARG;
-  a.w4[0] = FewW4Weight{gu.packed, gu.scales, gu.scale2};
-  a.w4[1] = FewW4Weight{dn.packed, dn.scales, dn.scale2};
+  a.w4[0] = FewW4Weight{gu.packed, gu.maps_few, gu.scale2};
+  a.w4[1] = FewW4Weight{dn.packed, dn.maps_few, dn.scale2};
   a.shared_out = shared_out;
   a.err = device_error_word();
   return few_launch(true, a, l, ws, static_cast<cudaStream_t>(stream));

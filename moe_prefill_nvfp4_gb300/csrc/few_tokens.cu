@@ -52,8 +52,12 @@ constexpr int MAX_T = MOE_FEW_MAX_TOKENS;
 constexpr int MAX_SLOTS = MAX_T * 32;
 
 // Shared-memory and record layouts.  A record is a token's (or an activation row's) part of a stage: 8 groups of
-// 128 codes, then 8 scales; records and weight rows lie 64 bytes past a multiple of 128 apart, so that the 16-byte
-// loads of two neighbouring rows' four lanes take the 32 banks once.
+// 128 codes, then 8 scales; records lie 64 bytes past a multiple of 128 apart, so that the 16-byte loads of two
+// neighbouring rows' four lanes take the 32 banks once.  The weights come as two blocks of ROWS / 2 rows by TMA:
+// lines of 128 bytes (a group in FP8, two in NVFP4), the same of all rows in turn, with the 128-byte swizzle; the
+// MMA's row g is row pi(g) of eight, so that neighbouring g differ in the swizzle's top bit, to the same effect.
+// (A copy per row instead, 16 of 1 KB to a stage, took 2200 cycles a stage: bulk copies of a warp's lanes are
+// issued one after another.  Two per stage.)
 template <bool W4>
 struct Fmt {
   static constexpr int ROWS = W4 ? 32 : 16;          // weight rows of a unit
@@ -62,15 +66,37 @@ struct Fmt {
   static constexpr int GROUP_BYTES = W4 ? 256 : 128; // of an activation row: FP16 or E4M3
   static constexpr int CODES = CHUNK * GROUP_BYTES;
   static constexpr int RECORD = CODES + 64;
-  static constexpr int COPIED = CODES + 32;
-  static constexpr int W_GROUP = W4 ? 64 : 128;      // bytes of a weight row's group
-  static constexpr int W_PITCH = CHUNK * W_GROUP + 64;
-  static constexpr int S_PITCH = 80;                 // NVFP4: a row's 64 block scales of a stage
-  static constexpr int SCALES_AT = ROWS * W_PITCH;   // NVFP4: block scales; FP8: 16 block scales (FP32)
-  static constexpr int ACT_AT = SCALES_AT + (W4 ? ROWS * S_PITCH : 64);
+  static constexpr int LINES = W4 ? 4 : 8;           // lines of a stage
+  static constexpr int LINE_BYTES = HALF * 128;      // of one block's rows
+  static constexpr int BLOCK_BYTES = LINES * LINE_BYTES;
+  static constexpr int SCALES_AT = 2 * BLOCK_BYTES;  // NVFP4: 64 block scales to a row; FP8: 16 block scales (FP32)
+  static constexpr int SCALES_BLOCK = HALF * 64;     // NVFP4: of one block's rows, with the 64-byte swizzle
+  static constexpr int ACT_AT = SCALES_AT + (W4 ? 2 * SCALES_BLOCK : 64);
+  static constexpr int LOADED = 2 * BLOCK_BYTES + (W4 ? 2 * SCALES_BLOCK : 0);
   static constexpr int PARTIAL = TILES * 512;        // a warp's partial sums per 8 tokens
-  static constexpr int stage_bytes(int T) { return (ACT_AT + T * RECORD + 127) / 128 * 128; }
+  static constexpr int stage_bytes(int T) { return (ACT_AT + T * RECORD + 1023) / 1024 * 1024; }
 };
+
+// The row of eight that the MMA's row g is.
+MOE_DEV int row_of(int g) { return (g >> 1) | ((g & 1) << 2); }
+
+struct FewMaps {
+  CUtensorMap w[4];  // FP8: gate/up, down; the shared expert's
+};
+
+MOE_DEV void load_3d(uint32_t dst, const void* map, int x, int y, int z, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
+MOE_DEV void load_4d(uint32_t dst, const void* map, int x, int y, int z, int w, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(
+          dst),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+      : "memory");
+}
 
 struct Entry {
   int expert;  // of the held ones; -1: the shared expert
@@ -156,12 +182,12 @@ MOE_DEV uint32_t mul_f16x2(uint32_t a, uint32_t b) {
 
 MOE_DEV uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
 
-// Group `grp` of a row, 4 consecutive columns to a lane, into the row's records.
+// Group `grp` of a row, 4 consecutive columns to a lane, into the row's records, which lie `rows` records apart.
 template <bool W4>
-MOE_DEV void write_group(const float (&v)[4], uint8_t* rows, int grp) {
+MOE_DEV void write_group(const float (&v)[4], uint8_t* first, int rows, int grp) {
   using F = Fmt<W4>;
   const int lane = threadIdx.x & 31;
-  uint8_t* rec = rows + (size_t)(grp / CHUNK) * F::RECORD;
+  uint8_t* rec = first + (size_t)(grp / CHUNK) * rows * F::RECORD;
   uint8_t* codes = rec + (grp % CHUNK) * F::GROUP_BYTES;
   float scale;
   if constexpr (W4) {
@@ -209,19 +235,20 @@ __global__ void __launch_bounds__(PREP_THREADS) prep_kernel(FewArgs a) {
   }
   if ((int)blockIdx.x <= a.T) {
     const int t = blockIdx.x - 1, groups = a.H / G;
-    uint8_t* rows = a.x_rec + (size_t)t * a.x_chunks * F::RECORD;
+    uint8_t* first = a.x_rec + (size_t)t * F::RECORD;
+    const size_t apart = (size_t)a.T * F::RECORD;
     if (!W4 && a.rows_q != nullptr) {
       for (int p = threadIdx.x; p < a.H / 16; p += PREP_THREADS)
-        *reinterpret_cast<uint4*>(rows + (size_t)(p / 64) * F::RECORD + (p % 64) * 16) =
+        *reinterpret_cast<uint4*>(first + (p / 64) * apart + (p % 64) * 16) =
             *reinterpret_cast<const uint4*>(a.rows_q + t * a.rows_ld + p * 16);
       for (int g = threadIdx.x; g < groups; g += PREP_THREADS)
-        reinterpret_cast<float*>(rows + (size_t)(g / CHUNK) * F::RECORD + F::CODES)[g % CHUNK] =
+        reinterpret_cast<float*>(first + (g / CHUNK) * apart + F::CODES)[g % CHUNK] =
             a.rows_s[t * a.rows_s_row + g * a.rows_s_grp];
     } else {
       for (int g = warp; g < groups; g += PREP_THREADS / 32) {
         const uint2 w = *reinterpret_cast<const uint2*>(a.x + (size_t)t * a.H + g * G + lane * 4);
         const float v[4] = {bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y)};
-        write_group<W4>(v, rows, g);
+        write_group<W4>(v, first, a.T, g);
       }
     }
     return;
@@ -369,7 +396,7 @@ struct Units {
 
 // Streams the weights of the units that this CTA draws.
 template <bool W4>
-MOE_DEV void load_weights(const FewArgs& a, Smem& s, uint32_t ring, int stages) {
+MOE_DEV void load_weights(const FewArgs& a, const FewMaps& maps, Smem& s, uint32_t ring, int stages) {
   using F = Fmt<W4>;
   const int lane = threadIdx.x & 31, stage_bytes = F::stage_bytes(a.T);
   const Units<W4> units(a, s.routed);
@@ -385,23 +412,19 @@ MOE_DEV void load_weights(const FewArgs& a, Smem& s, uint32_t ring, int stages) 
     const bool is_shared = en.expert < 0;
     const int inter = is_shared ? a.Is : a.I;
     const int groups = (un.down ? inter : a.H) / G;
-    // this lane's weight row
-    const int r = lane & (F::ROWS - 1), in_tile = r & 15;
-    const int row = un.down ? un.tile * F::ROWS + r
-                            : un.tile * F::HALF + (r >> 4) * 8 + (in_tile & 7) + (in_tile < 8 ? 0 : inter);
-    const uint8_t *src, *scales;
+    // the two blocks' first rows
+    const int row0 = un.down ? un.tile * F::ROWS : un.tile * F::HALF;
+    const int row1 = un.down ? row0 + F::HALF : row0 + inter;
+    const CUtensorMap* map;
+    const float* scales = nullptr;
     if constexpr (W4) {
-      const int e = a.first + en.expert, K = un.down ? a.I : a.H;
-      src = static_cast<const uint8_t*>(a.w4[un.down].packed[e]) + (size_t)row * (K / 2);
-      scales = static_cast<const uint8_t*>(a.w4[un.down].scales[e]) + (size_t)row * (K / 16);
+      map = a.w4[un.down].maps + 2 * (a.first + en.expert);
     } else {
+      map = &maps.w[(is_shared ? 2 : 0) + un.down];
       const FewFp8Weight& w = is_shared ? a.w8s[un.down] : a.w8[un.down];
-      const size_t e = is_shared ? 0 : (size_t)en.expert;
-      const int blocks = un.down ? a.H / G : 2 * inter / G;
-      // (lanes 0-7: a group each of the gate or down rows' block; 8-15: of the up rows')
-      const int block = un.down ? un.tile * F::ROWS / G : un.tile * F::HALF / G + (lane < 8 ? 0 : inter / G);
-      src = w.q + e * w.expert_stride + (size_t)row * w.ld;
-      scales = reinterpret_cast<const uint8_t*>(w.s + (e * blocks + block) * groups + (lane & 7));
+      const size_t blocks = (un.down ? a.H : 2 * inter) / G;
+      // (lanes 0-7: a group each of the first block's scales, 8-15: of the second's)
+      scales = w.s + ((is_shared ? 0 : en.expert) * blocks + (lane < 8 ? row0 : row1) / G) * groups + (lane & 7);
     }
     for (int g0 = 0; g0 < groups; g0 += CHUNK) {
       const int n = min(CHUNK, groups - g0);
@@ -409,15 +432,21 @@ MOE_DEV void load_weights(const FewArgs& a, Smem& s, uint32_t ring, int stages) 
       const uint32_t full = smem_u32(&s.full[slot]), at = ring + slot * stage_bytes;
       if (lane == 0) {
         s.info[slot] = make_int4(un.entry, un.tile, (un.down ? DOWN : 0) | (g0 == 0 ? FIRST : 0) | (g0 + n == groups ? LAST : 0), n);
-        mbar_arrive_expect_tx(full, F::ROWS * n * (F::W_GROUP + (W4 ? 8 : 0)));
+        mbar_arrive_expect_tx(full, F::LOADED);  // (lines past k come as zeros)
+        if constexpr (W4) {
+          load_3d(at, map, 0, row0, g0 / 2, full);
+          load_3d(at + F::BLOCK_BYTES, map, 0, row1, g0 / 2, full);
+          tma_load_2d(at + F::SCALES_AT, map + 1, g0 * 8, row0, full);
+          tma_load_2d(at + F::SCALES_AT + F::SCALES_BLOCK, map + 1, g0 * 8, row1, full);
+        } else {
+          const int e = is_shared ? 0 : en.expert;
+          load_4d(at, map, 0, row0, g0, e, full);
+          load_4d(at + F::BLOCK_BYTES, map, 0, row1, g0, e, full);
+        }
         mbar_arrive(smem_u32(&s.issued[slot]));
       }
-      __syncwarp();
-      if (lane < F::ROWS) bulk_load(at + r * F::W_PITCH, src + g0 * F::W_GROUP, n * F::W_GROUP, full);
-      if constexpr (W4) {
-        bulk_load(at + F::SCALES_AT + r * F::S_PITCH, scales + g0 * 8, n * 8, full);
-      } else {
-        if (lane < 16 && (lane & 7) < n) copy4_async(at + F::SCALES_AT + lane * 4, scales + g0 * 4);
+      if constexpr (!W4) {
+        if (lane < 16 && (lane & 7) < n) copy4_async(at + F::SCALES_AT + lane * 4, scales + g0);
         copies_arrive(full);
       }
       ++it;
@@ -459,8 +488,7 @@ MOE_DEV void load_records(const FewArgs& a, Smem& s, uint32_t ring, int stages) 
     }
     if (in.z & FIRST) chunk = 0;
     const Entry en = s.entry[in.x];
-    const int row = en.first + lane;
-    const uint8_t* src = nullptr;
+    const uint32_t to = ring + slot * stage_bytes + F::ACT_AT;
     if (in.z & DOWN) {
       const int inter = en.expert < 0 ? a.Is : a.I;
       if (ready != in.x) {
@@ -470,16 +498,18 @@ MOE_DEV void load_records(const FewArgs& a, Smem& s, uint32_t ring, int stages) 
         fence_proxy_async_global();
         ready = in.x;
       }
-      const int chunks = (inter / G + CHUNK - 1) / CHUNK;
-      if (lane < en.m)
-        src = (en.expert < 0 ? a.act_rec_shared + (size_t)(lane * chunks + chunk) * F::RECORD
-                             : a.act_rec + (size_t)(row * chunks + chunk) * F::RECORD);
-    } else if (lane < en.m) {
-      src = a.x_rec + (size_t)(s.token[row] * a.x_chunks + chunk) * F::RECORD;
     }
-    if (lane == 0) mbar_arrive_expect_tx(full, en.m * F::COPIED);
+    if (lane == 0) mbar_arrive_expect_tx(full, en.m * F::RECORD);
     __syncwarp();
-    if (lane < en.m) bulk_load(ring + slot * stage_bytes + F::ACT_AT + lane * F::RECORD, src, F::COPIED, full);
+    // an expert's activations lie one after another, and so do the rows of an expert that has all tokens
+    if ((in.z & DOWN) || en.m == a.T) {
+      const uint8_t* src = !(in.z & DOWN)  ? a.x_rec + (size_t)(chunk * a.T) * F::RECORD
+                           : en.expert < 0 ? a.act_rec_shared + (size_t)(chunk * a.T) * F::RECORD
+                                           : a.act_rec + (size_t)(chunk * a.T * a.k + en.first) * F::RECORD;
+      if (lane == 0) bulk_load(to, src, en.m * F::RECORD, full);
+    } else if (lane < en.m) {
+      bulk_load(to + lane * F::RECORD, a.x_rec + (size_t)(chunk * a.T + s.token[en.first + lane]) * F::RECORD, F::RECORD, full);
+    }
     ++chunk;
     ++it;
     if (++slot == stages) {
@@ -492,7 +522,7 @@ MOE_DEV void load_records(const FewArgs& a, Smem& s, uint32_t ring, int stages) 
 
 // This warp's group of a stage: acc += scale * (codes' products), for NT columns of 8 tokens.
 template <bool W4, int NT>
-MOE_DEV void group_product(uint32_t at, int warp, int m, float (&acc)[Fmt<W4>::TILES][2][4]) {
+MOE_DEV void group_product(uint32_t at, int warp, int m, bool down, float (&acc)[Fmt<W4>::TILES][2][4]) {
   using F = Fmt<W4>;
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   uint32_t b_at[NT];
@@ -505,7 +535,7 @@ MOE_DEV void group_product(uint32_t at, int warp, int m, float (&acc)[Fmt<W4>::T
     for (int c = 0; c < 2; ++c)
       sa[n][c] = lds_f32(at + F::ACT_AT + min(n * 8 + 2 * t + c, m - 1) * F::RECORD + F::CODES + warp * 4);
   }
-  const uint32_t a_at = at + g * F::W_PITCH + warp * F::W_GROUP + t * 16;
+  const int rg = row_of(g);
   float tmp[F::TILES][NT][4];
 #pragma unroll
   for (int i = 0; i < F::TILES; ++i)
@@ -515,11 +545,16 @@ MOE_DEV void group_product(uint32_t at, int warp, int m, float (&acc)[Fmt<W4>::T
     // 32 consecutive k to a lane (16 bytes of each row), 8 to a word: two MMAs
     uint4 p[4];
     uint32_t sc[4][2];
+    // (tile i / 2's rows g, then its rows g + 8: gate and up, or the two halves of one block)
+    const uint32_t line = at + (warp >> 1) * F::LINE_BYTES + rg * 128 + ((((warp & 1) * 4 + t) ^ rg) << 4);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      p[i] = lds128(a_at + i * 8 * F::W_PITCH);
+      const int block = down ? i >> 1 : i & 1, eight = down ? i & 1 : i >> 1;
+      p[i] = lds128(line + block * F::BLOCK_BYTES + eight * 1024);
       uint32_t both, unused;
-      e4m3x4_to_f16x2(lds_u16(at + F::SCALES_AT + (i * 8 + g) * F::S_PITCH + warp * 8 + t * 2), both, unused);
+      e4m3x4_to_f16x2(lds_u16(at + F::SCALES_AT + block * F::SCALES_BLOCK + (eight * 8 + rg) * 64 +
+                              (((warp >> 1) ^ (rg >> 1)) << 4) + (warp & 1) * 8 + t * 2),
+                      both, unused);
       sc[i][0] = prmt(both, both, 0x1010);
       sc[i][1] = prmt(both, both, 0x3232);
     }
@@ -550,10 +585,12 @@ MOE_DEV void group_product(uint32_t at, int warp, int m, float (&acc)[Fmt<W4>::T
 #pragma unroll
         for (int c = 0; c < 4; ++c) acc[i][n][c] = __fmaf_rn(tmp[i][n][c], sa[n][c & 1], acc[i][n][c]);
   } else {
+    const uint32_t line = at + warp * F::LINE_BYTES + rg * 128;
     const float sw[2] = {lds_f32(at + F::SCALES_AT + warp * 4), lds_f32(at + F::SCALES_AT + 32 + warp * 4)};
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      const uint4 lo = lds128(a_at + j * 64), hi = lds128(a_at + 8 * F::W_PITCH + j * 64);
+      const uint32_t piece = line + (((j * 4 + t) ^ rg) << 4);
+      const uint4 lo = lds128(piece), hi = lds128(piece + F::BLOCK_BYTES);
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         const uint4 b = lds128(b_at[n] + j * 64);
@@ -614,9 +651,9 @@ MOE_DEV void multiply(const FewArgs& a, Smem& s, uint32_t ring, uint32_t parts, 
       const int m = s.entry[in.x].m;
       const uint32_t at = ring + slot * stage_bytes;
       if (m <= 8)
-        group_product<W4, 1>(at, warp, m, acc);
+        group_product<W4, 1>(at, warp, m, in.z & DOWN, acc);
       else
-        group_product<W4, 2>(at, warp, m, acc);
+        group_product<W4, 2>(at, warp, m, in.z & DOWN, acc);
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_u32(&s.empty[slot]));
@@ -686,7 +723,7 @@ MOE_DEV void finish(const FewArgs& a, Smem& s, uint32_t parts, int nbuf) {
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
               const int col = n * 8 + 2 * t + c;
-              if (col < en.m) act[(size_t)col * inter + j0 + i * 8 + g] = swiglu_keep_nan<false>(sum[i][n][c], sum[i][n][2 + c], limit);
+              if (col < en.m) act[(size_t)col * inter + j0 + i * 8 + row_of(g)] = swiglu_keep_nan<false>(sum[i][n][c], sum[i][n][2 + c], limit);
             }
       const int grp = j0 / G;
       __syncwarp();
@@ -698,8 +735,8 @@ MOE_DEV void finish(const FewArgs& a, Smem& s, uint32_t parts, int nbuf) {
       }
       if (!__shfl_sync(0xffffffffu, last, 0)) continue;
       __syncwarp();
-      const int chunks = (inter / G + CHUNK - 1) / CHUNK;
-      uint8_t* rec = is_shared ? a.act_rec_shared : a.act_rec + (size_t)en.first * chunks * F::RECORD;
+      uint8_t* rec = is_shared ? a.act_rec_shared : a.act_rec + (size_t)en.first * F::RECORD;
+      const int apart = is_shared ? a.T : slots;
       for (int r0 = 0; r0 < en.m; r0 += 4) {
         float4 v[4];
 #pragma unroll
@@ -709,7 +746,7 @@ MOE_DEV void finish(const FewArgs& a, Smem& s, uint32_t parts, int nbuf) {
         for (int r = 0; r < 4; ++r)
           if (r0 + r < en.m) {
             const float f[4] = {v[r].x, v[r].y, v[r].z, v[r].w};
-            write_group<W4>(f, rec + (size_t)(r0 + r) * chunks * F::RECORD, grp);
+            write_group<W4>(f, rec + (size_t)(r0 + r) * F::RECORD, apart, grp);
           }
       }
       __syncwarp();
@@ -728,7 +765,7 @@ MOE_DEV void finish(const FewArgs& a, Smem& s, uint32_t parts, int nbuf) {
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
               const int col = n * 8 + 2 * t + (c & 1);
-              if (col < en.m) y[(size_t)col * a.H + i * 16 + g + 8 * (c >> 1)] = sum[i][n][c];
+              if (col < en.m) y[(size_t)col * a.H + i * 16 + row_of(g) + 8 * (c >> 1)] = sum[i][n][c];
             }
       __syncwarp();
       const int entries = s.routed + (a.Is > 0);
@@ -763,12 +800,14 @@ MOE_DEV void finish(const FewArgs& a, Smem& s, uint32_t parts, int nbuf) {
 }
 
 template <bool W4>
-__global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__ FewArgs a, int stages, int nbuf) {
+__global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__ FewArgs a, const __grid_constant__ FewMaps maps, int stages,
+                                                          int nbuf) {
   using F = Fmt<W4>;
   extern __shared__ __align__(128) uint8_t smem[];
-  Smem& s = *reinterpret_cast<Smem*>(smem);
-  const uint32_t parts = smem_u32(smem) + (sizeof(Smem) + 127) / 128 * 128;
-  const uint32_t ring = parts + (uint32_t)(nbuf * MMA_WARPS * (a.T > 8 ? 2 : 1)) * F::PARTIAL;
+  const uint32_t ring = (smem_u32(smem) + 1023) / 1024 * 1024;  // (the swizzle goes by address bits)
+  uint8_t* behind = smem + (ring - smem_u32(smem)) + stages * F::stage_bytes(a.T);
+  const uint32_t parts = smem_u32(behind);
+  Smem& s = *reinterpret_cast<Smem*>(behind + nbuf * MMA_WARPS * (a.T > 8 ? 2 : 1) * F::PARTIAL);
   Routing& r = *reinterpret_cast<Routing*>(smem + (ring - smem_u32(smem)));
   if (threadIdx.x == 0) {
     for (int i = 0; i < stages; ++i) {
@@ -795,7 +834,7 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
   fence_proxy_async_shared();  // (the ring's first bytes were the routing's)
   __syncthreads();
   if (warp == 0)
-    load_weights<W4>(a, s, ring, stages);
+    load_weights<W4>(a, maps, s, ring, stages);
   else if (warp == 1)
     load_records<W4>(a, s, ring, stages);
   else if (warp < 2 + MMA_WARPS)
@@ -811,6 +850,15 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
   }
 }
 
+// An FP8 weight as lines of 128 columns: line of a row, row, line's place in the row, expert; 8 rows by 8 lines.
+int weight_map(CUtensorMap* map, const FewFp8Weight& w, int N, int K, int count) {
+  const cuuint64_t dims[4] = {128, (cuuint64_t)N, (cuuint64_t)(K / 128), (cuuint64_t)count};
+  const cuuint64_t strides[3] = {(cuuint64_t)w.ld, 128, (cuuint64_t)(count > 1 ? w.expert_stride : w.ld * (int64_t)N)};
+  const cuuint32_t box[4] = {128, 8, 8, 1}, one[4] = {1, 1, 1, 1};
+  return encode_tmap(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<uint8_t*>(w.q), dims, strides, box, one,
+                     CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
 template <bool W4>
 int launch(const FewArgs& a, cudaStream_t st) {
   using F = Fmt<W4>;
@@ -819,23 +867,32 @@ int launch(const FewArgs& a, cudaStream_t st) {
   // (the partial sums of 16 tokens over 32 rows are 16 KB to a buffer: two of them then)
   const int nbuf = W4 && a.T > 8 ? 2 : MAX_EPI;
   constexpr int kSmem = 232448 - 1024;
-  const int fixed = (int)((sizeof(Smem) + 127) / 128 * 128) + nbuf * MMA_WARPS * (a.T > 8 ? 2 : 1) * F::PARTIAL;
+  const int fixed = (int)sizeof(Smem) + nbuf * MMA_WARPS * (a.T > 8 ? 2 : 1) * F::PARTIAL;
   const int stages = std::min(MAX_STAGES, (kSmem - fixed) / F::stage_bytes(a.T));
-  const int smem = fixed + std::max(stages * F::stage_bytes(a.T), (int)sizeof(Routing));
+  const int smem = 1024 + fixed + stages * F::stage_bytes(a.T);
+  static_assert(F::stage_bytes(1) * 2 >= (int)sizeof(Routing), "the routing has its arrays in the ring");
   static std::atomic<uint64_t> configured{0};  // a bit per device
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return MOE_ERR_CUDA;
   if (!(configured.load(std::memory_order_relaxed) >> (dev & 63) & 1)) {
-    if (cudaFuncSetAttribute(few_kernel<W4>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess)
+    if (cudaFuncSetAttribute(few_kernel<W4>, cudaFuncAttributeMaxDynamicSharedMemorySize, 1024 + kSmem) != cudaSuccess)
       return MOE_ERR_CUDA;
     configured.fetch_or(1ull << (dev & 63), std::memory_order_relaxed);
+  }
+  FewMaps maps = {};
+  if constexpr (!W4) {
+    int rc = weight_map(&maps.w[0], a.w8[0], 2 * a.I, a.H, a.count);
+    if (rc == MOE_OK) rc = weight_map(&maps.w[1], a.w8[1], a.H, a.I, a.count);
+    if (rc == MOE_OK && a.Is > 0) rc = weight_map(&maps.w[2], a.w8s[0], 2 * a.Is, a.H, 1);
+    if (rc == MOE_OK && a.Is > 0) rc = weight_map(&maps.w[3], a.w8s[1], a.H, a.Is, 1);
+    if (rc != MOE_OK) return rc;
   }
   const int blocks = 1 + a.T + (a.logits == nullptr ? a.E : 0);
   auto prep = a.T == 1 ? prep_kernel<W4, 1> : a.T <= 2 ? prep_kernel<W4, 2> : a.T <= 4 ? prep_kernel<W4, 4>
                        : a.T <= 8 ? prep_kernel<W4, 8> : prep_kernel<W4, 16>;
   const int rc = launch_pdl(prep, dim3(blocks), dim3(PREP_THREADS), 0, st, a);
   if (rc != MOE_OK) return rc;
-  return launch_pdl(few_kernel<W4>, dim3(nsm), dim3(THREADS), smem, st, a, stages, nbuf);
+  return launch_pdl(few_kernel<W4>, dim3(nsm), dim3(THREADS), smem, st, a, maps, stages, nbuf);
 }
 
 }  // namespace few
@@ -880,7 +937,6 @@ int few_launch(bool w4, FewArgs& a, const FewLayout& l, void* ws, cudaStream_t s
   a.groups_max = l.groups_max;
   a.logits_ws = reinterpret_cast<float*>(base + l.logits);
   a.x_rec = base + l.x_rec;
-  a.x_chunks = (a.H / few::G + few::CHUNK - 1) / few::CHUNK;
   a.act = reinterpret_cast<float*>(base + l.act);
   a.act_shared = reinterpret_cast<float*>(base + l.act_shared);
   a.act_rec = base + l.act_rec;
