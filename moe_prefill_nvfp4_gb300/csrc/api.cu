@@ -19,7 +19,6 @@ struct moe_expert_table {
   int device;
   CUtensorMap* d_maps;    // [E][2] (128-row boxes)
   CUtensorMap* d_maps64;  // [E][2] (64-row boxes, the CTA-pair kernel)
-  CUtensorMap* d_maps_few;  // [E][2] (16 rows x 4 lines of 128 bytes, 16 rows of 64 scales: the few-token layer)
   const void** d_packed;  // [E]
   const void** d_scales;  // [E]
   float* d_scale2;        // [E]
@@ -108,7 +107,7 @@ int device_sm_count() {
 int current_device_index() { return current_device(); }
 
 ExpertTableView expert_table_view(const moe_expert_table* t) {
-  return ExpertTableView{t->E, t->N, t->K, t->device, t->d_packed, t->d_maps_few, t->d_scale2};
+  return ExpertTableView{t->E, t->N, t->K, t->device, t->d_packed, t->d_scales, t->d_scale2};
 }
 
 int* device_error_word() {
@@ -194,9 +193,8 @@ int moe_expert_table_create(const void* const* packed, const void* const* scales
   if (rc != MOE_OK) return rc;
 
   // two tensor maps per expert and box height: 128-row boxes (single-CTA kernel), 64-row boxes
-  // (CTA-pair kernel), 16-row boxes (few-token layer)
-  std::vector<CUtensorMap> maps(2 * (size_t)E), maps64(2 * (size_t)E), maps_few(2 * (size_t)E);
-  std::memset(maps_few.data(), 0, maps_few.size() * sizeof(CUtensorMap));
+  // (CTA-pair kernel)
+  std::vector<CUtensorMap> maps(2 * (size_t)E), maps64(2 * (size_t)E);
   std::memset(maps.data(), 0, maps.size() * sizeof(CUtensorMap));
   std::memset(maps64.data(), 0, maps64.size() * sizeof(CUtensorMap));
   for (int e = 0; e < E; ++e) {
@@ -222,22 +220,6 @@ int moe_expert_table_create(const void* const* packed, const void* const* scales
         if (rc != MOE_OK) return rc;
       }
     }
-    {  // packed nibbles as lines of 128 bytes: line of a row, row, line's place in the row
-      const cuuint64_t dims[3] = {128, (cuuint64_t)N, (cuuint64_t)K / 256};
-      const cuuint64_t strides[2] = {(cuuint64_t)K / 2, 128};
-      const cuuint32_t box[3] = {128, 16, 4}, one[3] = {1, 1, 1};
-      rc = encode_tmap(&maps_few[2 * e], CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(packed[e]), dims, strides, box,
-                       one, CU_TENSOR_MAP_SWIZZLE_128B);
-      if (rc != MOE_OK) return rc;
-    }
-    {
-      const cuuint64_t dims[2] = {(cuuint64_t)K / 16, (cuuint64_t)N};
-      const cuuint64_t strides[1] = {(cuuint64_t)K / 16};
-      const cuuint32_t box[2] = {64, 16};
-      rc = encode_tmap(&maps_few[2 * e + 1], CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(scales[e]), dims, strides,
-                       box, estr, CU_TENSOR_MAP_SWIZZLE_64B);
-      if (rc != MOE_OK) return rc;
-    }
   }
   moe_expert_table* t = new moe_expert_table();
   t->E = E;
@@ -246,21 +228,17 @@ int moe_expert_table_create(const void* const* packed, const void* const* scales
   t->device = current_device();
   t->d_maps = nullptr;
   t->d_maps64 = nullptr;
-  t->d_maps_few = nullptr;
   t->d_packed = nullptr;
   t->d_scales = nullptr;
   t->d_scale2 = nullptr;
   bool ok = cudaMalloc(&t->d_maps, maps.size() * sizeof(CUtensorMap)) == cudaSuccess &&
             cudaMalloc(&t->d_maps64, maps64.size() * sizeof(CUtensorMap)) == cudaSuccess &&
-            cudaMalloc(&t->d_maps_few, maps_few.size() * sizeof(CUtensorMap)) == cudaSuccess &&
             cudaMalloc(&t->d_packed, (size_t)E * sizeof(void*)) == cudaSuccess &&
             cudaMalloc(&t->d_scales, (size_t)E * sizeof(void*)) == cudaSuccess &&
             cudaMalloc(&t->d_scale2, (size_t)E * sizeof(float)) == cudaSuccess;
   ok = ok && cudaMemcpy(t->d_maps, maps.data(), maps.size() * sizeof(CUtensorMap), cudaMemcpyHostToDevice) == cudaSuccess;
   ok = ok &&
        cudaMemcpy(t->d_maps64, maps64.data(), maps64.size() * sizeof(CUtensorMap), cudaMemcpyHostToDevice) == cudaSuccess;
-  ok = ok && cudaMemcpy(t->d_maps_few, maps_few.data(), maps_few.size() * sizeof(CUtensorMap),
-                        cudaMemcpyHostToDevice) == cudaSuccess;
   ok = ok && cudaMemcpy(t->d_packed, packed, (size_t)E * sizeof(void*), cudaMemcpyHostToDevice) == cudaSuccess;
   ok = ok && cudaMemcpy(t->d_scales, scales, (size_t)E * sizeof(void*), cudaMemcpyHostToDevice) == cudaSuccess;
   ok = ok && cudaMemcpy(t->d_scale2, scale2, (size_t)E * sizeof(float), cudaMemcpyHostToDevice) == cudaSuccess;
@@ -277,7 +255,6 @@ int moe_expert_table_destroy(moe_expert_table* t) {
   cudaDeviceSynchronize();
   cudaFree(t->d_maps);
   cudaFree(t->d_maps64);
-  cudaFree(t->d_maps_few);
   cudaFree(t->d_packed);
   cudaFree(t->d_scales);
   cudaFree(t->d_scale2);

@@ -1,7 +1,6 @@
 // few.h -- arguments of the few-token layers (few_tokens.cu).
 #pragma once
 
-#include <cuda.h>
 #include <cuda_runtime.h>
 #include <stddef.h>
 #include <stdint.h>
@@ -15,7 +14,7 @@ struct FewFp8Weight {  // codes [experts][N, ld], scales [experts][N / 128][K / 
 };
 struct FewW4Weight {  // by expert (an expert table's arrays)
   const void* const* packed;
-  const CUtensorMap* maps;  // [E][2]: packed weights (16 rows x 4 lines of 128 bytes), scales (16 rows x 64 bytes)
+  const void* const* scales;
   const float* scale2;
 };
 
@@ -37,18 +36,31 @@ struct FewArgs {
   uint16_t* out;               // BF16 [T, H]
   int* err;
   // workspace
-  int *counters, *ready, *group_done, *tile_done;
+  int *counters, *ready, *group_done, *columns_done;
   int n_counters, groups_max;
+  int slices[2], slice_groups[2];  // of k, gate/up and down
+  int lag;                         // entries between one's gate/up and its down units
+  size_t y_slice;
   float* logits_ws;
-  uint8_t *x_rec, *act_rec, *act_rec_shared;
-  float *act, *act_shared, *Y;
+  const uint8_t* x_codes;  // the tokens' rows: the given ones, or
+  const float* x_scales;
+  int64_t x_ld, x_s_row, x_s_grp;
+  uint8_t* x_made;         // these, made of x (NULL: given)
+  float* x_scales_made;
+  uint8_t *act_codes, *act_codes_shared;
+  float *gu, *act_scales, *gu_shared, *act_scales_shared, *Y;
 };
 
 struct FewLayout {
-  size_t counters, logits, x_rec, act, act_shared, act_rec, act_rec_shared, Y, total;
-  int n_counters, n_ready, n_groups, n_tiles, groups_max;
+  size_t counters, logits, x_values, x_scales, gu, act_values, act_scales, gu_shared, act_values_shared, act_scales_shared, Y,
+      total;
+  size_t y_slice;
+  int n_counters, n_ready, n_groups, n_columns, groups_max;
+  int slices[2], slice_groups[2], lag;
 };
-FewLayout few_layout(bool w4, int T, int H, int I, int Is, int E, int k);
-int few_launch(bool w4, FewArgs& a, const FewLayout& l, void* ws, cudaStream_t st);
+FewLayout few_fp8_layout(int T, int H, int I, int Is, int E, int k);
+int few_fp8_launch(FewArgs& a, const FewLayout& l, void* ws, cudaStream_t st);
+FewLayout few_w4_layout(bool w4, int T, int H, int I, int Is, int E, int k);
+int few_w4_launch(bool w4, FewArgs& a, const FewLayout& l, void* ws, cudaStream_t st);
 
 }  // namespace moe

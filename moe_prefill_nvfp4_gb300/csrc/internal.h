@@ -67,7 +67,7 @@ int current_device_index();  // -1 where there is none
 struct ExpertTableView {
   int E, N, K, device;
   const void* const* packed;
-  const CUtensorMap* maps_few;  // [E][2], see FewW4Weight
+  const void* const* scales;
   const float* scale2;
 };
 ExpertTableView expert_table_view(const moe_expert_table* t);
