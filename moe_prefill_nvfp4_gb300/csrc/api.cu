@@ -107,7 +107,7 @@ int device_sm_count() {
 int current_device_index() { return current_device(); }
 
 ExpertTableView expert_table_view(const moe_expert_table* t) {
-  return ExpertTableView{t->E, t->N, t->K, t->device, t->d_packed, t->d_scales, t->d_scale2};
+  return ExpertTableView{t->E, t->N, t->K, t->device, t->d_maps, t->d_packed, t->d_scales, t->d_scale2};
 }
 
 int* device_error_word() {

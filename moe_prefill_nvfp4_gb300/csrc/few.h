@@ -1,4 +1,4 @@
-// few.h -- arguments of the few-token layers (few_tokens.cu).
+// few.h -- arguments of the few-token layers (few.cuh).
 #pragma once
 
 #include <cuda_runtime.h>
@@ -13,7 +13,8 @@ struct FewFp8Weight {  // codes [experts][N, ld], scales [experts][N / 128][K / 
   const float* s;
 };
 struct FewW4Weight {  // by expert (an expert table's arrays)
-  const void* const* packed;
+  const void* maps;           // two tensor maps each: boxes of 128 rows and 128 bytes of the packed codes, and another
+  const void* const* packed;  // (NULL: absent)
   const void* const* scales;
   const float* scale2;
 };
@@ -36,10 +37,9 @@ struct FewArgs {
   uint16_t* out;               // BF16 [T, H]
   int* err;
   // workspace
-  int *counters, *ready, *group_done, *columns_done;
-  int n_counters, groups_max;
-  int slices[2], slice_groups[2];  // of k, gate/up and down
-  int lag;                         // entries between one's gate/up and its down units
+  int *counters, *ready, *block_done, *columns_done;
+  int n_counters, blocks_max;
+  int slices[2], slice_blocks[2];  // of k, gate/up and down
   size_t y_slice;
   float* logits_ws;
   const uint8_t* x_codes;  // the tokens' rows: the given ones, or
@@ -55,12 +55,12 @@ struct FewLayout {
   size_t counters, logits, x_values, x_scales, gu, act_values, act_scales, gu_shared, act_values_shared, act_scales_shared, Y,
       total;
   size_t y_slice;
-  int n_counters, n_ready, n_groups, n_columns, groups_max;
-  int slices[2], slice_groups[2], lag;
+  int n_counters, n_ready, n_blocks, n_columns, blocks_max;
+  int slices[2], slice_blocks[2];
 };
 FewLayout few_fp8_layout(int T, int H, int I, int Is, int E, int k);
 int few_fp8_launch(FewArgs& a, const FewLayout& l, void* ws, cudaStream_t st);
-FewLayout few_w4_layout(bool w4, int T, int H, int I, int Is, int E, int k);
-int few_w4_launch(bool w4, FewArgs& a, const FewLayout& l, void* ws, cudaStream_t st);
+FewLayout few_w4_layout(int T, int H, int I, int Is, int E, int k);
+int few_w4_launch(FewArgs& a, const FewLayout& l, void* ws, cudaStream_t st);
 
 }  // namespace moe

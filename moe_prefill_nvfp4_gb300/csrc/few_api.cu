@@ -48,7 +48,7 @@ int common(const moe_prefill_config* c, const uint16_t* x, int T, const uint16_t
   a.routed_scale = c->routed_scale;
   a.limit = c->swiglu_limit;
   a.out = out;
-  l = fp8 ? few_fp8_layout(T, a.H, a.I, a.Is, a.E, a.k) : few_w4_layout(true, T, a.H, a.I, a.Is, a.E, a.k);
+  l = fp8 ? few_fp8_layout(T, a.H, a.I, a.Is, a.E, a.k) : few_w4_layout(T, a.H, a.I, a.Is, a.E, a.k);
   return ws_bytes < l.total ? MOE_ERR_WORKSPACE_TOO_SMALL : MOE_OK;
 }
 
@@ -73,7 +73,7 @@ extern "C" {
 size_t moe_few_workspace_bytes(const moe_prefill_config* cfg, int fp8, int shared_intermediate, int T) {
   if (!sizes_ok(cfg, shared_intermediate, fp8, T)) return 0;
   const int E = cfg->num_experts, k = cfg->top_k, H = cfg->hidden, I = cfg->moe_intermediate;
-  return (fp8 ? few_fp8_layout(T, H, I, shared_intermediate, E, k) : few_w4_layout(true, T, H, I, shared_intermediate, E, k)).total;
+  return (fp8 ? few_fp8_layout(T, H, I, shared_intermediate, E, k) : few_w4_layout(T, H, I, shared_intermediate, E, k)).total;
 }
 
 int moe_fp8_few_forward(const moe_prefill_config* cfg, const uint16_t* x, const moe_fp8_rows* rows, int T,
@@ -134,11 +134,11 @@ int moe_w4a16_few_forward(const moe_prefill_config* cfg, const uint16_t* x, int 
     return MOE_ERR_INVALID_ARG;
   if ((rc = ensure_device()) != MOE_OK) return rc;
   if (current_device_index() != gu.device || current_device_index() != dn.device) return MOE_ERR_INVALID_ARG;
-  a.w4[0] = FewW4Weight{gu.packed, gu.scales, gu.scale2};
-  a.w4[1] = FewW4Weight{dn.packed, dn.scales, dn.scale2};
+  a.w4[0] = FewW4Weight{gu.maps, gu.packed, gu.scales, gu.scale2};
+  a.w4[1] = FewW4Weight{dn.maps, dn.packed, dn.scales, dn.scale2};
   a.shared_out = shared_out;
   a.err = device_error_word();
-  return few_w4_launch(true, a, l, ws, static_cast<cudaStream_t>(stream));
+  return few_w4_launch(a, l, ws, static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

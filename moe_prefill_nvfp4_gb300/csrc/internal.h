@@ -66,6 +66,7 @@ int current_device_index();  // -1 where there is none
 // What kernels need of an NVFP4 table: device arrays by expert (packed NULL: absent).
 struct ExpertTableView {
   int E, N, K, device;
+  const void* maps;  // [E][2]: of the packed codes and the scales, boxes of 128 rows
   const void* const* packed;
   const void* const* scales;
   const float* scale2;

@@ -4,10 +4,17 @@ A sum over k columns: the products are exact in FP32 (E4M3 and E2M1 x E4M3 codes
 added in the MMA, each addition off by at most 2^-23 of the sum of magnitudes (truncation allowed); then KB groups
 by FMAs and eight warps' parts by additions, 2^-24 each, and the scales' product:
     (128 * 2^-23 + (KB + 12) * 2^-24) * sum |a w|.
+NVFP4: a value is the sum of six pieces of at most 2 significant bits, each the rest of the ones before it rounded.
+A piece that is not zero is at most twice its rest (zero could be chosen too), leaves no more than the rest itself, and from
+the second on at most a half of a step where the step is an eighth of the rest's or less: the magnitudes add up to at most 5
+times the value's, 2 + 2 + 2 / 8 + ... .  A block of 256 is added in the MMA, then the six by FMAs, KB blocks by FMAs, and
+at most KB slices by additions:
+    5 * (256 * 2^-23 + (2 KB + 8) * 2^-24) * sum |a w|.
 The activation silu(g) u: 1.1 |u| dg + |silu(g)| du + 2^-20 |act| (|silu'| <= 1.1; the clamps do not widen).
 FP8: a quantised activation is its code times its scale; the scale is off as its group's largest activation is, and
 a value that lies that close to the middle between two codes may get either.
-NVFP4: an activation is rounded to 11 bits, 2^-12 of it.
+NVFP4: what the pieces leave of a value is at most 2^-15 s, s the power of two with 3 s < max <= 6 s of its 16 columns, so
+2^-15 / 3 of the largest magnitude of those; or, where s is below 2^-14 of that of the block of 256, 2^-29 / 3 of its largest.
 The weighted sum: the weights to 2^-20 (exponentials, their sum, a division), k + 1 additions; one rounding to BF16, 2^-8.
 """
 
@@ -20,6 +27,10 @@ from test_gpu_fp8 import dequant_blocks64, dequant_rows64, rand, weights  # noqa
 
 def sum_bound(k):
     return 128 * 2.0 ** -23 + (-(-k // 128) + 12) * 2.0 ** -24
+
+
+def sum_bound_pieces(k):
+    return 5 * (256 * 2.0 ** -23 + (2 * -(-k // 256) + 8) * 2.0 ** -24)
 
 
 def step_e4m3(v):
@@ -46,15 +57,19 @@ def quantised64(a, da):
     return (code * s).view(n, inter), bound.view(n, inter)
 
 
-def rounded64(a, da):
-    return a, da + a.abs() * 2.0 ** -12 + a.abs().amax(-1, keepdim=True) * 2.0 ** -39
+def pieces64(a, da):
+    """Values [n, K] and their bounds as sums of six pieces."""
+    n, k = a.shape
+    of16 = (a.abs() + da).view(n, -1, 16).amax(-1, keepdim=True).expand(n, k // 16, 16).reshape(n, k)
+    of256 = (a.abs() + da).view(n, -1, 256).amax(-1, keepdim=True).expand(n, k // 256, 256).reshape(n, k)
+    return a, da + of16 * (2.0 ** -15 / 3) + of256 * (2.0 ** -29 / 3)
 
 
-def mlp64(rows, gate_up, down, limit, through, drows=None):
+def mlp64(rows, gate_up, down, limit, through, drows=None, bound=sum_bound):
     """SwiGLU MLP of FP64 weights on rows [n, H]: (y, bound)."""
     inter = down.shape[1]
     y, mag = rows @ gate_up.t(), rows.abs() @ gate_up.abs().t()
-    dy = sum_bound(rows.shape[1]) * mag
+    dy = bound(rows.shape[1]) * mag
     if drows is not None:
         dy = dy + drows @ gate_up.abs().t()
     g, u = y[:, :inter].clamp(max=limit), y[:, inter:].clamp(-limit, limit)
@@ -62,10 +77,10 @@ def mlp64(rows, gate_up, down, limit, through, drows=None):
     act = silu * u
     dact = 1.1 * u.abs() * dy[:, :inter] + silu.abs() * dy[:, inter:] + 1.1 * dy[:, :inter] * dy[:, inter:] + 2.0 ** -20 * act.abs()
     a, da = through(act, dact)
-    return a @ down.t(), da @ down.abs().t() + sum_bound(inter) * (a.abs() @ down.abs().t())
+    return a @ down.t(), da @ down.abs().t() + bound(inter) * (a.abs() @ down.abs().t())
 
 
-def layer64(rows, ids, wts, gate_up, down, limit, through, shared=None, held=None):
+def layer64(rows, ids, wts, gate_up, down, limit, through, shared=None, held=None, drows=None, bound=sum_bound):
     """(out, tolerance of a BF16 result) of FP64 rows [T, H]; gate_up(e), down(e): FP64 weights of expert e; shared:
     (y, bound) to add; held: the experts that count."""
     out, tol = torch.zeros_like(rows), torch.zeros_like(rows)
@@ -74,7 +89,7 @@ def layer64(rows, ids, wts, gate_up, down, limit, through, shared=None, held=Non
         if held is not None and e not in held:
             continue
         t, s = (ids == e).nonzero(as_tuple=True)
-        y, dy = mlp64(rows[t], gate_up(e), down(e), limit, through)
+        y, dy = mlp64(rows[t], gate_up(e), down(e), limit, through, None if drows is None else drows[t], bound)
         w = wts[t, s].double()[:, None]
         out.index_add_(0, t, y * w)
         tol.index_add_(0, t, dy * w.abs() + (2.0 ** -20 + (k + 1) * 2.0 ** -24) * (y * w).abs())
@@ -154,8 +169,9 @@ class W4Layer:
     def ref(self, x, logits, bias=None, shared_out=None):
         ids, wts = moe.moe_route_topk(logits, self.top_k, bias, bool(self.cfg.renormalize), self.cfg.routed_scale)
         sh = None if shared_out is None else (shared_out.double(), 2.0 ** -24 * shared_out.double().abs())
-        return layer64(x.double(), ids.long(), wts, lambda e: dequant_nvfp4(*self.gu[e]), lambda e: dequant_nvfp4(*self.dn[e]),
-                       self.limit, rounded64, sh, self.held)
+        rows = x.double()
+        return layer64(rows, ids.long(), wts, lambda e: dequant_nvfp4(*self.gu[e]), lambda e: dequant_nvfp4(*self.dn[e]),
+                       self.limit, pieces64, sh, self.held, pieces64(rows, torch.zeros_like(rows))[1], sum_bound_pieces)
 
     def run(self, x, **kw):
         return moe.moe_w4a16_few_forward(self.cfg, x, *self.tables, **kw)
