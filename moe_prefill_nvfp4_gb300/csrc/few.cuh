@@ -363,7 +363,7 @@ MOE_DEV Unit unit_at(const FewArgs& a, const Smem& s, const Units& us, int u) {
 
 // Draws units, says what they are, and streams their weights.
 template <class F>
-MOE_DEV void load_weights(const FewArgs& a, const typename F::Maps& maps, Smem& s, uint32_t stages) {
+MOE_DEV void load_weights(const FewArgs& a, const typename F::Maps& maps, Smem& s, uint32_t stages, int u0, int u1) {
   const int lane = lane_id();
   const Units us(a, s.routed);
   int i = 0, n = 0;
@@ -388,7 +388,7 @@ MOE_DEV void load_weights(const FewArgs& a, const typename F::Maps& maps, Smem& 
     return true;
   };
   // two draws are under way while another's copies are issued
-  for (int u0 = draw(a.counters), u1 = draw(a.counters);;) {
+  for (;;) {
     if (!load(u0)) break;
     u0 = draw(a.counters);
     if (!load(u1)) break;
@@ -552,7 +552,7 @@ MOE_DEV void publish(const FewArgs& a, Smem& s) {
 // activations, and brings them into the down products' form.
 template <class F>
 MOE_DEV void finish_block(const FewArgs& a, Smem& s, int entry, int kb) {
-  constexpr int QUADS = F::LANE / 4, AT_ONCE = 4 / QUADS;
+  constexpr int QUADS = F::LANE / 4, AT_ONCE = 5 / QUADS;
   const Entry en = s.entry[entry];
   const bool is_shared = en.expert < 0;
   const int inter = is_shared ? a.Is : a.I, first = is_shared ? 0 : en.first;
@@ -601,7 +601,7 @@ MOE_DEV void finish_block(const FewArgs& a, Smem& s, int entry, int kb) {
 
 // All units of 32 columns of the result are stored: the whole warp adds up slices and experts of TOKENS tokens, a lane
 // to a column, of several slots at once (their loads take a round trip to L2).
-template <int TOKENS, int SLOTS>
+template <int TOKENS, int SLOTS, int SLICES>
 MOE_DEV void finish_columns(const FewArgs& a, Smem& s, int place, int t0) {
   constexpr uint32_t NONE = ~0u;
   const int h = place * 32 + (threadIdx.x & 31);
@@ -620,16 +620,21 @@ MOE_DEV void finish_columns(const FewArgs& a, Smem& s, int place, int t0) {
         sum[t][c] = 0.f;
       }
     const float* Y = a.Y;
-    for (int i = 0; i < a.slices[1]; ++i, Y += a.y_slice) {
-      float y[TOKENS][SLOTS];
+    for (int i0 = 0; i0 < a.slices[1]; i0 += SLICES, Y += SLICES * a.y_slice) {
+      float y[SLICES][TOKENS][SLOTS];
 #pragma unroll
-      for (int t = 0; t < TOKENS; ++t)
+      for (int i = 0; i < SLICES; ++i)
 #pragma unroll
-        for (int c = 0; c < SLOTS; ++c) y[t][c] = at[t][c] != NONE ? __ldcg(Y + at[t][c]) : 0.f;
+        for (int t = 0; t < TOKENS; ++t)
 #pragma unroll
-      for (int t = 0; t < TOKENS; ++t)
+          for (int c = 0; c < SLOTS; ++c)
+            y[i][t][c] = at[t][c] != NONE && i0 + i < a.slices[1] ? __ldcg(Y + i * a.y_slice + at[t][c]) : 0.f;
 #pragma unroll
-        for (int c = 0; c < SLOTS; ++c) sum[t][c] += y[t][c];
+      for (int i = 0; i < SLICES; ++i)
+#pragma unroll
+        for (int t = 0; t < TOKENS; ++t)
+#pragma unroll
+          for (int c = 0; c < SLOTS; ++c) sum[t][c] += y[i][t][c];
     }
 #pragma unroll
     for (int t = 0; t < TOKENS; ++t)
@@ -651,11 +656,11 @@ MOE_DEV void finish_columns(const FewArgs& a, Smem& s, int place, int t0) {
 // Finishes what all its units are stored of: each entry's blocks of activations, then the columns of the result, drawn
 // in this order.  One warp of a CTA does so from the start, the others when their own work is done.
 template <class F>
-MOE_DEV void finish(const FewArgs& a, Smem& s) {
+MOE_DEV void finish(const FewArgs& a, Smem& s, int drawn) {
   const int sh = shared_entries(a), entries = s.routed + sh, per_entry = a.I / F::KB, blocks_shared = a.Is / F::KB;
   const int blocks = blocks_shared + s.routed * per_entry, places = a.H / 32;
   const int total = blocks + places * (a.T <= 2 ? a.T : (a.T + 1) / 2);
-  for (int drawn = draw(a.counters + 32);;) {
+  for (;;) {
     const int u = __shfl_sync(0xffffffffu, drawn, 0);
     if (u >= total) return;
     drawn = draw(a.counters + 32);
@@ -663,9 +668,9 @@ MOE_DEV void finish(const FewArgs& a, Smem& s) {
       const int t = (u - blocks) / places, place = u - blocks - t * places;
       if (!wait_count(a.columns_done + place * 32 / 256, entries * a.slices[1], s, a.err)) return;
       if (a.T <= 2)
-        finish_columns<1, 8>(a, s, place, t);
+        finish_columns<1, 8, 3>(a, s, place, t);
       else
-        finish_columns<2, 4>(a, s, place, 2 * t);
+        finish_columns<2, 4, 2>(a, s, place, 2 * t);
     } else {
       int v = u - blocks_shared, e = 0;
       if (v < 0) {
@@ -716,6 +721,14 @@ __global__ void __launch_bounds__(THREADS, PER_SM) few_kernel(const __grid_const
   for (int e = threadIdx.x; e < a.E; e += THREADS) r.tokens[e] = 0;
   griddep_wait();
   griddep_launch_dependents();
+  // (the first draws' answers come while the tokens are routed)
+  int u0 = 0, u1 = 0;
+  if (warp == 0) {
+    u0 = draw(a.counters);
+    u1 = draw(a.counters);
+  } else if (warp == WARPS - 1) {
+    u0 = draw(a.counters + 32);
+  }
   make_entries<F>(a, s, r);
   fence_proxy_async_shared();  // (the stages' first bytes were the routing's)
   tc_fence_before();
@@ -725,7 +738,7 @@ __global__ void __launch_bounds__(THREADS, PER_SM) few_kernel(const __grid_const
     for (int64_t i = blockIdx.x * THREADS + threadIdx.x; i < (int64_t)a.T * a.H; i += (int64_t)gridDim.x * THREADS)
       a.out[i] = a.shared_out != nullptr ? a.shared_out[i] : 0;
   } else if (warp == 0) {
-    load_weights<F>(a, maps, s, stages);
+    load_weights<F>(a, maps, s, stages, u0, u1);
   } else if (warp == 1) {
     multiply<F>(a, s, stages);
   } else if (warp < 6) {
@@ -736,7 +749,8 @@ __global__ void __launch_bounds__(THREADS, PER_SM) few_kernel(const __grid_const
     publish<F>(a, s);
   }
   __syncwarp();
-  if (s.routed + shared_entries(a) > 0 && !*(volatile int*)&s.abort) finish<F>(a, s);
+  if (s.routed + shared_entries(a) > 0 && !*(volatile int*)&s.abort)
+    finish<F>(a, s, warp == WARPS - 1 ? u0 : draw(a.counters + 32));
   __syncwarp();
   tc_fence_before();
   __syncthreads();
