@@ -337,8 +337,9 @@ int moe_fp8_quantize_blocks(const void* w, int w_dtype, int64_t ld_w, int N, int
 
 /*
  * The step in front of the experts: residual addition, root-mean-square norm, and the row quantiser on its result,
- *   h = x + r,  y = h / sqrt(sum_k h^2 / K + eps) * w,  (q, s) = moe_fp8_quantize_rows of y,
- * in FP32 without rounding in between: y is made of the unrounded h, the codes of the unrounded y.
+ *   h = x + r,  y = h / sqrt(sum_k h^2 / K + eps) * w,  (q, s) as moe_fp8_quantize_rows has them of y,
+ * in FP32 without rounding in between: y is made of the unrounded h, and the codes of h w itself, in pairs of FP32
+ * numbers up to their one rounding (1 / sqrt(...) is a factor of y and of its scale).
  *   x     device BF16 or FP32 (x_dtype) [R, ld_x]
  *   r     NULL (h = x, not stored), or device BF16 or FP32 (r_dtype) [R, ld_r]
  *   w     device BF16 or FP32 (w_dtype) [K]
@@ -448,10 +449,12 @@ typedef struct {
  *              its own clamp shared_limit; it goes with first = 0
  * Requirements: H, I and Is multiples of 128.
  *
- * moe_w4a16_few_forward: experts in NVFP4 tables (absent ones add nothing).  The weights are exact (E2M1 x E4M3
- * in FP16, scale2 on the FP32 sums), x and the activations FP16 times a power of two per 128 columns: x exactly
- * down to 2^-31 of its group's largest magnitude (and to 2^-39 of that below), the activations to 2^-12 of their
- * value.  g and u are not rounded to BF16 (as in the small-row products).
+ * moe_w4a16_few_forward: experts in NVFP4 tables (absent ones add nothing).  The weights are exact (E2M1 x E4M3,
+ * scale2 on the FP32 sums); x and the activations are sums of six E2M1 codes with a scale to 16 columns, which leaves
+ * at most 2^-16.5 of the 16's largest magnitude (and at most 2^-30 of that of 256 columns where the 16 are below
+ * 2^-14 of it): a BF16 x within 2^-7 of the largest is exact.  g and u are not rounded to BF16 (as in the
+ * small-row products).  A row with a value that is not finite gives NaN.  The block scales are not negative (as
+ * NVFP4 has them; their sign bit is not looked at).
  *   shared_out device BF16 [T, H] or NULL, added to out
  * Requirements: H and I multiples of 256.
  */

@@ -102,6 +102,28 @@ MOE_DEV bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, 
   }
 }
 
+// A whole warp's wait, with one outcome for all its lanes.  The timer is looked at once in a while only: reading it
+// takes longer than most waits for a copy that was issued early.
+MOE_DEV bool mbar_wait_warp(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* err) {
+  bool ok = mbar_try_wait(bar, parity);
+  if (!__all_sync(0xffffffffu, ok)) {
+    uint64_t t0 = 0;
+    for (int n = 0; !ok; ++n) {
+      ok = mbar_try_wait_sleep(bar, parity, kSleepHintNs);
+      if (ok || *abort_flag) break;
+      if (n % 64 == 63) {
+        if (t0 == 0) t0 = globaltimer_ns();
+        if (globaltimer_ns() - t0 > kWaitLimitNs) {
+          *abort_flag = 1;
+          set_error(err, MOE_DEVERR_TIMEOUT);
+        }
+      }
+    }
+    ok = __all_sync(0xffffffffu, ok);
+  }
+  return ok;
+}
+
 // Waits until the counter at p (global memory, written by other CTAs or grids) reaches `need`,
 // with acquire ordering at GPU scope; the same bounds as mbar_wait.
 MOE_DEV bool wait_counter_geq(const int* p, int need, volatile int* abort_flag, int* err) {

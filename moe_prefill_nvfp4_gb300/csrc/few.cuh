@@ -97,28 +97,7 @@ struct Routing {
 
 MOE_DEV uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
 
-// A whole warp's wait, with one outcome for all its lanes: bounded by kWaitLimitNs, which is looked at once in a
-// while only (reading the timer takes longer than most of these waits).
-MOE_DEV bool warp_wait(uint64_t& bar, uint32_t parity, Smem& s, int* err) {
-  const uint32_t at = smem_u32(&bar);
-  bool ok = mbar_try_wait(at, parity);
-  if (!__all_sync(0xffffffffu, ok)) {
-    uint64_t t0 = 0;
-    for (int n = 0; !ok; ++n) {
-      ok = mbar_try_wait_sleep(at, parity, kSleepHintNs);
-      if (ok || *(volatile int*)&s.abort) break;
-      if (n % 64 == 63) {
-        if (t0 == 0) t0 = globaltimer_ns();
-        if (globaltimer_ns() - t0 > kWaitLimitNs) {
-          s.abort = 1;
-          set_error(err, MOE_DEVERR_TIMEOUT);
-        }
-      }
-    }
-    ok = __all_sync(0xffffffffu, ok);
-  }
-  return ok;
-}
+MOE_DEV bool warp_wait(uint64_t& bar, uint32_t parity, Smem& s, int* err) { return mbar_wait_warp(smem_u32(&bar), parity, &s.abort, err); }
 
 // Waits for a count of what other warps have stored and published (a poll is a round trip to L2).
 MOE_DEV bool wait_count(const int* count, int need, Smem& s, int* err) {

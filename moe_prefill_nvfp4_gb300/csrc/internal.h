@@ -184,6 +184,7 @@ struct RmsNormArgs {
   int R, K;
   float eps;
   bool x_bf16, r_bf16, w_bf16;
+  int* err;
 };
 int rms_norm_launch(const RmsNormArgs& a, cudaStream_t st);
 
