@@ -452,8 +452,8 @@ typedef struct {
  * moe_w4a16_few_forward: experts in NVFP4 tables (absent ones add nothing).  The weights are exact (E2M1 x E4M3,
  * scale2 on the FP32 sums); x and the activations are sums of six E2M1 codes with a scale to 16 columns, which leaves
  * at most 2^-16.5 of the 16's largest magnitude (and at most 2^-30 of that of 256 columns where the 16 are below
- * 2^-14 of it): a BF16 x within 2^-7 of the largest is exact.  g and u are not rounded to BF16 (as in the
- * small-row products).  A row with a value that is not finite gives NaN.  The block scales are not negative (as
+ * 2^-14 of it, and 2^-133 of magnitudes below 2^-115): a BF16 x within 2^-7 of the largest is exact.  g and u are not
+ * rounded to BF16 (as in the small-row products).  A row with a value that is not finite gives NaN.  The block scales are not negative (as
  * NVFP4 has them; their sign bit is not looked at).
  *   shared_out device BF16 [T, H] or NULL, added to out
  * Requirements: H and I multiples of 256.

@@ -9,7 +9,8 @@
 // its 16, and a BF16 value within 2^-7 of that one is exact.  The six rows have the same scales and make six columns
 // of the accumulator, which the epilogue adds up, smallest first.  s is an E4M3 number of exponent -6 .. 8 times a
 // power of two to the row's block of 256 columns, its factor: columns in which the scale would be smaller are
-// off by at most 2^-15 2^-6, 2^-30 of the block's largest.
+// off by at most 2^-15 2^-6, 2^-30 of the block's largest.  The largest magnitude counts as 2^-115 at least: what is
+// smaller is off by at most 2^-15 2^-118.
 // A block with a value that is not finite has the factor NaN.  (The MMA knows no sign of a scale: NVFP4 has none.)
 //
 // Compared with converting the weights to 16 bits in registers this leaves all of an SM's issue slots and
@@ -90,7 +91,7 @@ struct W4 {
     uint8_t* to = rows + ((size_t)row * blocks + kb) * BLOCK_BYTES;
     // the exponent of the power of two whose sixfold a magnitude does not pass
     auto exponent = [](uint32_t bits) { return (int)(bits >> 23) - 129 + ((bits & 0x7FFFFFu) > 0x400000u); };
-    uint32_t most = 0x0D800000u;  // 2^-100
+    uint32_t most = 0x06000000u;  // 2^-115: the factor is no less than 2^-126
 #pragma unroll
     for (int j = 0; j < 8; ++j) most = max(most, abs_bits(v[j]));
     most = max(most, __shfl_xor_sync(0xffffffffu, most, 1));

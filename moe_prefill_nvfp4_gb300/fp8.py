@@ -6,8 +6,10 @@ sort and combine are the library's usual calls; the products are the FP8 ones.
     logits -> top-k -> expert sort -> quantise x by rows -> gate/up product with SwiGLU and quantisation
            -> down product -> weighted combine (+ shared expert)
 
-Between gate/up and down only codes and scales go to memory.  ``python -m moe_prefill_nvfp4_gb300.fp8``
-runs one chunk of random weights and prints its time and its distance from the same experts in FP32.
+Between gate/up and down only codes and scales go to memory.  The step before it, residual addition and RMS norm,
+gives the quantised rows too (``moe_fp8_add_rms_norm``), and a few tokens take the whole layer in one call
+(``forward_few``).  ``python -m moe_prefill_nvfp4_gb300.fp8`` runs a chunk and a few tokens of random weights and
+prints their times and distances from the same experts in FP32.
 """
 
 from __future__ import annotations
@@ -93,8 +95,10 @@ class Fp8Experts:
         self.renormalize, self.routed_scale, self.shared = renormalize, routed_scale, shared
 
     def forward(self, x: torch.Tensor, w_router: Optional[torch.Tensor] = None, logits: Optional[torch.Tensor] = None,
-                router_bias: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+                router_bias: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None, stream=None,
+                rows: Optional[tuple] = None) -> torch.Tensor:
         """BF16 [T, H] of a chunk x BF16 [T, H], routed by ``logits`` FP32 [T, E] or by ``w_router`` BF16 [E, H].
+        ``rows``: the codes and scales of x where it is quantised already (``moe_fp8_add_rms_norm``).
 
         With ``stream`` everything runs on it, temporaries and a new result are allocated on it, and nothing waits
         for the current stream: the caller has the inputs ready on ``stream``, keeps them until it is done, and
@@ -106,14 +110,29 @@ class Fp8Experts:
                 logits = moe.moe_router_logits(x, w_router, stream=stream)
             if logits.shape != (x.shape[0], self.num_experts):
                 raise ValueError(f"logits: need {(x.shape[0], self.num_experts)}, got {tuple(logits.shape)}")
-            y = self._chunk(x, logits, router_bias, out, stream)
+            y = self._chunk(x, logits, router_bias, out, stream, rows)
         return y if out is not None else _result(y, stream)
 
-    def _chunk(self, x, logits, router_bias, out, stream) -> torch.Tensor:
+    def forward_few(self, x: Optional[torch.Tensor], w_router: Optional[torch.Tensor] = None,
+                    logits: Optional[torch.Tensor] = None, router_bias: Optional[torch.Tensor] = None,
+                    out: Optional[torch.Tensor] = None, stream=None, rows: Optional[tuple] = None,
+                    ws: Optional[torch.Tensor] = None) -> torch.Tensor:
+        """The same layer for at most ``MOE_FEW_MAX_TOKENS`` tokens in one call (``moe_fp8_few_forward``), as a decode
+        step has them: its sums have an order of their own, and nothing but the result is rounded to BF16.  x may be
+        None with ``rows`` and ``logits``.  ``ws``: a workspace of this call's own (``moe_few_workspace_bytes``)."""
+        shared = self.shared
+        parts = None if shared is None else (shared.gate_up.q, shared.gate_up.s, shared.down.q, shared.down.s)
+        with _on(stream):
+            y = moe.moe_fp8_few_forward(x, self.gate_up.q, self.gate_up.s, self.down.q, self.down.s, self.top_k, w_router, logits,
+                                        router_bias, self.limit, self.renormalize, self.routed_scale, self.num_experts,
+                                        self.first, parts, None if shared is None else shared.limit, rows, ws, out, stream)
+        return y if out is not None else _result(y, stream)
+
+    def _chunk(self, x, logits, router_bias, out, stream, rows) -> torch.Tensor:
         ids, wts = moe.moe_route_topk(logits, self.top_k, router_bias, self.renormalize, self.routed_scale, stream=stream)
         order = moe.moe_sort_by_expert(ids, self.num_experts, stream=stream)
         slots = ids.numel()
-        q, s = moe.moe_fp8_quantize_rows(x, stream=stream)
+        q, s = rows if rows is not None else moe.moe_fp8_quantize_rows(x, stream=stream)
         act = moe.moe_fp8_grouped_gemm_swiglu(q, s, self.gate_up.q, self.gate_up.s, order["expert_offsets"], slots,
                                               limit=self.limit, gather_ids=order["sorted_token_ids"], first=self.first,
                                               stream=stream)
@@ -136,28 +155,42 @@ def _reference(x, logits, gate_up, down, top_k, limit):
     return out
 
 
-def main(tokens: int = 256, hidden: int = 2048, inter: int = 768, experts: int = 64, top_k: int = 8) -> None:
+def main(tokens: int = 256, hidden: int = 2048, inter: int = 768, experts: int = 64, top_k: int = 8, few: int = 4) -> None:
     g = torch.Generator(device="cuda").manual_seed(0)
     rand = lambda *shape: torch.randn(*shape, generator=g, device="cuda", dtype=torch.bfloat16)  # noqa: E731
     x, logits = rand(tokens, hidden), rand(tokens, experts).float()
     gate_up, down = rand(experts, 2 * inter, hidden) * hidden ** -0.5, rand(experts, hidden, inter) * inter ** -0.5
     layer = Fp8Experts(Fp8Weight.quantise(gate_up), Fp8Weight.quantise(down), top_k)
+    few = min(few, tokens)
+    # a decode step: the residual stream through the norm, which also quantises, to the router and the experts
+    residual, w_norm, w_router = rand(few, hidden), 1 + 0.1 * rand(hidden), rand(experts, hidden) * hidden ** -0.5
+
+    def step():
+        q, s, _, normed = moe.moe_fp8_add_rms_norm(x[:few], w_norm, residual, normed=True)
+        return normed, layer.forward_few(normed, w_router, rows=(q, s))
+
+    def report(what, run, y, ref):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            run()
+        for _ in range(3):
+            graph.replay()
+        start, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        start.record()
+        for _ in range(20):
+            graph.replay()
+        end.record()
+        torch.cuda.synchronize()
+        print(f"{what}, {experts} experts, top-{top_k}: {start.elapsed_time(end) / 20 * 1e3:.1f} us, "
+              f"{float((y.float() - ref).norm() / ref.norm()):.3f} of the unquantised experts' norm apart, "
+              f"device error {moe.moe_get_device_error()}")
+
     y = layer.forward(x, logits=logits)
-    ref = _reference(x, logits, gate_up, down, top_k, layer.limit)
-    graph = torch.cuda.CUDAGraph()
-    with torch.cuda.graph(graph):
-        layer.forward(x, logits=logits)
-    for _ in range(3):
-        graph.replay()
-    start, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
-    start.record()
-    for _ in range(20):
-        graph.replay()
-    end.record()
-    torch.cuda.synchronize()
-    print(f"{tokens} tokens, {experts} experts, top-{top_k}: {start.elapsed_time(end) / 20 * 1e3:.1f} us a chunk, "
-          f"{float((y.float() - ref).norm() / ref.norm()):.3f} of the unquantised experts' norm apart, "
-          f"device error {moe.moe_get_device_error()}")
+    report(f"{tokens} tokens", lambda: layer.forward(x, logits=logits), y,
+           _reference(x, logits, gate_up, down, top_k, layer.limit))
+    normed, y = step()
+    report(f"norm and layer of {few} tokens", step, y,
+           _reference(normed, moe.moe_router_logits(normed, w_router), gate_up, down, top_k, layer.limit))
 
 
 if __name__ == "__main__":

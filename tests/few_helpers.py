@@ -14,8 +14,10 @@ The activation silu(g) u: 1.1 |u| dg + |silu(g)| du + 2^-20 |act| (|silu'| <= 1.
 FP8: a quantised activation is its code times its scale; the scale is off as its group's largest activation is, and
 a value that lies that close to the middle between two codes may get either.
 NVFP4: what the pieces leave of a value is at most 2^-15 s, s the power of two with 3 s < max <= 6 s of its 16 columns, so
-2^-15 / 3 of the largest magnitude of those; or, where s is below 2^-14 of that of the block of 256, 2^-29 / 3 of its largest.
-The weighted sum: the weights to 2^-20 (exponentials, their sum, a division), k + 1 additions; one rounding to BF16, 2^-8.
+2^-15 / 3 of the largest magnitude of those; or, where s is below 2^-14 of that of the block of 256, 2^-29 / 3 of its largest;
+or, where all are below 2^-115, 2^-133 (s >= 2^-118).
+The weighted sum: the weights to 2^-20 (exponentials, their sum, a division), k + 1 additions; one rounding to BF16, 2^-8,
+or below 2^-126, where BF16 numbers are 2^-133 apart, 2^-134.
 """
 
 import torch
@@ -62,7 +64,7 @@ def pieces64(a, da):
     n, k = a.shape
     of16 = (a.abs() + da).view(n, -1, 16).amax(-1, keepdim=True).expand(n, k // 16, 16).reshape(n, k)
     of256 = (a.abs() + da).view(n, -1, 256).amax(-1, keepdim=True).expand(n, k // 256, 256).reshape(n, k)
-    return a, da + of16 * (2.0 ** -15 / 3) + of256 * (2.0 ** -29 / 3)
+    return a, da + of16 * (2.0 ** -15 / 3) + of256 * (2.0 ** -29 / 3) + 2.0 ** -133
 
 
 def mlp64(rows, gate_up, down, limit, through, drows=None, bound=sum_bound):
@@ -95,7 +97,7 @@ def layer64(rows, ids, wts, gate_up, down, limit, through, shared=None, held=Non
         tol.index_add_(0, t, dy * w.abs() + (2.0 ** -20 + (k + 1) * 2.0 ** -24) * (y * w).abs())
     if shared is not None:
         out, tol = out + shared[0], tol + shared[1]
-    return out, tol * (1 + 2.0 ** -8) + out.abs() * 2.0 ** -8
+    return out, tol * (1 + 2.0 ** -8) + out.abs() * 2.0 ** -8 + 2.0 ** -134
 
 
 def assert_near(got, ref, tol):
