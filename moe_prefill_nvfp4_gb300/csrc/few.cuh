@@ -29,7 +29,7 @@
 //   TMEM_COLS, accumulators(a)   tensor memory, and how many accumulators it is divided into
 //   FULL_ARRIVALS            arrivals that make a stage full: the weights' bytes, lanes whose copies have landed
 //   Maps, held(a, e)         tensor maps by value, whether expert e is here
-//   Weights, Rows            the loads of a unit's k blocks
+//   Weights, Rows            the loads of a unit's k blocks: the weights; their scales (load_scales), and the rows with theirs
 //   multiply, add            a stage's MMAs, an accumulator's scaling and addition
 //   output_scale(a, expert)  factor of a unit's sums
 //   LANE, write_block        a block of KB columns of a row, LANE to a lane, into the operand's form
@@ -389,17 +389,20 @@ MOE_DEV void load_rows(const FewArgs& a, Smem& s, uint32_t stages) {
     if (!warp_wait(s.drawn[slot], n / DRAWN & 1, s, a.err)) break;
     const Unit un = s.unit[slot];
     if (un.flags & END) break;
-    if (un.flags & DOWN && un.entry != seen) {
-      if (!wait_count(a.ready + un.entry, (un.flags & SHARED ? a.Is : a.I) / F::KB, s, a.err)) break;
-      seen = un.entry;
-    }
     typename F::Rows rows(a, s, un);
     bool ok = true;
     for (int kb = un.kb0; kb < un.kb1; ++kb, ++i) {
       const int st = i % NS;
       ok = warp_wait(s.empty[st], (i / NS & 1) ^ 1, s, a.err);
       if (!ok) break;
-      rows.load(s, un, kb, stages + st * F::STAGE, s.scales[i % NF]);
+      const uint32_t at = stages + st * F::STAGE;
+      rows.load_scales(kb, at);
+      if (un.flags & DOWN && un.entry != seen) {
+        ok = wait_count(a.ready + un.entry, (un.flags & SHARED ? a.Is : a.I) / F::KB, s, a.err);
+        if (!ok) break;
+        seen = un.entry;
+      }
+      rows.load(s, un, kb, at, s.scales[i % NF]);
       cp_async_arrive(smem_u32(&s.full[st]));
     }
     if (!ok) break;

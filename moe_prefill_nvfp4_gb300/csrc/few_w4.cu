@@ -74,7 +74,7 @@ struct W4 {
   static constexpr int MAX_N = NT * PIECES, SF = 512, ROWS = 2 * BLK, SCALES_A = ROWS + MAX_N * RB,
                        SCALES_B = SCALES_A + 8 * SF, STAGE = SCALES_B + 4 * SF;
   static constexpr int TMEM_COLS = 256, TMEM_SCALES = 208;  // (32 columns of the weight's scales, 16 of the pieces')
-  static constexpr int FULL_ARRIVALS = 1 + 32 + 32;
+  static constexpr int FULL_ARRIVALS = 1 + 32;
   static_assert(STAGE % 1024 == 0 && 2 * MAX_N <= TMEM_SCALES && MAX_N <= 128, "");
 
   struct Maps {};
@@ -121,19 +121,12 @@ struct W4 {
 
   struct Weights {
     const uint8_t* map;
-    const uint8_t* scales[2];  // this lane's: of every eighth row 4 of a block's 16, of the rows' first half and second
-    int row0, row1, pitch;
+    int row0, row1;
     MOE_DEV Weights(const FewArgs& a, const Maps&, const Unit& un) {
       const bool down = un.flags & DOWN;
-      const FewW4Weight& w = a.w4[down ? 1 : 0];
-      const int lane = lane_id();
-      map = static_cast<const uint8_t*>(w.maps) + (size_t)un.expert * 2 * sizeof(CUtensorMap);
+      map = static_cast<const uint8_t*>(a.w4[down ? 1 : 0].maps) + (size_t)un.expert * 2 * sizeof(CUtensorMap);
       row0 = un.place * (down ? 256 : 128);
       row1 = row0 + (down ? 128 : a.I);
-      pitch = (down ? a.I : a.H) / 16;
-      const uint8_t* of = static_cast<const uint8_t*>(w.scales[un.expert]) + lane % 4 * 4;
-      scales[0] = of + (size_t)(row0 + lane / 4) * pitch;
-      scales[1] = of + (size_t)(row1 + lane / 4) * pitch;
     }
     MOE_DEV void load(int kb, uint32_t at, uint32_t full) const {
       if (elect_one()) {
@@ -142,25 +135,32 @@ struct W4 {
         tma_load_2d(at + BLK, map, kb * RB, row1, full);
       }
       __syncwarp();
-      const int lane = lane_id();
-      const uint32_t to = at + SCALES_A + lane % 4 * SF + lane / 4 * 16;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint8_t* src = scales[h] + kb * 16;
-#pragma unroll
-        for (int j = 0; j < 16; ++j, src += 8 * pitch) cp_async4(to + h * 4 * SF + j % 4 * 128 + j / 4 * 4, src);
-      }
-      cp_async_arrive(full);
     }
   };
 
   struct Rows {
     const uint8_t* of;
     size_t pitch;
+    const uint8_t* scales[2];  // this lane's of the weight's: of every eighth row 4 of a block's 16, of the rows' halves
+    int scale_pitch;
     MOE_DEV Rows(const FewArgs& a, const Smem&, const Unit& un) {
       const bool down = un.flags & DOWN;
+      const int row = un.place * (down ? 256 : 128) + lane_id() / 4;
+      scale_pitch = (down ? a.I : a.H) / 16;
+      const uint8_t* w = static_cast<const uint8_t*>(a.w4[down ? 1 : 0].scales[un.expert]) + lane_id() % 4 * 4;
+      scales[0] = w + (size_t)row * scale_pitch;
+      scales[1] = w + (size_t)(row + (down ? 128 : a.I)) * scale_pitch;
       pitch = (size_t)((down ? a.I : a.H) / KB) * BLOCK_BYTES;
       of = down ? a.act_codes : a.x_made;
+    }
+    MOE_DEV void load_scales(int kb, uint32_t at) const {
+      const uint32_t to = at + SCALES_A + lane_id() % 4 * SF + lane_id() / 4 * 16;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint8_t* src = scales[h] + kb * 16;
+#pragma unroll
+        for (int j = 0; j < 16; ++j, src += 8 * scale_pitch) cp_async4(to + h * 4 * SF + j % 4 * 128 + j / 4 * 4, src);
+      }
     }
     MOE_DEV void load(const Smem& s, const Unit& un, int kb, uint32_t at, float* factors) const {
       const int lane = lane_id();
