@@ -5,7 +5,7 @@
 //
 // Bound by the weights' bytes: of each expert that a token has picked, once.  So everything else is kept out of
 // their way:
-//   prep  router logits (a CTA to an expert and eight tokens), the tokens' rows in the form of the products' operand,
+//   prep  router logits (a CTA to a few experts and tokens), the tokens' rows in the form of the products' operand,
 //         counters to zero.
 //   few   persistent, two CTAs to an SM.  Each CTA routes the few tokens by itself (logits -> picks -> list of the
 //         picked experts: the same in all CTAs), which is shorter than a launch.  Then it draws units from a counter --
@@ -29,7 +29,8 @@
 //   TMEM_COLS, accumulators(a)   tensor memory, and how many accumulators it is divided into
 //   FULL_ARRIVALS            arrivals that make a stage full: the weights' bytes, lanes whose copies have landed
 //   Maps, held(a, e)         tensor maps by value, whether expert e is here
-//   Weights, Rows            the loads of a unit's k blocks: the weights; their scales (load_scales), and the rows with theirs
+//   Weights, Rows            the loads of a unit's k blocks: the weights; their scales through
+//                            registers (fetch_scales, store_scales), and the rows with theirs
 //   multiply, add            a stage's MMAs, an accumulator's scaling and addition
 //   output_scale(a, expert)  factor of a unit's sums
 //   LANE, write_block        a block of KB columns of a row, LANE to a lane, into the operand's form
@@ -93,6 +94,7 @@ struct Routing {
   uint32_t tokens[MOE_FEW_MAX_EXPERTS];  // bit t: token t has picked the expert
   short first[MOE_FEW_MAX_EXPERTS];      // its first row
   int sums[MOE_FEW_MAX_EXPERTS / 32];    // of 32 experts each: rows, experts << 16
+  bool held[MOE_FEW_MAX_EXPERTS];        // the expert is here
 };
 
 MOE_DEV uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
@@ -127,13 +129,13 @@ MOE_DEV bool wait_count(const int* count, int need, Smem& s, int* err) {
 
 // ------------------------------------------------------------------------------------------------
 // prep: block 0 clears the counters, blocks 1 .. T bring the tokens' rows into the operand's form (unless they are given so), the others
-// make the router's logits, of one expert and eight tokens each
+// make the router's logits, of EE experts and TT tokens each
 
-constexpr int PREP_THREADS = 256, PREP_TOKENS = 8;
+constexpr int PREP_THREADS = 256;
 
-template <class F, int TT>
+template <class F, int EE, int TT>
 __global__ void __launch_bounds__(PREP_THREADS) prep_kernel(FewArgs a) {
-  __shared__ float s_part[PREP_THREADS / 32][TT];
+  __shared__ float s_part[PREP_THREADS / 32][EE * TT];
   griddep_wait();
   griddep_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -159,41 +161,52 @@ __global__ void __launch_bounds__(PREP_THREADS) prep_kernel(FewArgs a) {
     }
     return;
   }
-  // one expert's logits of TT tokens: its router row is read once, the tokens' rows come from the caches
-  const int at = blockIdx.x - 1 - row_blocks, e = at % a.E, t0 = at / a.E * PREP_TOKENS;
-  float acc[TT];
+  // the logits of EE experts and TT tokens, whose rows come from the caches
+  const int groups = (a.E + EE - 1) / EE, at = blockIdx.x - 1 - row_blocks, e0 = at % groups * EE, t0 = at / groups * TT;
+  float acc[EE][TT];
 #pragma unroll
-  for (int t = 0; t < TT; ++t) acc[t] = 0.f;
-  const uint4* w = reinterpret_cast<const uint4*>(a.w_router + (size_t)e * a.H);
-  const uint4* x = reinterpret_cast<const uint4*>(a.x + (size_t)t0 * a.H);
+  for (int e = 0; e < EE; ++e)
+#pragma unroll
+    for (int t = 0; t < TT; ++t) acc[e][t] = 0.f;
   const int n = a.H / 8;
-#pragma unroll 3
+  const uint4* w = reinterpret_cast<const uint4*>(a.w_router) + (size_t)e0 * n;
+  const uint4* x = reinterpret_cast<const uint4*>(a.x) + (size_t)t0 * n;
+#pragma unroll (EE * TT == 1 ? 3 : 1)
   for (int i = threadIdx.x; i < n; i += PREP_THREADS) {
-    const uint4 wv = w[i];
-    const uint32_t ww[4] = {wv.x, wv.y, wv.z, wv.w};
+    uint4 wv[EE], xv[TT];
 #pragma unroll
-    for (int t = 0; t < TT; ++t) {
-      const uint4 xv = t0 + t < a.T ? x[(size_t)t * n + i] : make_uint4(0, 0, 0, 0);
-      const uint32_t xx[4] = {xv.x, xv.y, xv.z, xv.w};
+    for (int e = 0; e < EE; ++e) wv[e] = e0 + e < a.E ? w[(size_t)e * n + i] : make_uint4(0, 0, 0, 0);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        acc[t] = __fmaf_rn(bf16_lo(ww[j]), bf16_lo(xx[j]), acc[t]);
-        acc[t] = __fmaf_rn(bf16_hi(ww[j]), bf16_hi(xx[j]), acc[t]);
+    for (int t = 0; t < TT; ++t) xv[t] = t0 + t < a.T ? x[(size_t)t * n + i] : make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int e = 0; e < EE; ++e) {
+      const uint32_t ww[4] = {wv[e].x, wv[e].y, wv[e].z, wv[e].w};
+#pragma unroll
+      for (int t = 0; t < TT; ++t) {
+        const uint32_t xx[4] = {xv[t].x, xv[t].y, xv[t].z, xv[t].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          acc[e][t] = __fmaf_rn(bf16_lo(ww[j]), bf16_lo(xx[j]), acc[e][t]);
+          acc[e][t] = __fmaf_rn(bf16_hi(ww[j]), bf16_hi(xx[j]), acc[e][t]);
+        }
       }
     }
   }
 #pragma unroll
-  for (int t = 0; t < TT; ++t) {
+  for (int e = 0; e < EE; ++e)
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) acc[t] += __shfl_xor_sync(0xffffffffu, acc[t], o);
-    if (lane == 0) s_part[warp][t] = acc[t];
-  }
+    for (int t = 0; t < TT; ++t) {
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) acc[e][t] += __shfl_xor_sync(0xffffffffu, acc[e][t], o);
+      if (lane == 0) s_part[warp][e * TT + t] = acc[e][t];
+    }
   __syncthreads();
-  if (threadIdx.x < TT && t0 + (int)threadIdx.x < a.T) {
+  const int e = threadIdx.x / TT, t = threadIdx.x % TT;
+  if (e < EE && e0 + e < a.E && t0 + t < a.T) {
     float v = s_part[0][threadIdx.x];
 #pragma unroll
     for (int i = 1; i < PREP_THREADS / 32; ++i) v += s_part[i][threadIdx.x];
-    a.logits_ws[(size_t)(t0 + threadIdx.x) * a.E + e] = v;
+    a.logits_ws[(size_t)(t0 + t) * a.E + e0 + e] = v;
   }
 }
 
@@ -221,7 +234,7 @@ MOE_DEV void route_rows(const FewArgs& a, Smem& s, Routing& r) {
 
 // The list of the picked experts that are held here, in expert order, and their rows, in token order: row p of
 // an entry is row p of the activations and of Y.  A shared expert is entry 0, with rows T k .. T k + T - 1.
-// r.tokens is zero before.
+// r.tokens is zero before, r.held is set.
 template <class F>
 MOE_DEV void make_entries(const FewArgs& a, Smem& s, Routing& r) {
   constexpr int CHUNKS = MOE_FEW_MAX_EXPERTS / 32, PER = CHUNKS / 8;
@@ -230,7 +243,7 @@ MOE_DEV void make_entries(const FewArgs& a, Smem& s, Routing& r) {
   __syncthreads();
   for (int i = tid; i < slots; i += THREADS) {
     const int e = r.ids[i];
-    if (F::held(a, e)) atomicOr(&r.tokens[e], 1u << (i / a.k));
+    if (r.held[e]) atomicOr(&r.tokens[e], 1u << (i / a.k));
   }
   __syncthreads();
   const int sh = shared_entries(a);
@@ -390,13 +403,13 @@ MOE_DEV void load_rows(const FewArgs& a, Smem& s, uint32_t stages) {
     const Unit un = s.unit[slot];
     if (un.flags & END) break;
     typename F::Rows rows(a, s, un);
+    rows.fetch_scales(un.kb0);
     bool ok = true;
     for (int kb = un.kb0; kb < un.kb1; ++kb, ++i) {
       const int st = i % NS;
       ok = warp_wait(s.empty[st], (i / NS & 1) ^ 1, s, a.err);
       if (!ok) break;
       const uint32_t at = stages + st * F::STAGE;
-      rows.load_scales(kb, at);
       if (un.flags & DOWN && un.entry != seen) {
         ok = wait_count(a.ready + un.entry, (un.flags & SHARED ? a.Is : a.I) / F::KB, s, a.err);
         if (!ok) break;
@@ -404,6 +417,8 @@ MOE_DEV void load_rows(const FewArgs& a, Smem& s, uint32_t stages) {
       }
       rows.load(s, un, kb, at, s.scales[i % NF]);
       cp_async_arrive(smem_u32(&s.full[st]));
+      rows.store_scales(at, smem_u32(&s.full[st]));
+      if (kb + 1 < un.kb1) rows.fetch_scales(kb + 1);
     }
     if (!ok) break;
     __syncwarp();
@@ -415,7 +430,10 @@ MOE_DEV void load_rows(const FewArgs& a, Smem& s, uint32_t stages) {
   if (*(volatile int*)&s.abort) {
     const uint64_t t0 = globaltimer_ns();
     while (s.issued < 0 && globaltimer_ns() - t0 < kWaitLimitNs) __nanosleep(100);
-    for (; i < s.issued; ++i) cp_async_arrive(smem_u32(&s.full[i % NS]));
+    for (; i < s.issued; ++i) {
+      cp_async_arrive(smem_u32(&s.full[i % NS]));
+      F::Rows::arrive_scales(smem_u32(&s.full[i % NS]));
+    }
   }
 }
 
@@ -700,7 +718,10 @@ __global__ void __launch_bounds__(THREADS, PER_SM) few_kernel(const __grid_const
     tmem_relinquish();
   }
   if (warp == 0) F::prefetch(a, maps);
-  for (int e = threadIdx.x; e < a.E; e += THREADS) r.tokens[e] = 0;
+  for (int e = threadIdx.x; e < a.E; e += THREADS) {
+    r.tokens[e] = 0;
+    r.held[e] = F::held(a, e);
+  }
   griddep_wait();
   griddep_launch_dependents();
   // (the first draws' answers come while the tokens are routed)
@@ -750,7 +771,7 @@ int launch(const FewArgs& a, const typename F::Maps& maps, cudaStream_t st) {
   static_assert(PER_SM * (smem + sizeof(Smem) + 1024) <= 228 * 1024 && PER_SM * F::TMEM_COLS <= 512, "CTAs per SM");
   static_assert(NS * F::STAGE >= (int)sizeof(Routing), "the routing has its arrays in the stages");
   using Prep = void (*)(FewArgs);
-  const Prep preps[4] = {prep_kernel<F, 1>, prep_kernel<F, 2>, prep_kernel<F, 4>, prep_kernel<F, 8>};
+  const Prep preps[3] = {prep_kernel<F, 1, 1>, prep_kernel<F, 1, 4>, prep_kernel<F, 4, 4>};
   static std::atomic<uint64_t> configured{0};  // a bit per device
   const int dev = current_device_index();
   if (dev < 0) return MOE_ERR_CUDA;
@@ -763,9 +784,12 @@ int launch(const FewArgs& a, const typename F::Maps& maps, cudaStream_t st) {
       if (cudaFuncSetAttribute(p, cudaFuncAttributePreferredSharedMemoryCarveout, 100) != cudaSuccess) return MOE_ERR_CUDA;
     configured.fetch_or(1ull << (dev & 63), std::memory_order_relaxed);
   }
+  // one token's rows take no longer than their latency, so an expert to a block spreads them best; many tokens' rows are
+  // read again for each expert, or for four of them
+  const int which = a.T == 1 ? 0 : a.T <= 4 ? 1 : 2, ee = which == 2 ? 4 : 1, tt = which == 0 ? 1 : 4;
   const int blocks = 1 + (a.x_made != nullptr ? a.T : 0) +
-                     (a.logits == nullptr ? a.E * ((a.T + PREP_TOKENS - 1) / PREP_TOKENS) : 0);
-  const Prep prep = preps[a.T == 1 ? 0 : a.T <= 2 ? 1 : a.T <= 4 ? 2 : 3];
+                     (a.logits == nullptr ? (a.E + ee - 1) / ee * ((a.T + tt - 1) / tt) : 0);
+  const Prep prep = preps[which];
   const int rc = launch_pdl(prep, dim3(blocks), dim3(PREP_THREADS), 0, st, a);
   if (rc != MOE_OK) return rc;
   return launch_pdl(few_kernel<F>, dim3(nsm * PER_SM), dim3(THREADS), smem, st, a, maps);

@@ -86,7 +86,9 @@ struct Fp8 {
              ((size_t)e * blocks + block) * groups + un.kb0;
       }
     }
-    MOE_DEV void load_scales(int, uint32_t) const {}  // (with the rows')
+    MOE_DEV void fetch_scales(int) const {}  // (they come with the rows')
+    MOE_DEV void store_scales(uint32_t, uint32_t) const {}
+    MOE_DEV static void arrive_scales(uint32_t) {}
     MOE_DEV void load(Smem&, const Unit& un, int, uint32_t at, float* scales) {
       const int lane = lane_id(), piece = lane & 7;
 #pragma unroll

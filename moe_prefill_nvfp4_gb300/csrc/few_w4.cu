@@ -34,6 +34,10 @@ MOE_DEV void tmem_ld_32x32b_x4(uint32_t taddr, uint32_t (&r)[12]) {  // into the
                : "memory");
 }
 
+MOE_DEV void sts128(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+
 // 32 rows of 16 bytes of shared memory to four columns of tensor memory, for each of its four quarters of lanes.
 MOE_DEV void tmem_copy_scales(uint32_t taddr, uint32_t at) {
   const uint64_t desc = (uint64_t)((at & 0x3FFFFu) >> 4) | ((uint64_t)(128 >> 4) << 32) | ((uint64_t)1 << 46);
@@ -74,7 +78,7 @@ struct W4 {
   static constexpr int MAX_N = NT * PIECES, SF = 512, ROWS = 2 * BLK, SCALES_A = ROWS + MAX_N * RB,
                        SCALES_B = SCALES_A + 8 * SF, STAGE = SCALES_B + 4 * SF;
   static constexpr int TMEM_COLS = 256, TMEM_SCALES = 208;  // (32 columns of the weight's scales, 16 of the pieces')
-  static constexpr int FULL_ARRIVALS = 1 + 32;
+  static constexpr int FULL_ARRIVALS = 1 + 32 + 1;
   static_assert(STAGE % 1024 == 0 && 2 * MAX_N <= TMEM_SCALES && MAX_N <= 128, "");
 
   struct Maps {};
@@ -141,26 +145,43 @@ struct W4 {
   struct Rows {
     const uint8_t* of;
     size_t pitch;
-    const uint8_t* scales[2];  // this lane's of the weight's: of every eighth row 4 of a block's 16, of the rows' halves
+    const uint8_t* scales[2];  // this lane's of the weight's, one of 32 rows, of the rows' two halves
     int scale_pitch;
+    uint4 v[2][4];
     MOE_DEV Rows(const FewArgs& a, const Smem&, const Unit& un) {
       const bool down = un.flags & DOWN;
-      const int row = un.place * (down ? 256 : 128) + lane_id() / 4;
+      const int row = un.place * (down ? 256 : 128) + lane_id();
       scale_pitch = (down ? a.I : a.H) / 16;
-      const uint8_t* w = static_cast<const uint8_t*>(a.w4[down ? 1 : 0].scales[un.expert]) + lane_id() % 4 * 4;
+      const uint8_t* w = static_cast<const uint8_t*>(a.w4[down ? 1 : 0].scales[un.expert]);
       scales[0] = w + (size_t)row * scale_pitch;
       scales[1] = w + (size_t)(row + (down ? 128 : a.I)) * scale_pitch;
       pitch = (size_t)((down ? a.I : a.H) / KB) * BLOCK_BYTES;
       of = down ? a.act_codes : a.x_made;
     }
-    MOE_DEV void load_scales(int kb, uint32_t at) const {
-      const uint32_t to = at + SCALES_A + lane_id() % 4 * SF + lane_id() / 4 * 16;
+    // A block's 16 scales of four rows of each half to a lane, and from there to where the MMA wants them.  (As copies
+    // of 4 bytes past the registers they took 3 us more of 48, one token, and 5 of 209, 16 tokens.)
+    MOE_DEV void fetch_scales(int kb) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          v[h][j] = __ldg(reinterpret_cast<const uint4*>(scales[h] + (size_t)(32 * j) * scale_pitch + kb * 16));
+    }
+    MOE_DEV void store_scales(uint32_t at, uint32_t full) const {
+      const uint32_t to = at + SCALES_A + lane_id() * 16;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const uint8_t* src = scales[h] + kb * 16;
-#pragma unroll
-        for (int j = 0; j < 16; ++j, src += 8 * scale_pitch) cp_async4(to + h * 4 * SF + j % 4 * 128 + j / 4 * 4, src);
+        const uint4 (&w)[4] = v[h];
+        sts128(to + (h * 4 + 0) * SF, w[0].x, w[1].x, w[2].x, w[3].x);
+        sts128(to + (h * 4 + 1) * SF, w[0].y, w[1].y, w[2].y, w[3].y);
+        sts128(to + (h * 4 + 2) * SF, w[0].z, w[1].z, w[2].z, w[3].z);
+        sts128(to + (h * 4 + 3) * SF, w[0].w, w[1].w, w[2].w, w[3].w);
       }
+      arrive_scales(full);
+    }
+    MOE_DEV static void arrive_scales(uint32_t full) {
+      __syncwarp();
+      if (lane_id() == 0) mbar_arrive(full);
     }
     MOE_DEV void load(const Smem& s, const Unit& un, int kb, uint32_t at, float* factors) const {
       const int lane = lane_id();
