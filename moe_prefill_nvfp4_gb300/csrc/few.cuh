@@ -26,7 +26,7 @@
 // What differs between the weights' formats is in a class F:
 //   KB                       columns of a k block (of the weights' 128 bytes, one swizzle row)
 //   STAGE                    bytes of a stage: 256 weight rows of 128 bytes, then what goes with them
-//   TMEM_COLS, accumulators(a)   tensor memory, and how many accumulators it is divided into
+//   TMEM_COLS, accumulators(most)   tensor memory, and the accumulators in it for units of that many tokens at most
 //   FULL_ARRIVALS            arrivals that make a stage full: the weights' bytes, lanes whose copies have landed
 //   Maps, held(a, e)         tensor maps by value, whether expert e is here
 //   Weights, Rows            the loads of a unit's k blocks: the weights; their scales through
@@ -55,8 +55,8 @@ constexpr int ND = 8;              // accumulators, at most
 constexpr int NF = 16;             // k blocks whose scales are held, more than accumulators and stages together
 constexpr int F_SLOT = NT + 4;     // the rows' scales, then the weight's
 constexpr int DRAWN = 8;           // units that a CTA has drawn and not finished
-// warps: 0 draws and loads weights, 1 issues MMAs, 2-5 epilogue, 6 loads activations, 7 publishes, 8 finishes
-constexpr int WARPS = 9;
+// warps: 0 draws and loads weights, 1 issues MMAs, 2-5 epilogue, 6 loads activations, 7 publishes, 8 and 9 finish
+constexpr int WARPS = 10;
 constexpr int THREADS = 32 * WARPS;
 constexpr int PER_SM = 2;
 constexpr int MAX_T = MOE_FEW_MAX_TOKENS;
@@ -80,11 +80,12 @@ struct Smem {
   Unit unit[DRAWN];
   alignas(16) float scales[NF][F_SLOT];
   uint32_t tmem;
-  int routed, abort;
+  int routed, rows, most, abort;     // picked experts, their rows, tokens of one at most
   volatile int issued;               // k blocks whose weights were loaded, -1 before the end
   float wts[MAX_SLOTS];
   short pos[MAX_SLOTS];              // row of slot (t, s), -1: of an expert held elsewhere
   uint8_t token[MAX_SLOTS + MAX_T];  // of row p
+  short entry_of[MAX_SLOTS];         // of row p, not of a shared expert's
   Entry entry[MAX_SLOTS + 1];
 };
 static_assert(offsetof(Smem, scales) % 16 == 0 && F_SLOT % 4 == 0, "read by 16 bytes");
@@ -274,13 +275,19 @@ MOE_DEV void make_entries(const FewArgs& a, Smem& s, Routing& r) {
       const int at = before + sums[c] - (m | 1 << 16), first = at & 0xFFFF;
       r.first[e] = (short)first;
       s.entry[sh + (at >> 16)] = Entry{e - a.first, (short)m, (short)first};
+      atomicMax(&s.most, m);
       int q = first;
-      for (uint32_t b = mine[c]; b != 0; b &= b - 1) s.token[q++] = (uint8_t)(__ffs(b) - 1);
+      for (uint32_t b = mine[c]; b != 0; b &= b - 1, ++q) {
+        s.token[q] = (uint8_t)(__ffs(b) - 1);
+        s.entry_of[q] = (short)(sh + (at >> 16));
+      }
     }
     before += __shfl_sync(0xffffffffu, sums[c], 31);
   }
   if (tid == 0) {
     s.routed = all >> 16;
+    s.rows = all & 0xFFFF;
+    s.most = max(s.most, sh ? a.T : 0);
     if (sh) s.entry[0] = Entry{-1, (short)a.T, (short)slots};
   }
   if (sh && tid < a.T) s.token[slots + tid] = (uint8_t)tid;
@@ -411,7 +418,7 @@ MOE_DEV void load_rows(const FewArgs& a, Smem& s, uint32_t stages) {
       if (!ok) break;
       const uint32_t at = stages + st * F::STAGE;
       if (un.flags & DOWN && un.entry != seen) {
-        ok = wait_count(a.ready + un.entry, (un.flags & SHARED ? a.Is : a.I) / F::KB, s, a.err);
+        ok = wait_count(a.ready + un.entry, un.m * ((un.flags & SHARED ? a.Is : a.I) / F::KB), s, a.err);
         if (!ok) break;
         seen = un.entry;
       }
@@ -440,7 +447,7 @@ MOE_DEV void load_rows(const FewArgs& a, Smem& s, uint32_t stages) {
 // Issues the MMAs of every stage, with an accumulator to each k block.
 template <class F>
 MOE_DEV void multiply(const FewArgs& a, Smem& s, uint32_t stages) {
-  const int nd = F::accumulators(a);
+  const int nd = F::accumulators(s.most);
   int i = 0, db = 0, turn = 0;
   bool ok = true;
   for (int n = 0; ok; ++n) {
@@ -458,7 +465,7 @@ MOE_DEV void multiply(const FewArgs& a, Smem& s, uint32_t stages) {
       fence_proxy_async_shared();  // (the rows came through the generic proxy)
       tc_fence_after();
       if (elect_one()) {
-        F::multiply(a, s.tmem, db, stages + st * F::STAGE, m);
+        F::multiply(s.tmem, db, stages + st * F::STAGE, m, s.most);
         mma_commit(smem_u32(&s.d_full[db]));
         mma_commit(smem_u32(&s.empty[st]));
       }
@@ -483,7 +490,7 @@ template <class F>
 MOE_DEV void epilogue(const FewArgs& a, Smem& s) {
   const int lane = lane_id(), warp = threadIdx.x >> 5, q = warp & 3, wr = q * 32 + lane;
   const uint32_t lane_base = s.tmem + ((uint32_t)(q * 32) << 16);
-  const int nd = F::accumulators(a);
+  const int nd = F::accumulators(s.most);
   int i = 0, db = 0, turn = 0;
   for (int n = 0;; ++n) {
     const int slot = n % DRAWN;
@@ -498,7 +505,7 @@ MOE_DEV void epilogue(const FewArgs& a, Smem& s) {
     for (int kb = un.kb0; kb < un.kb1; ++kb, ++i) {
       if (!warp_wait(s.d_full[db], turn, s, a.err)) return;
       tc_fence_after();
-      F::add(a, acc, lane_base, db, s.scales[i % NF], un.m, smem_u32(&s.d_empty[db]));
+      F::add(acc, lane_base, db, s.scales[i % NF], un.m, s.most, smem_u32(&s.d_empty[db]));
       if (++db == nd) {
         db = 0;
         turn ^= 1;
@@ -548,53 +555,51 @@ MOE_DEV void publish(const FewArgs& a, Smem& s) {
 // ------------------------------------------------------------------------------------------------
 // few: what follows the products
 
-// All units of a block of KB activations of an entry are stored: the whole warp adds up their slices, makes the
-// activations, and brings them into the down products' form.
+// All units of a block of KB activations of an entry are stored: the whole warp adds up the slices of its row r, makes
+// the activations, and brings them into the down products' form.
 template <class F>
-MOE_DEV void finish_block(const FewArgs& a, Smem& s, int entry, int kb) {
-  constexpr int QUADS = F::LANE / 4, AT_ONCE = 5 / QUADS;
+MOE_DEV void finish_block(const FewArgs& a, Smem& s, int entry, int kb, int r) {
+  constexpr int QUADS = F::LANE / 4, AT_ONCE = 4 / QUADS;
   const Entry en = s.entry[entry];
   const bool is_shared = en.expert < 0;
   const int inter = is_shared ? a.Is : a.I, first = is_shared ? 0 : en.first;
   const float limit = is_shared ? a.shared_limit : a.limit;
   const size_t slice = (size_t)(is_shared ? a.T : a.T * a.k) * 2 * inter;
-  const float* gu = (is_shared ? a.gu_shared : a.gu) + (size_t)first * 2 * inter + kb * F::KB + lane_id() * F::LANE;
-  for (int r = 0; r < en.m; ++r, gu += 2 * inter) {
-    float4 gate[QUADS], up[QUADS];
+  const float* gu = (is_shared ? a.gu_shared : a.gu) + (size_t)(first + r) * 2 * inter + kb * F::KB + lane_id() * F::LANE;
+  float4 gate[QUADS], up[QUADS];
 #pragma unroll
-    for (int j = 0; j < QUADS; ++j) gate[j] = up[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int i0 = 0; i0 < a.slices[0]; i0 += AT_ONCE) {
-      float4 p[AT_ONCE][QUADS], q[AT_ONCE][QUADS];
+  for (int j = 0; j < QUADS; ++j) gate[j] = up[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i0 = 0; i0 < a.slices[0]; i0 += AT_ONCE) {
+    float4 p[AT_ONCE][QUADS], q[AT_ONCE][QUADS];
 #pragma unroll
-      for (int i = 0; i < AT_ONCE; ++i)
-        if (i0 + i < a.slices[0]) {
-          const float4* at = reinterpret_cast<const float4*>(gu + (i0 + i) * slice);
+    for (int i = 0; i < AT_ONCE; ++i)
+      if (i0 + i < a.slices[0]) {
+        const float4* at = reinterpret_cast<const float4*>(gu + (i0 + i) * slice);
 #pragma unroll
-          for (int j = 0; j < QUADS; ++j) {
-            p[i][j] = __ldcg(at + j);
-            q[i][j] = __ldcg(at + inter / 4 + j);
-          }
+        for (int j = 0; j < QUADS; ++j) {
+          p[i][j] = __ldcg(at + j);
+          q[i][j] = __ldcg(at + inter / 4 + j);
         }
+      }
 #pragma unroll
-      for (int i = 0; i < AT_ONCE; ++i)
-        if (i0 + i < a.slices[0])
+    for (int i = 0; i < AT_ONCE; ++i)
+      if (i0 + i < a.slices[0])
 #pragma unroll
-          for (int j = 0; j < QUADS; ++j) {
-            gate[j] = make_float4(gate[j].x + p[i][j].x, gate[j].y + p[i][j].y, gate[j].z + p[i][j].z, gate[j].w + p[i][j].w);
-            up[j] = make_float4(up[j].x + q[i][j].x, up[j].y + q[i][j].y, up[j].z + q[i][j].z, up[j].w + q[i][j].w);
-          }
-    }
-    float v[F::LANE];
-#pragma unroll
-    for (int j = 0; j < QUADS; ++j) {
-      v[4 * j] = swiglu_keep_nan<false>(gate[j].x, up[j].x, limit);
-      v[4 * j + 1] = swiglu_keep_nan<false>(gate[j].y, up[j].y, limit);
-      v[4 * j + 2] = swiglu_keep_nan<false>(gate[j].z, up[j].z, limit);
-      v[4 * j + 3] = swiglu_keep_nan<false>(gate[j].w, up[j].w, limit);
-    }
-    F::write_block(v, is_shared ? a.act_codes_shared : a.act_codes, is_shared ? a.act_scales_shared : a.act_scales,
-                   first + r, kb, inter / F::KB, F::scale_pitch(inter / F::KB));
+        for (int j = 0; j < QUADS; ++j) {
+          gate[j] = make_float4(gate[j].x + p[i][j].x, gate[j].y + p[i][j].y, gate[j].z + p[i][j].z, gate[j].w + p[i][j].w);
+          up[j] = make_float4(up[j].x + q[i][j].x, up[j].y + q[i][j].y, up[j].z + q[i][j].z, up[j].w + q[i][j].w);
+        }
   }
+  float v[F::LANE];
+#pragma unroll
+  for (int j = 0; j < QUADS; ++j) {
+    v[4 * j] = swiglu_keep_nan<false>(gate[j].x, up[j].x, limit);
+    v[4 * j + 1] = swiglu_keep_nan<false>(gate[j].y, up[j].y, limit);
+    v[4 * j + 2] = swiglu_keep_nan<false>(gate[j].z, up[j].z, limit);
+    v[4 * j + 3] = swiglu_keep_nan<false>(gate[j].w, up[j].w, limit);
+  }
+  F::write_block(v, is_shared ? a.act_codes_shared : a.act_codes, is_shared ? a.act_scales_shared : a.act_scales,
+                 first + r, kb, inter / F::KB, F::scale_pitch(inter / F::KB));
   __syncwarp();
   if (lane_id() == 0) counter_add_release(a.ready + entry, 1);
 }
@@ -653,12 +658,14 @@ MOE_DEV void finish_columns(const FewArgs& a, Smem& s, int place, int t0) {
   }
 }
 
-// Finishes what all its units are stored of: each entry's blocks of activations, then the columns of the result, drawn
-// in this order.  One warp of a CTA does so from the start, the others when their own work is done.
+// Finishes what all its units are stored of: each entry's blocks of activations, row by row, then the columns of the
+// result, drawn in this order.  Two warps of a CTA do so from the start, the others when their own work is done.
+// (A task of all of an expert's rows takes too long where it has many: 16 tokens at 8 experts, all picked by all, took
+// 92 us in FP8, and @@.)
 template <class F>
 MOE_DEV void finish(const FewArgs& a, Smem& s, int drawn) {
-  const int sh = shared_entries(a), entries = s.routed + sh, per_entry = a.I / F::KB, blocks_shared = a.Is / F::KB;
-  const int blocks = blocks_shared + s.routed * per_entry, places = a.H / 32;
+  const int sh = shared_entries(a), entries = s.routed + sh, per_row = a.I / F::KB, places = a.H / 32;
+  const int shared_blocks = sh * a.T * (a.Is / F::KB), blocks = shared_blocks + s.rows * per_row;
   const int total = blocks + places * (a.T <= 2 ? a.T : (a.T + 1) / 2);
   for (;;) {
     const int u = __shfl_sync(0xffffffffu, drawn, 0);
@@ -672,16 +679,16 @@ MOE_DEV void finish(const FewArgs& a, Smem& s, int drawn) {
       else
         finish_columns<2, 4, 2>(a, s, place, 2 * t);
     } else {
-      int v = u - blocks_shared, e = 0;
-      if (v < 0) {
-        v = u;
-      } else {
-        e = v / per_entry;
-        v -= e * per_entry;
-        e += sh;
+      int v = u, e = 0, m = a.T;
+      if (u >= shared_blocks) {
+        v -= shared_blocks;
+        e = s.entry_of[v / per_row];
+        m = s.entry[e].m;
+        v -= s.entry[e].first * per_row;
       }
-      if (!wait_count(a.block_done + e * a.blocks_max + v, a.slices[0] * F::KB / 128, s, a.err)) return;
-      finish_block<F>(a, s, e, v);
+      const int kb = v / m;
+      if (!wait_count(a.block_done + e * a.blocks_max + kb, a.slices[0] * F::KB / 128, s, a.err)) return;
+      finish_block<F>(a, s, e, kb, v - kb * m);
     }
   }
 }
@@ -711,6 +718,7 @@ __global__ void __launch_bounds__(THREADS, PER_SM) few_kernel(const __grid_const
     mbar_init(smem_u32(&s.drain), 1);
     s.issued = -1;
     s.abort = 0;
+    s.most = 0;
     fence_barrier_init();
   }
   if (warp == 1) {
@@ -729,7 +737,7 @@ __global__ void __launch_bounds__(THREADS, PER_SM) few_kernel(const __grid_const
   if (warp == 0) {
     u0 = draw(a.counters);
     u1 = draw(a.counters);
-  } else if (warp == WARPS - 1) {
+  } else if (warp >= 8) {
     u0 = draw(a.counters + 32);
   }
   make_entries<F>(a, s, r);
@@ -753,7 +761,7 @@ __global__ void __launch_bounds__(THREADS, PER_SM) few_kernel(const __grid_const
   }
   __syncwarp();
   if (s.routed + shared_entries(a) > 0 && !*(volatile int*)&s.abort)
-    finish<F>(a, s, warp == WARPS - 1 ? u0 : draw(a.counters + 32));
+    finish<F>(a, s, warp >= 8 ? u0 : draw(a.counters + 32));
   __syncwarp();
   tc_fence_before();
   __syncthreads();

@@ -20,7 +20,7 @@ struct Fp8 {
     if (lane_id() < (a.Is > 0 ? 4 : 2)) prefetch_tmap(&maps.w[lane_id()]);
   }
   MOE_DEV static bool held(const FewArgs& a, int e) { return e >= a.first && e < a.first + a.count; }
-  MOE_DEV static int accumulators(const FewArgs&) { return ND; }
+  MOE_DEV static int accumulators(int) { return ND; }
 
   // Distance of an activation row's scales: rows share no 128 bytes, so that an SM whose L1 has one row's does not
   // have another's from before they were made.
@@ -102,14 +102,14 @@ struct Fp8 {
     }
   };
 
-  MOE_DEV static void multiply(const FewArgs&, uint32_t tmem, int db, uint32_t at, int) {
+  MOE_DEV static void multiply(uint32_t tmem, int db, uint32_t at, int, int) {
     constexpr uint32_t idesc = make_idesc_e4m3(128, NT);
     const uint64_t rows = make_sdesc_sw128(at + 2 * BLK);
     mma4_e4m3_ss(tmem + (uint32_t)(db * 2 * NT), make_sdesc_sw128(at), rows, idesc);
     mma4_e4m3_ss(tmem + (uint32_t)(db * 2 * NT + NT), make_sdesc_sw128(at + BLK), rows, idesc);
   }
 
-  MOE_DEV static void add(const FewArgs&, uint64_t (&acc)[2][NT / 2], uint32_t lane_base, int db, const float* f, int, uint32_t d_empty) {
+  MOE_DEV static void add(uint64_t (&acc)[2][NT / 2], uint32_t lane_base, int db, const float* f, int, int, uint32_t d_empty) {
     uint32_t v[2][16];
     tmem_ld_32x32b_x16(lane_base + (uint32_t)(db * 2 * NT), v[0]);
     tmem_ld_32x32b_x16(lane_base + (uint32_t)(db * 2 * NT + NT), v[1]);

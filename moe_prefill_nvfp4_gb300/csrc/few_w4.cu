@@ -86,7 +86,7 @@ struct W4 {
   MOE_DEV static bool held(const FewArgs& a, int e) { return a.w4[0].packed[e] != nullptr && a.w4[1].packed[e] != nullptr; }
   // Columns of an accumulator's half of 128 weight rows; as many accumulators as fit.
   MOE_DEV static int columns(int m) { return (m * PIECES + 15) / 16 * 16; }
-  MOE_DEV static int accumulators(const FewArgs& a) { return min(ND, TMEM_SCALES / (2 * columns(a.T))); }
+  MOE_DEV static int accumulators(int most) { return min(ND, TMEM_SCALES / (2 * columns(most))); }
 
   __host__ __device__ static constexpr int scale_pitch(int blocks) { return blocks; }
 
@@ -201,9 +201,9 @@ struct W4 {
     }
   };
 
-  MOE_DEV static void multiply(const FewArgs& a, uint32_t tmem, int db, uint32_t at, int m) {
+  MOE_DEV static void multiply(uint32_t tmem, int db, uint32_t at, int m, int most) {
     const uint32_t idesc = make_idesc_nvfp4(128, columns(m));
-    const int half = columns(a.T);
+    const int half = columns(most);
     const uint64_t rows = make_sdesc_sw128(at + ROWS);
 #pragma unroll
     for (int k64 = 0; k64 < 4; ++k64) {
@@ -219,16 +219,17 @@ struct W4 {
     }
   }
 
-  MOE_DEV static void add(const FewArgs& a, uint64_t (&acc)[2][NT / 2], uint32_t lane_base, int db, const float* f, int m,
+  MOE_DEV static void add(uint64_t (&acc)[2][NT / 2], uint32_t lane_base, int db, const float* f, int m, int most,
                           uint32_t d_empty) {
-    const uint32_t at = lane_base + (uint32_t)(2 * db * columns(a.T));
+    const int half = columns(most);
+    const uint32_t at = lane_base + (uint32_t)(2 * db * half);
 #pragma unroll
     for (int j = 0; j < NT / 2; ++j) {
       if (2 * j < m) {  // two tokens at once
         uint32_t v[2][2 * PIECES];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const uint32_t from = at + (uint32_t)(h * columns(a.T) + j * 2 * PIECES);
+          const uint32_t from = at + (uint32_t)(h * half + j * 2 * PIECES);
           tmem_ld_32x32b_x8(from, v[h]);
           tmem_ld_32x32b_x4(from + 8, v[h]);
         }
