@@ -29,8 +29,7 @@
 //   TMEM_COLS, accumulators(most)   tensor memory, and the accumulators in it for units of that many tokens at most
 //   FULL_ARRIVALS            arrivals that make a stage full: the weights' bytes, lanes whose copies have landed
 //   Maps, held(a, e)         tensor maps by value, whether expert e is here
-//   Weights, Rows            the loads of a unit's k blocks: the weights; their scales through
-//                            registers (fetch_scales, store_scales), and the rows with theirs
+//   Weights, Rows            the loads of a unit's k blocks: the weights, and the rows with their scales
 //   multiply, add            a stage's MMAs, an accumulator's scaling and addition
 //   output_scale(a, expert)  factor of a unit's sums
 //   LANE, write_block        a block of KB columns of a row, LANE to a lane, into the operand's form
@@ -97,6 +96,14 @@ struct Routing {
   int sums[MOE_FEW_MAX_EXPERTS / 32];    // of 32 experts each: rows, experts << 16
   bool held[MOE_FEW_MAX_EXPERTS];        // the expert is here
 };
+
+// The weights are read once and are more than L2 holds: as the first to be evicted they leave it to what every layer
+// needs again, above all to this kernel's instructions.
+MOE_DEV uint64_t streaming_policy() {
+  uint64_t p;
+  asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+  return p;
+}
 
 MOE_DEV uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
 
@@ -410,7 +417,6 @@ MOE_DEV void load_rows(const FewArgs& a, Smem& s, uint32_t stages) {
     const Unit un = s.unit[slot];
     if (un.flags & END) break;
     typename F::Rows rows(a, s, un);
-    rows.fetch_scales(un.kb0);
     bool ok = true;
     for (int kb = un.kb0; kb < un.kb1; ++kb, ++i) {
       const int st = i % NS;
@@ -424,8 +430,6 @@ MOE_DEV void load_rows(const FewArgs& a, Smem& s, uint32_t stages) {
       }
       rows.load(s, un, kb, at, s.scales[i % NF]);
       cp_async_arrive(smem_u32(&s.full[st]));
-      rows.store_scales(at, smem_u32(&s.full[st]));
-      if (kb + 1 < un.kb1) rows.fetch_scales(kb + 1);
     }
     if (!ok) break;
     __syncwarp();
@@ -439,7 +443,6 @@ MOE_DEV void load_rows(const FewArgs& a, Smem& s, uint32_t stages) {
     while (s.issued < 0 && globaltimer_ns() - t0 < kWaitLimitNs) __nanosleep(100);
     for (; i < s.issued; ++i) {
       cp_async_arrive(smem_u32(&s.full[i % NS]));
-      F::Rows::arrive_scales(smem_u32(&s.full[i % NS]));
     }
   }
 }

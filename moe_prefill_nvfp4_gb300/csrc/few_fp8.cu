@@ -8,6 +8,14 @@
 namespace moe {
 namespace few {
 
+MOE_DEV void tma_load_3d(uint32_t dst, const void* tmap, int x, int y, int z, uint32_t bar, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, {%2, %3, %4}], "
+      "[%5], %6;" ::"r"(dst),
+      "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(bar), "l"(policy)
+      : "memory");
+}
+
 struct Fp8 {
   static constexpr int KB = BK, G = KB, LANE = 4, LEAST = 4, BLOCK_BYTES = KB;
   static constexpr int STAGE = 2 * BLK + NT * BK, TMEM_COLS = ND * 2 * NT;
@@ -38,7 +46,8 @@ struct Fp8 {
   struct Weights {
     const CUtensorMap* map;
     int e, row0, row1;
-    MOE_DEV Weights(const FewArgs& a, const Maps& maps, const Unit& un) {
+    uint64_t policy;
+    MOE_DEV Weights(const FewArgs& a, const Maps& maps, const Unit& un) : policy(streaming_policy()) {
       const bool down = un.flags & DOWN, is_shared = un.flags & SHARED;
       map = &maps.w[(is_shared ? 2 : 0) + (down ? 1 : 0)];
       e = is_shared ? 0 : un.expert;
@@ -48,8 +57,8 @@ struct Fp8 {
     MOE_DEV void load(int kb, uint32_t at, uint32_t full) const {
       if (elect_one()) {
         mbar_arrive_expect_tx(full, 2 * BLK);  // (rows past the weight's come as zeros)
-        tma_load_3d(at, map, kb * BK, row0, e, full);
-        tma_load_3d(at + BLK, map, kb * BK, row1, e, full);
+        tma_load_3d(at, map, kb * BK, row0, e, full, policy);
+        tma_load_3d(at + BLK, map, kb * BK, row1, e, full, policy);
       }
       __syncwarp();
     }
@@ -86,9 +95,6 @@ struct Fp8 {
              ((size_t)e * blocks + block) * groups + un.kb0;
       }
     }
-    MOE_DEV void fetch_scales(int) const {}  // (they come with the rows')
-    MOE_DEV void store_scales(uint32_t, uint32_t) const {}
-    MOE_DEV static void arrive_scales(uint32_t) {}
     MOE_DEV void load(Smem&, const Unit& un, int, uint32_t at, float* scales) {
       const int lane = lane_id(), piece = lane & 7;
 #pragma unroll

@@ -34,6 +34,14 @@ MOE_DEV void tmem_ld_32x32b_x4(uint32_t taddr, uint32_t (&r)[12]) {  // into the
                : "memory");
 }
 
+// (Issued where it stands, a block ahead of its use: the compiler would move a plain load down to that, with 16 tokens
+// in 230 us instead of 200.)
+MOE_DEV uint4 load_once(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
+
 MOE_DEV void sts128(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
@@ -65,6 +73,14 @@ MOE_DEV uint32_t pack_e2m1x8(const float (&v)[8]) {
       : "=r"(out)
       : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
   return out;
+}
+
+MOE_DEV void tma_load_2d(uint32_t dst, const void* tmap, int x, int y, uint32_t bar, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, {%2, %3}], [%4], "
+      "%5;" ::"r"(dst),
+      "l"(tmap), "r"(x), "r"(y), "r"(bar), "l"(policy)
+      : "memory");
 }
 
 struct W4 {
@@ -125,38 +141,21 @@ struct W4 {
 
   struct Weights {
     const uint8_t* map;
-    int row0, row1;
-    MOE_DEV Weights(const FewArgs& a, const Maps&, const Unit& un) {
+    int row0, row1, scale_pitch, end;
+    uint64_t policy;
+    const uint8_t* scales[2];  // this lane's, one of 32 rows, of the rows' two halves
+    uint4 v[2][4];
+    MOE_DEV Weights(const FewArgs& a, const Maps&, const Unit& un) : end(un.kb1), policy(streaming_policy()) {
       const bool down = un.flags & DOWN;
-      map = static_cast<const uint8_t*>(a.w4[down ? 1 : 0].maps) + (size_t)un.expert * 2 * sizeof(CUtensorMap);
+      const FewW4Weight& w = a.w4[down ? 1 : 0];
+      map = static_cast<const uint8_t*>(w.maps) + (size_t)un.expert * 2 * sizeof(CUtensorMap);
       row0 = un.place * (down ? 256 : 128);
       row1 = row0 + (down ? 128 : a.I);
-    }
-    MOE_DEV void load(int kb, uint32_t at, uint32_t full) const {
-      if (elect_one()) {
-        mbar_arrive_expect_tx(full, 2 * BLK);
-        tma_load_2d(at, map, kb * RB, row0, full);
-        tma_load_2d(at + BLK, map, kb * RB, row1, full);
-      }
-      __syncwarp();
-    }
-  };
-
-  struct Rows {
-    const uint8_t* of;
-    size_t pitch;
-    const uint8_t* scales[2];  // this lane's of the weight's, one of 32 rows, of the rows' two halves
-    int scale_pitch;
-    uint4 v[2][4];
-    MOE_DEV Rows(const FewArgs& a, const Smem&, const Unit& un) {
-      const bool down = un.flags & DOWN;
-      const int row = un.place * (down ? 256 : 128) + lane_id();
       scale_pitch = (down ? a.I : a.H) / 16;
-      const uint8_t* w = static_cast<const uint8_t*>(a.w4[down ? 1 : 0].scales[un.expert]);
-      scales[0] = w + (size_t)row * scale_pitch;
-      scales[1] = w + (size_t)(row + (down ? 128 : a.I)) * scale_pitch;
-      pitch = (size_t)((down ? a.I : a.H) / KB) * BLOCK_BYTES;
-      of = down ? a.act_codes : a.x_made;
+      const uint8_t* of = static_cast<const uint8_t*>(w.scales[un.expert]);
+      scales[0] = of + (size_t)(row0 + lane_id()) * scale_pitch;
+      scales[1] = of + (size_t)(row1 + lane_id()) * scale_pitch;
+      fetch_scales(un.kb0);
     }
     // A block's 16 scales of four rows of each half to a lane, and from there to where the MMA wants them.  (As copies
     // of 4 bytes past the registers they took 3 us more of 48, one token, and 5 of 209, 16 tokens.)
@@ -165,7 +164,7 @@ struct W4 {
       for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          v[h][j] = __ldg(reinterpret_cast<const uint4*>(scales[h] + (size_t)(32 * j) * scale_pitch + kb * 16));
+          v[h][j] = load_once(scales[h] + (size_t)(32 * j) * scale_pitch + kb * 16);
     }
     MOE_DEV void store_scales(uint32_t at, uint32_t full) const {
       const uint32_t to = at + SCALES_A + lane_id() * 16;
@@ -177,11 +176,28 @@ struct W4 {
         sts128(to + (h * 4 + 2) * SF, w[0].z, w[1].z, w[2].z, w[3].z);
         sts128(to + (h * 4 + 3) * SF, w[0].w, w[1].w, w[2].w, w[3].w);
       }
-      arrive_scales(full);
-    }
-    MOE_DEV static void arrive_scales(uint32_t full) {
       __syncwarp();
       if (lane_id() == 0) mbar_arrive(full);
+    }
+    MOE_DEV void load(int kb, uint32_t at, uint32_t full) {
+      if (elect_one()) {
+        mbar_arrive_expect_tx(full, 2 * BLK);
+        tma_load_2d(at, map, kb * RB, row0, full, policy);
+        tma_load_2d(at + BLK, map, kb * RB, row1, full, policy);
+      }
+      __syncwarp();
+      store_scales(at, full);
+      if (kb + 1 < end) fetch_scales(kb + 1);
+    }
+  };
+
+  struct Rows {
+    const uint8_t* of;
+    size_t pitch;
+    MOE_DEV Rows(const FewArgs& a, const Smem&, const Unit& un) {
+      const bool down = un.flags & DOWN;
+      pitch = (size_t)((down ? a.I : a.H) / KB) * BLOCK_BYTES;
+      of = down ? a.act_codes : a.x_made;
     }
     MOE_DEV void load(const Smem& s, const Unit& un, int kb, uint32_t at, float* factors) const {
       const int lane = lane_id();
