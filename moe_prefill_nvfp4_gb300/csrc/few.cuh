@@ -27,7 +27,7 @@
 //   KB                       columns of a k block (of the weights' 128 bytes, one swizzle row)
 //   STAGE                    bytes of a stage: 256 weight rows of 128 bytes, then what goes with them
 //   TMEM_COLS, accumulators(most)   tensor memory, and the accumulators in it for units of that many tokens at most
-//   FULL_ARRIVALS            arrivals that make a stage full: the weights' bytes, lanes whose copies have landed
+//   WEIGHT_ARRIVALS, FULL_ARRIVALS   arrivals that make a stage full: the weights', and with the rows'
 //   Maps, held(a, e)         tensor maps by value, whether expert e is here
 //   Weights, Rows            the loads of a unit's k blocks: the weights, and the rows with their scales
 //   multiply, add            a stage's MMAs, an accumulator's scaling and addition
@@ -408,7 +408,7 @@ MOE_DEV void load_weights(const FewArgs& a, const typename F::Maps& maps, Smem& 
 
 // Loads the activation rows and all scales of the same k blocks, once they are there.
 template <class F>
-MOE_DEV void load_rows(const FewArgs& a, Smem& s, uint32_t stages) {
+MOE_DEV void load_rows(const FewArgs& a, const typename F::Maps& maps, Smem& s, uint32_t stages) {
   const int lane = lane_id();
   int i = 0, seen = -1;
   for (int n = 0;; ++n) {
@@ -416,20 +416,19 @@ MOE_DEV void load_rows(const FewArgs& a, Smem& s, uint32_t stages) {
     if (!warp_wait(s.drawn[slot], n / DRAWN & 1, s, a.err)) break;
     const Unit un = s.unit[slot];
     if (un.flags & END) break;
-    typename F::Rows rows(a, s, un);
+    typename F::Rows rows(a, maps, un);
     bool ok = true;
+    if (un.flags & DOWN && un.entry != seen) {
+      ok = wait_count(a.ready + un.entry, un.m * ((un.flags & SHARED ? a.Is : a.I) / F::KB), s, a.err);
+      seen = un.entry;
+    }
+    if (!ok) break;
+    rows.start(s, un);
     for (int kb = un.kb0; kb < un.kb1; ++kb, ++i) {
       const int st = i % NS;
       ok = warp_wait(s.empty[st], (i / NS & 1) ^ 1, s, a.err);
       if (!ok) break;
-      const uint32_t at = stages + st * F::STAGE;
-      if (un.flags & DOWN && un.entry != seen) {
-        ok = wait_count(a.ready + un.entry, un.m * ((un.flags & SHARED ? a.Is : a.I) / F::KB), s, a.err);
-        if (!ok) break;
-        seen = un.entry;
-      }
-      rows.load(s, un, kb, at, s.scales[i % NF]);
-      cp_async_arrive(smem_u32(&s.full[st]));
+      rows.load(s, un, kb, stages + st * F::STAGE, s.scales[i % NF], smem_u32(&s.full[st]));
     }
     if (!ok) break;
     __syncwarp();
@@ -437,13 +436,18 @@ MOE_DEV void load_rows(const FewArgs& a, Smem& s, uint32_t stages) {
   }
   cp_async_commit();
   cp_async_wait<0>();
-  // (after a wait that ran out: the arrivals that the stages whose weights are on their way are still short of)
+  // (after a wait that ran out: the arrivals that stages are still short of, this warp's or the weights', so that what is
+  // on its way to them can be waited for)
   if (*(volatile int*)&s.abort) {
     const uint64_t t0 = globaltimer_ns();
     while (s.issued < 0 && globaltimer_ns() - t0 < kWaitLimitNs) __nanosleep(100);
-    for (; i < s.issued; ++i) {
-      cp_async_arrive(smem_u32(&s.full[i % NS]));
-    }
+    const int issued = s.issued;
+    for (int j = i; j < issued; ++j) F::Rows::arrive(smem_u32(&s.full[j % NS]));
+    if (issued >= 0 && lane == 0)
+      for (int j = issued; j < i; ++j) {
+        for (int n = 0; n < F::WEIGHT_ARRIVALS; ++n) mbar_arrive(smem_u32(&s.full[j % NS]));
+        mbar_wait_drain(smem_u32(&s.full[j % NS]), j / NS & 1);
+      }
   }
 }
 
@@ -758,7 +762,7 @@ __global__ void __launch_bounds__(THREADS, PER_SM) few_kernel(const __grid_const
   } else if (warp < 6) {
     epilogue<F>(a, s);
   } else if (warp == 6) {
-    load_rows<F>(a, s, stages);
+    load_rows<F>(a, maps, s, stages);
   } else if (warp == 7) {
     publish<F>(a, s);
   }

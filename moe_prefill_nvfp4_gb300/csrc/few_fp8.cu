@@ -19,7 +19,7 @@ MOE_DEV void tma_load_3d(uint32_t dst, const void* tmap, int x, int y, int z, ui
 struct Fp8 {
   static constexpr int KB = BK, G = KB, LANE = 4, LEAST = 4, BLOCK_BYTES = KB;
   static constexpr int STAGE = 2 * BLK + NT * BK, TMEM_COLS = ND * 2 * NT;
-  static constexpr int FULL_ARRIVALS = 1 + 32;
+  static constexpr int WEIGHT_ARRIVALS = 1, FULL_ARRIVALS = WEIGHT_ARRIVALS + 32;
 
   struct Maps {
     CUtensorMap w[4];  // gate/up, down; the shared expert's
@@ -66,10 +66,13 @@ struct Fp8 {
 
   // A stage's rows of 128 bytes, as the MMA takes them (128-byte swizzle), and the scales.
   struct Rows {
+    const FewArgs& a_;
     const uint8_t* src[NT / 4];
     const float* sc;
     int64_t step;
-    MOE_DEV Rows(const FewArgs& a, const Smem& s, const Unit& un) {
+    MOE_DEV Rows(const FewArgs& a, const Maps&, const Unit&) : a_(a) {}
+    MOE_DEV void start(const Smem& s, const Unit& un) {
+      const FewArgs& a = a_;
       const int lane = lane_id(), piece = lane & 7;
       const bool down = un.flags & DOWN, is_shared = un.flags & SHARED;
       const int inter = is_shared ? a.Is : a.I, groups = (down ? inter : a.H) / G;
@@ -95,7 +98,7 @@ struct Fp8 {
              ((size_t)e * blocks + block) * groups + un.kb0;
       }
     }
-    MOE_DEV void load(Smem&, const Unit& un, int, uint32_t at, float* scales) {
+    MOE_DEV void load(const Smem&, const Unit& un, int, uint32_t at, float* scales, uint32_t full) {
       const int lane = lane_id(), piece = lane & 7;
 #pragma unroll
       for (int c = 0; c < NT / 4; ++c) {
@@ -105,7 +108,9 @@ struct Fp8 {
       }
       if (lane < NT + 2) cp_async4(smem_u32(scales + lane), sc);
       sc += step;
+      arrive(full);
     }
+    MOE_DEV static void arrive(uint32_t full) { cp_async_arrive(full); }
   };
 
   MOE_DEV static void multiply(uint32_t tmem, int db, uint32_t at, int, int) {

@@ -34,11 +34,21 @@ MOE_DEV void tmem_ld_32x32b_x4(uint32_t taddr, uint32_t (&r)[12]) {  // into the
                : "memory");
 }
 
-// (Issued where it stands, a block ahead of its use: the compiler would move a plain load down to that, with 16 tokens
-// in 230 us instead of 200.)
+// Loads that are issued where they stand, a block ahead of their use: the compiler would move plain ones down to that, with
+// 16 tokens in 230 us instead of 200.  Of what no kernel writes meanwhile, and of what other SMs have stored.
 MOE_DEV uint4 load_once(const void* p) {
   uint4 v;
   asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
+MOE_DEV uint4 load_l2(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.cg.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p) : "memory");
+  return v;
+}
+MOE_DEV float load_l2_f32(const void* p) {
+  float v;
+  asm volatile("ld.global.cg.f32 %0, [%1];" : "=f"(v) : "l"(p) : "memory");
   return v;
 }
 
@@ -83,22 +93,32 @@ MOE_DEV void tma_load_2d(uint32_t dst, const void* tmap, int x, int y, uint32_t 
       : "memory");
 }
 
+MOE_DEV void tma_load_4d(uint32_t dst, const void* tmap, int x, int y, int z, int u, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+      "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(u), "r"(bar)
+      : "memory");
+}
+
 struct W4 {
   static constexpr int KB = 256, LANE = 8, LEAST = 2;
   static constexpr int PIECES = 6, RB = 128;  // rows of codes to an activation row, bytes of one in a k block
-  // a block of a row: the pieces, 16 scales, the factor; in whole lines, so that an SM whose L1 has one block's does not
-  // have another's from before they were made
+  // a block of a row: the pieces, 16 scales, the factor; padded to whole lines
   static constexpr int BLOCK_BYTES = 896, SCALES = PIECES * RB, FACTOR = SCALES + 16;
   // a stage: 256 weight rows, the pieces' rows, the weight's scales, the pieces'.  Scales are as the MMA wants them:
   // of 128 rows and 64 columns 512 bytes, four scales of row r at r % 32 * 16 + r / 32 * 4.
   static constexpr int MAX_N = NT * PIECES, SF = 512, ROWS = 2 * BLK, SCALES_A = ROWS + MAX_N * RB,
                        SCALES_B = SCALES_A + 8 * SF, STAGE = SCALES_B + 4 * SF;
   static constexpr int TMEM_COLS = 256, TMEM_SCALES = 208;  // (32 columns of the weight's scales, 16 of the pieces')
-  static constexpr int FULL_ARRIVALS = 1 + 32 + 1;
+  static constexpr int WEIGHT_ARRIVALS = 2, FULL_ARRIVALS = WEIGHT_ARRIVALS + 1;
   static_assert(STAGE % 1024 == 0 && 2 * MAX_N <= TMEM_SCALES && MAX_N <= 128, "");
 
-  struct Maps {};
-  MOE_DEV static void prefetch(const FewArgs&, const Maps&) {}
+  struct Maps {
+    CUtensorMap x, act;  // rows of 128 bytes, pieces, blocks, rows of activations
+  };
+  MOE_DEV static void prefetch(const FewArgs&, const Maps& maps) {
+    if (lane_id() < 2) prefetch_tmap(lane_id() == 0 ? &maps.x : &maps.act);
+  }
   MOE_DEV static bool held(const FewArgs& a, int e) { return a.w4[0].packed[e] != nullptr && a.w4[1].packed[e] != nullptr; }
   // Columns of an accumulator's half of 128 weight rows; as many accumulators as fit.
   MOE_DEV static int columns(int m) { return (m * PIECES + 15) / 16 * 16; }
@@ -191,29 +211,52 @@ struct W4 {
     }
   };
 
+  // A token's six rows are one tile; their scales and the factor go through registers, a block ahead.
   struct Rows {
     const uint8_t* of;
+    const CUtensorMap* map;
     size_t pitch;
-    MOE_DEV Rows(const FewArgs& a, const Smem&, const Unit& un) {
+    uint4 v[MAX_N / 32];  // the block's scales of rows lane, lane + 32, ...
+    float factor;         // of token `lane`
+    MOE_DEV Rows(const FewArgs& a, const Maps& maps, const Unit& un) {
       const bool down = un.flags & DOWN;
       pitch = (size_t)((down ? a.I : a.H) / KB) * BLOCK_BYTES;
       of = down ? a.act_codes : a.x_made;
+      map = down ? &maps.act : &maps.x;
     }
-    MOE_DEV void load(const Smem& s, const Unit& un, int kb, uint32_t at, float* factors) const {
+    MOE_DEV static int row(const Smem& s, const Unit& un, int c) {
+      return un.flags & DOWN ? un.first + c : (int)s.token[un.first + c];
+    }
+    MOE_DEV void start(const Smem& s, const Unit& un) {
+      fence_proxy_async_global();  // (the rows were stored through the generic proxy)
+      fetch(s, un, un.kb0);
+    }
+    MOE_DEV void fetch(const Smem& s, const Unit& un, int kb) {
       const int lane = lane_id();
-      auto block = [&](int c) {
-        const int p = un.first + c;
-        return of + (un.flags & DOWN ? p : (int)s.token[p]) * pitch + (size_t)kb * BLOCK_BYTES;
-      };
-      for (int q = lane; q < un.m * PIECES * 8; q += 32) {
-        const int n = q / 8, piece = q % 8, c = n / PIECES;
-        cp_async16(at + ROWS + n * RB + ((piece ^ (n & 7)) << 4), block(c) + (n - c * PIECES) * RB + piece * 16, 16);
+#pragma unroll
+      for (int j = 0; j < MAX_N / 32; ++j) {
+        const int c = (lane + 32 * j) / PIECES;
+        if (c < un.m) v[j] = load_l2(of + row(s, un, c) * pitch + (size_t)kb * BLOCK_BYTES + SCALES);
       }
-      for (int q = lane; q < un.m * PIECES * 4; q += 32) {
-        const int n = q / 4, k64 = q % 4;
-        cp_async4(at + SCALES_B + k64 * SF + n % 32 * 16 + n / 32 * 4, block(n / PIECES) + SCALES + k64 * 4);
-      }
-      if (lane < un.m) cp_async4(smem_u32(factors + lane), block(lane) + FACTOR);
+      if (lane < un.m) factor = load_l2_f32(of + row(s, un, lane) * pitch + (size_t)kb * BLOCK_BYTES + FACTOR);
+    }
+    MOE_DEV void load(const Smem& s, const Unit& un, int kb, uint32_t at, float* factors, uint32_t full) {
+      const int lane = lane_id();
+      if (elect_one())
+        for (int c = 0; c < un.m; ++c) tma_load_4d(at + ROWS + c * PIECES * RB, map, 0, 0, kb, row(s, un, c), full);
+      __syncwarp();
+      const uint32_t to = at + SCALES_B + lane * 16;
+      sts128(to, v[0].x, v[1].x, v[2].x, 0);
+      sts128(to + SF, v[0].y, v[1].y, v[2].y, 0);
+      sts128(to + 2 * SF, v[0].z, v[1].z, v[2].z, 0);
+      sts128(to + 3 * SF, v[0].w, v[1].w, v[2].w, 0);
+      if (lane < un.m) factors[lane] = factor;
+      __syncwarp();
+      if (lane == 0) mbar_arrive_expect_tx(full, un.m * PIECES * RB);
+      if (kb + 1 < un.kb1) fetch(s, un, kb + 1);
+    }
+    MOE_DEV static void arrive(uint32_t full) {
+      if (lane_id() == 0) mbar_arrive(full);
     }
   };
 
@@ -276,13 +319,25 @@ struct W4 {
   }
 };
 
+// Activations [rows][blocks] of BLOCK_BYTES: tiles of the six pieces of a block.
+int rows_map(CUtensorMap* map, const uint8_t* base, int blocks, int rows) {
+  const cuuint64_t dims[4] = {W4::RB, W4::PIECES, (cuuint64_t)blocks, (cuuint64_t)rows};
+  const cuuint64_t strides[3] = {W4::RB, W4::BLOCK_BYTES, (cuuint64_t)blocks * W4::BLOCK_BYTES};
+  const cuuint32_t box[4] = {W4::RB, W4::PIECES, 1, 1}, one[4] = {1, 1, 1, 1};
+  return encode_tmap(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<uint8_t*>(base), dims, strides, box, one,
+                     CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
 }  // namespace few
 
 FewLayout few_w4_layout(int T, int H, int I, int Is, int E, int k) { return few::layout<few::W4>(T, H, I, Is, E, k); }
 
 int few_w4_launch(FewArgs& a, const FewLayout& l, void* ws, cudaStream_t st) {
   few::place(a, l, ws);
-  return few::launch<few::W4>(a, few::W4::Maps{}, st);
+  few::W4::Maps maps = {};
+  int rc = few::rows_map(&maps.x, a.x_made, a.H / few::W4::KB, a.T);
+  if (rc == MOE_OK) rc = few::rows_map(&maps.act, a.act_codes, a.I / few::W4::KB, a.T * a.k);
+  return rc == MOE_OK ? few::launch<few::W4>(a, maps, st) : rc;
 }
 
 }  // namespace moe
