@@ -10,6 +10,7 @@ import moe_prefill_nvfp4_gb300 as moe  # noqa: E402
 from moe_prefill_nvfp4_gb300 import fp8  # noqa: E402
 
 from few_helpers import Fp8Layer, W4Layer, assert_near, dequant_rows64, logits_of, rand  # noqa: E402
+from test_gpu_rms_norm import check  # noqa: E402
 
 BF16, F32, F8 = torch.bfloat16, torch.float32, torch.float8_e4m3fn
 
@@ -375,3 +376,11 @@ def test_norm_codes_are_the_nearest(k):
     got = dequant_rows64(q, torch.ones_like(s)).cuda()
     step = torch.ldexp(torch.ones_like(v), torch.frexp(v.abs().clamp(min=2.0 ** -6))[1] - 4)
     assert ((got - v).abs() <= step / 2 + v.abs() * 2.0 ** -22).all()
+
+
+@pytest.mark.parametrize("rows,k,x_type,r_type", [(400, 32768, F32, F32), (3000, 640, BF16, BF16), (2000, 1000, F32, F32), (5000, 8, BF16, None)])
+def test_norm_of_many_rows(rows, k, x_type, r_type):
+    """More rows than CTAs that the GPU holds: rows too long for shared memory, several to a CTA, the shortest."""
+    x, w = rand((rows, k), 1, 0.5, x_type), 1 + rand((k,), 2, 0.3, F32)
+    r = None if r_type is None else rand((rows, k), 3, 2.0, r_type)
+    check(x, w, r, 1e-5, *moe.moe_fp8_add_rms_norm(x, w, r, eps=1e-5, normed=True))
