@@ -5,7 +5,7 @@
 //
 // Bound by the weights' bytes: of each expert that a token has picked, once.  So everything else is kept out of
 // their way:
-//   prep  router logits (a CTA to a few experts and tokens), the tokens' rows in the form of the products' operand,
+//   prep  router logits (a CTA to an expert and four tokens), the tokens' rows in the form of the products' operand,
 //         counters to zero.
 //   few   persistent, two CTAs to an SM.  Each CTA routes the few tokens by itself (logits -> picks -> list of the
 //         picked experts: the same in all CTAs), which is shorter than a launch.  Then it draws units from a counter --
@@ -142,13 +142,13 @@ MOE_DEV bool wait_count(const int* count, int need, Smem& s, int* err) {
 
 // ------------------------------------------------------------------------------------------------
 // prep: block 0 clears the counters, blocks 1 .. T bring the tokens' rows into the operand's form (unless they are given so), the others
-// make the router's logits, of EE experts and TT tokens each
+// make the router's logits, of one expert and TT tokens each
 
-constexpr int PREP_THREADS = 256;
+constexpr int PREP_THREADS = 256, PREP_TOKENS = 4;  // (four experts to a block as well: no difference at 16 tokens)
 
-template <class F, int EE, int TT>
+template <class F, int TT>
 __global__ void __launch_bounds__(PREP_THREADS) prep_kernel(FewArgs a) {
-  __shared__ float s_part[PREP_THREADS / 32][EE * TT];
+  __shared__ float s_part[PREP_THREADS / 32][TT];
   griddep_wait();
   griddep_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -174,52 +174,43 @@ __global__ void __launch_bounds__(PREP_THREADS) prep_kernel(FewArgs a) {
     }
     return;
   }
-  // the logits of EE experts and TT tokens, whose rows come from the caches
-  const int groups = (a.E + EE - 1) / EE, at = blockIdx.x - 1 - row_blocks, e0 = at % groups * EE, t0 = at / groups * TT;
-  float acc[EE][TT];
+  // one expert's logits of TT tokens: its router row is read once, the tokens' rows come from the caches
+  const int at = blockIdx.x - 1 - row_blocks, e = at % a.E, t0 = at / a.E * TT;
+  float acc[TT];
 #pragma unroll
-  for (int e = 0; e < EE; ++e)
-#pragma unroll
-    for (int t = 0; t < TT; ++t) acc[e][t] = 0.f;
+  for (int t = 0; t < TT; ++t) acc[t] = 0.f;
   const int n = a.H / 8;
-  const uint4* w = reinterpret_cast<const uint4*>(a.w_router) + (size_t)e0 * n;
+  const uint4* w = reinterpret_cast<const uint4*>(a.w_router) + (size_t)e * n;
   const uint4* x = reinterpret_cast<const uint4*>(a.x) + (size_t)t0 * n;
-#pragma unroll (EE * TT == 1 ? 3 : 1)
+#pragma unroll (TT == 1 ? 3 : 1)
   for (int i = threadIdx.x; i < n; i += PREP_THREADS) {
-    uint4 wv[EE], xv[TT];
-#pragma unroll
-    for (int e = 0; e < EE; ++e) wv[e] = e0 + e < a.E ? w[(size_t)e * n + i] : make_uint4(0, 0, 0, 0);
+    const uint4 wv = w[i];
+    uint4 xv[TT];
 #pragma unroll
     for (int t = 0; t < TT; ++t) xv[t] = t0 + t < a.T ? x[(size_t)t * n + i] : make_uint4(0, 0, 0, 0);
+    const uint32_t ww[4] = {wv.x, wv.y, wv.z, wv.w};
 #pragma unroll
-    for (int e = 0; e < EE; ++e) {
-      const uint32_t ww[4] = {wv[e].x, wv[e].y, wv[e].z, wv[e].w};
+    for (int t = 0; t < TT; ++t) {
+      const uint32_t xx[4] = {xv[t].x, xv[t].y, xv[t].z, xv[t].w};
 #pragma unroll
-      for (int t = 0; t < TT; ++t) {
-        const uint32_t xx[4] = {xv[t].x, xv[t].y, xv[t].z, xv[t].w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          acc[e][t] = __fmaf_rn(bf16_lo(ww[j]), bf16_lo(xx[j]), acc[e][t]);
-          acc[e][t] = __fmaf_rn(bf16_hi(ww[j]), bf16_hi(xx[j]), acc[e][t]);
-        }
+      for (int j = 0; j < 4; ++j) {
+        acc[t] = __fmaf_rn(bf16_lo(ww[j]), bf16_lo(xx[j]), acc[t]);
+        acc[t] = __fmaf_rn(bf16_hi(ww[j]), bf16_hi(xx[j]), acc[t]);
       }
     }
   }
 #pragma unroll
-  for (int e = 0; e < EE; ++e)
+  for (int t = 0; t < TT; ++t) {
 #pragma unroll
-    for (int t = 0; t < TT; ++t) {
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) acc[e][t] += __shfl_xor_sync(0xffffffffu, acc[e][t], o);
-      if (lane == 0) s_part[warp][e * TT + t] = acc[e][t];
-    }
+    for (int o = 16; o > 0; o >>= 1) acc[t] += __shfl_xor_sync(0xffffffffu, acc[t], o);
+    if (lane == 0) s_part[warp][t] = acc[t];
+  }
   __syncthreads();
-  const int e = threadIdx.x / TT, t = threadIdx.x % TT;
-  if (e < EE && e0 + e < a.E && t0 + t < a.T) {
+  if (threadIdx.x < TT && t0 + (int)threadIdx.x < a.T) {
     float v = s_part[0][threadIdx.x];
 #pragma unroll
     for (int i = 1; i < PREP_THREADS / 32; ++i) v += s_part[i][threadIdx.x];
-    a.logits_ws[(size_t)(t0 + t) * a.E + e0 + e] = v;
+    a.logits_ws[(size_t)(t0 + threadIdx.x) * a.E + e] = v;
   }
 }
 
@@ -686,7 +677,7 @@ MOE_DEV void finish(const FewArgs& a, Smem& s, int drawn) {
     if (u >= blocks) {
       const int t = (u - blocks) / places, place = u - blocks - t * places;
       if (!wait_count(a.columns_done + place * 32 / 256, entries * a.slices[1], s, a.err)) return;
-      if (a.T <= 2)
+      if (a.T <= 2)  // (one token by the other form 46.6 us instead of 45.7)
         finish_columns<1, 8, 3>(a, s, place, t);
       else
         finish_columns<2, 4, 2>(a, s, place, 2 * t);
@@ -791,7 +782,7 @@ int launch(const FewArgs& a, const typename F::Maps& maps, cudaStream_t st) {
   static_assert(PER_SM * (smem + sizeof(Smem) + 1024) <= 228 * 1024 && PER_SM * F::TMEM_COLS <= 512, "CTAs per SM");
   static_assert(NS * F::STAGE >= (int)sizeof(Routing), "the routing has its arrays in the stages");
   using Prep = void (*)(FewArgs);
-  const Prep preps[3] = {prep_kernel<F, 1, 1>, prep_kernel<F, 1, 4>, prep_kernel<F, 4, 4>};
+  const Prep preps[2] = {prep_kernel<F, 1>, prep_kernel<F, PREP_TOKENS>};
   static std::atomic<uint64_t> configured{0};  // a bit per device
   const int dev = current_device_index();
   if (dev < 0) return MOE_ERR_CUDA;
@@ -804,19 +795,17 @@ int launch(const FewArgs& a, const typename F::Maps& maps, cudaStream_t st) {
       if (cudaFuncSetAttribute(p, cudaFuncAttributePreferredSharedMemoryCarveout, 100) != cudaSuccess) return MOE_ERR_CUDA;
     configured.fetch_or(1ull << (dev & 63), std::memory_order_relaxed);
   }
-  // one token's rows take no longer than their latency, so an expert to a block spreads them best; many tokens' rows are
-  // read again for each expert, or for four of them
-  const int which = a.T == 1 ? 0 : a.T <= 4 ? 1 : 2, ee = which == 2 ? 4 : 1, tt = which == 0 ? 1 : 4;
-  const int blocks = 1 + (a.x_made != nullptr ? a.T : 0) +
-                     (a.logits == nullptr ? (a.E + ee - 1) / ee * ((a.T + tt - 1) / tt) : 0);
-  const Prep prep = preps[which];
+  const int tokens = a.T == 1 ? 1 : PREP_TOKENS;
+  const int blocks = 1 + (a.x_made != nullptr ? a.T : 0) + (a.logits == nullptr ? a.E * ((a.T + tokens - 1) / tokens) : 0);
+  const Prep prep = preps[a.T == 1 ? 0 : 1];  // (one token by the other: 46.7 us instead of 45.9)
   const int rc = launch_pdl(prep, dim3(blocks), dim3(PREP_THREADS), 0, st, a);
   if (rc != MOE_OK) return rc;
   return launch_pdl(few_kernel<F>, dim3(nsm * PER_SM), dim3(THREADS), smem, st, a, maps);
 }
 
 // K blocks of a slice over `blocks` of them, of a phase of `units` units a slice: 8 (256 KB to a unit), and half of that,
-// or down to `least`, where it would leave the CTAs fewer than two units each.
+// or down to `least`, where it would leave the CTAs fewer than two units each (four each: 16 tokens at 24 experts 102 us
+// in FP8 instead of 100; one token with at least 2 k blocks in FP8 46 us, with 4 45, in NVFP4 with 1 45, with 2 41).
 inline int slice_blocks(int blocks, int64_t units, int least) {
   int want = 8;
   while (want > least && units * ((blocks + want - 1) / want) < 2 * 152 * PER_SM) want /= 2;
