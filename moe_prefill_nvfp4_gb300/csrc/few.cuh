@@ -607,58 +607,45 @@ MOE_DEV void finish_block(const FewArgs& a, Smem& s, int entry, int kb, int r) {
   if (lane_id() == 0) counter_add_release(a.ready + entry, 1);
 }
 
-// All units of 32 columns of the result are stored: the whole warp adds up slices and experts of TOKENS tokens, a lane
-// to a column, of several slots at once (their loads take a round trip to L2).
-template <int TOKENS, int SLOTS, int SLICES>
-MOE_DEV void finish_columns(const FewArgs& a, Smem& s, int place, int t0) {
+// All units of 32 columns of the result are stored: the whole warp adds up slices and experts of token t, a lane to a
+// column, of several slots and slices at once (their loads take a round trip to L2).  The sums of a slot first, in the
+// order of its slices, then the slots in theirs.
+MOE_DEV void finish_columns(const FewArgs& a, Smem& s, int place, int t) {
+  constexpr int SLOTS = 8, SLICES = 2;
   constexpr uint32_t NONE = ~0u;
   const int h = place * 32 + (threadIdx.x & 31);
-  float v[TOKENS];
-#pragma unroll
-  for (int t = 0; t < TOKENS; ++t) v[t] = 0.f;
+  float v = 0.f;
   for (int c0 = 0; c0 < a.k; c0 += SLOTS) {
-    float sum[TOKENS][SLOTS];
-    uint32_t at[TOKENS][SLOTS];  // of the slot's row (at most 528 of them), or NONE
+    float sum[SLOTS];
+    uint32_t at[SLOTS];  // of the slot's row (at most 528 of them), or NONE
 #pragma unroll
-    for (int t = 0; t < TOKENS; ++t)
-#pragma unroll
-      for (int c = 0; c < SLOTS; ++c) {
-        const int p = t0 + t < a.T && c0 + c < a.k ? s.pos[(t0 + t) * a.k + c0 + c] : -1;
-        at[t][c] = p >= 0 ? (uint32_t)p * a.H + h : NONE;
-        sum[t][c] = 0.f;
-      }
+    for (int c = 0; c < SLOTS; ++c) {
+      const int p = c0 + c < a.k ? s.pos[t * a.k + c0 + c] : -1;
+      at[c] = p >= 0 ? (uint32_t)p * a.H + h : NONE;
+      sum[c] = 0.f;
+    }
     const float* Y = a.Y;
     for (int i0 = 0; i0 < a.slices[1]; i0 += SLICES, Y += SLICES * a.y_slice) {
-      float y[SLICES][TOKENS][SLOTS];
+      float y[SLICES][SLOTS];
 #pragma unroll
       for (int i = 0; i < SLICES; ++i)
 #pragma unroll
-        for (int t = 0; t < TOKENS; ++t)
-#pragma unroll
-          for (int c = 0; c < SLOTS; ++c)
-            y[i][t][c] = at[t][c] != NONE && i0 + i < a.slices[1] ? __ldcg(Y + i * a.y_slice + at[t][c]) : 0.f;
+        for (int c = 0; c < SLOTS; ++c)
+          y[i][c] = at[c] != NONE && i0 + i < a.slices[1] ? __ldcg(Y + i * a.y_slice + at[c]) : 0.f;
 #pragma unroll
       for (int i = 0; i < SLICES; ++i)
 #pragma unroll
-        for (int t = 0; t < TOKENS; ++t)
-#pragma unroll
-          for (int c = 0; c < SLOTS; ++c) sum[t][c] += y[i][t][c];
+        for (int c = 0; c < SLOTS; ++c) sum[c] += y[i][c];
     }
 #pragma unroll
-    for (int t = 0; t < TOKENS; ++t)
-#pragma unroll
-      for (int c = 0; c < SLOTS; ++c)
-        if (at[t][c] != NONE) v[t] = __fmaf_rn(s.wts[(t0 + t) * a.k + c0 + c], sum[t][c], v[t]);
+    for (int c = 0; c < SLOTS; ++c)
+      if (at[c] != NONE) v = __fmaf_rn(s.wts[t * a.k + c0 + c], sum[c], v);
   }
-#pragma unroll
-  for (int t = 0; t < TOKENS; ++t) {
-    if (t0 + t >= a.T) break;
-    if (a.Is > 0)
-      for (int i = 0; i < a.slices[1]; ++i) v[t] += __ldcg(a.Y + (size_t)(a.T * a.k + t0 + t) * a.H + h + i * a.y_slice);
-    const size_t o = (size_t)(t0 + t) * a.H + h;
-    if (a.shared_out != nullptr) v[t] += __bfloat162float(__ushort_as_bfloat16(a.shared_out[o]));
-    a.out[o] = __bfloat16_as_ushort(__float2bfloat16_rn(v[t]));
-  }
+  if (a.Is > 0)
+    for (int i = 0; i < a.slices[1]; ++i) v += __ldcg(a.Y + (size_t)(a.T * a.k + t) * a.H + h + i * a.y_slice);
+  const size_t o = (size_t)t * a.H + h;
+  if (a.shared_out != nullptr) v += __bfloat162float(__ushort_as_bfloat16(a.shared_out[o]));
+  a.out[o] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
 }
 
 // Finishes what all its units are stored of: each entry's blocks of activations, row by row, then the columns of the
@@ -669,7 +656,7 @@ template <class F>
 MOE_DEV void finish(const FewArgs& a, Smem& s, int drawn) {
   const int sh = shared_entries(a), entries = s.routed + sh, per_row = a.I / F::KB, places = a.H / 32;
   const int shared_blocks = sh * a.T * (a.Is / F::KB), blocks = shared_blocks + s.rows * per_row;
-  const int total = blocks + places * (a.T <= 2 ? a.T : (a.T + 1) / 2);
+  const int total = blocks + places * a.T;
   for (;;) {
     const int u = __shfl_sync(0xffffffffu, drawn, 0);
     if (u >= total) return;
@@ -677,10 +664,7 @@ MOE_DEV void finish(const FewArgs& a, Smem& s, int drawn) {
     if (u >= blocks) {
       const int t = (u - blocks) / places, place = u - blocks - t * places;
       if (!wait_count(a.columns_done + place * 32 / 256, entries * a.slices[1], s, a.err)) return;
-      if (a.T <= 2)  // (one token by the other form 46.6 us instead of 45.7)
-        finish_columns<1, 8, 3>(a, s, place, t);
-      else
-        finish_columns<2, 4, 2>(a, s, place, 2 * t);
+      finish_columns(a, s, place, t);
     } else {
       int v = u, e = 0, m = a.T;
       if (u >= shared_blocks) {
