@@ -290,7 +290,6 @@ MOE_DEV void make_entries(const FewArgs& a, Smem& s, Routing& r) {
   if (tid == 0) {
     s.routed = all >> 16;
     s.rows = all & 0xFFFF;
-    s.most = max(s.most, sh ? a.T : 0);
     if (sh) s.entry[0] = Entry{-1, (short)a.T, (short)slots};
   }
   if (sh && tid < a.T) s.token[slots + tid] = (uint8_t)tid;
@@ -705,7 +704,7 @@ __global__ void __launch_bounds__(THREADS, PER_SM) few_kernel(const __grid_const
     mbar_init(smem_u32(&s.drain), 1);
     s.issued = -1;
     s.abort = 0;
-    s.most = 0;
+    s.most = shared_entries(a) ? a.T : 0;  // (from here on raised by atomics alone, of every warp that has picked experts)
     fence_barrier_init();
   }
   if (warp == 1) {
