@@ -4,12 +4,18 @@ Argument marshalling only: every function takes torch tensors, passes their devi
 and the current CUDA stream to the library of the same name, and raises ``MoeError`` on a
 non-zero status.  All computation runs in the library's kernels; there is no fallback: if the
 library is missing the import of this module's functions fails loudly.
+
+A call with ``stream=`` runs on it, and allocates its new results and workspaces on it too; it waits for
+no other stream: the caller has the inputs ready there, and waits for it before using the results elsewhere.
 """
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import functools
 import importlib.util
+import inspect
 import os
 import re
 from typing import Optional, Sequence
@@ -186,12 +192,41 @@ def _stream(stream=None):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
-def _used_on(t: torch.Tensor, stream):
-    """`t`, a workspace of this call alone, is dropped on return: its memory may be handed out again behind its
-    use on `stream` only (None: the current stream, whose allocations are ordered behind it anyway)."""
+def _on(stream):
+    """Context in which torch's own operations and allocations belong to `stream` too, as the calls that are
+    given it do.  Memory of the current stream's pool may still be used there by what is queued, and may be handed
+    out again there before `stream` has used it."""
+    if stream is None:
+        return contextlib.nullcontext()
+    return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream)
+                             else torch.cuda.ExternalStream(stream.cuda_stream))
+
+
+def _result(r, stream):
+    """Results allocated on `stream`, for the current stream to use (and to drop) once it has waited for it: a
+    tensor, or a tuple or dict of them."""
     if stream is not None:
-        t.record_stream(stream if isinstance(stream, torch.cuda.Stream)
-                        else torch.cuda.ExternalStream(stream.cuda_stream))
+        now = torch.cuda.current_stream()
+        for t in r.values() if isinstance(r, dict) else r if isinstance(r, tuple) else (r,):
+            if t is not None and t.is_cuda:
+                t.record_stream(now)
+    return r
+
+
+def _allocates(call):
+    """A call that makes its outputs and workspaces itself: on the stream that it is given."""
+    at = list(inspect.signature(call).parameters).index("stream")
+
+    @functools.wraps(call)
+    def run(*args, **kw):
+        stream = args[at] if len(args) > at else kw.get("stream")
+        if stream is None:
+            return call(*args, **kw)
+        with _on(stream):
+            r = call(*args, **kw)
+        return _result(r, stream)
+
+    return run
 
 
 def _need(t: torch.Tensor, dtype, name: str):
@@ -240,6 +275,7 @@ class ExpertTable:
 # ------------------------------------------------------------------------------------------ calls
 
 
+@_allocates
 def moe_router_logits(x: torch.Tensor, w_router: torch.Tensor, out: Optional[torch.Tensor] = None, stream=None):
     _need(x, torch.bfloat16, "x")
     _need(w_router, torch.bfloat16, "w_router")
@@ -251,6 +287,7 @@ def moe_router_logits(x: torch.Tensor, w_router: torch.Tensor, out: Optional[tor
     return out
 
 
+@_allocates
 def moe_route_topk(logits: torch.Tensor, k: int, bias: Optional[torch.Tensor] = None, renormalize: bool = True,
                    routed_scale: float = 1.0, ids=None, wts=None, stream=None):
     _need(logits, torch.float32, "logits")
@@ -268,6 +305,7 @@ def moe_sort_workspace_bytes(T: int, k: int, E: int) -> int:
     return int(lib().moe_sort_workspace_bytes(T, k, E))
 
 
+@_allocates
 def moe_sort_by_expert(ids: torch.Tensor, E: int, ws: Optional[torch.Tensor] = None, stream=None) -> dict:
     _need(ids, torch.int32, "ids")
     T, k = ids.shape
@@ -280,13 +318,13 @@ def moe_sort_by_expert(ids: torch.Tensor, E: int, ws: Optional[torch.Tensor] = N
     need = moe_sort_workspace_bytes(T, k, E)
     if ws is None:
         ws = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
-        _used_on(ws, stream)
     _check(lib().moe_sort_by_expert(_ptr(ids), T, k, E, _ptr(out["sorted_token_ids"]), _ptr(out["sorted_expert_ids"]),
                                     _ptr(out["expert_offsets"]), _ptr(out["token_to_perm"]), _ptr(ws), ws.numel(),
                                     _stream(stream)), "moe_sort_by_expert")
     return out
 
 
+@_allocates
 def moe_sort_by_expert_noalloc(ids: torch.Tensor, E: int, out: Optional[dict] = None, stream=None) -> dict:
     """moe_sort_by_expert on the library's fixed scratch (no workspace, nothing allocated by the
     library).  `out` may hold preallocated output tensors with the keys of the returned dict."""
@@ -306,6 +344,7 @@ def moe_sort_by_expert_noalloc(ids: torch.Tensor, E: int, out: Optional[dict] = 
     return out
 
 
+@_allocates
 def moe_w4a16_grouped_gemm_swiglu(A: torch.Tensor, W: ExpertTable, expert_offsets: torch.Tensor, R: int,
                                   limit: float = 7.0, gather_ids: Optional[torch.Tensor] = None,
                                   out: Optional[torch.Tensor] = None, stream=None):
@@ -323,6 +362,7 @@ def moe_w4a16_grouped_gemm_swiglu(A: torch.Tensor, W: ExpertTable, expert_offset
     return out
 
 
+@_allocates
 def moe_w4a16_grouped_gemv(A: torch.Tensor, W: ExpertTable, expert_offsets: torch.Tensor, R: int,
                            gather_ids: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None, stream=None):
     """Small-row product (<= 8 rows per expert), FP32 dequantised weights, BF16 [R, N]."""
@@ -338,6 +378,7 @@ def moe_w4a16_grouped_gemv(A: torch.Tensor, W: ExpertTable, expert_offsets: torc
     return out
 
 
+@_allocates
 def moe_w4a16_grouped_gemv_swiglu(A: torch.Tensor, W: ExpertTable, expert_offsets: torch.Tensor, R: int,
                                   limit: float = 7.0, gather_ids: Optional[torch.Tensor] = None,
                                   out: Optional[torch.Tensor] = None, stream=None):
@@ -355,6 +396,7 @@ def moe_w4a16_grouped_gemv_swiglu(A: torch.Tensor, W: ExpertTable, expert_offset
     return out
 
 
+@_allocates
 def moe_w4a16_grouped_gemm(A: torch.Tensor, W: ExpertTable, expert_offsets: torch.Tensor, R: int,
                            gather_ids: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
                            c_dtype: torch.dtype = torch.bfloat16, stream=None):
@@ -371,6 +413,7 @@ def moe_w4a16_grouped_gemm(A: torch.Tensor, W: ExpertTable, expert_offsets: torc
     return out
 
 
+@_allocates
 def moe_dequant_nvfp4(packed: torch.Tensor, scales: torch.Tensor, scale2: float, stream=None) -> torch.Tensor:
     _need(packed, torch.uint8, "packed")
     _need(scales, torch.uint8, "scales")
@@ -381,6 +424,7 @@ def moe_dequant_nvfp4(packed: torch.Tensor, scales: torch.Tensor, scale2: float,
     return out
 
 
+@_allocates
 def moe_swiglu_clamp(gate: torch.Tensor, up: torch.Tensor, limit: float, out: Optional[torch.Tensor] = None,
                      stream=None) -> torch.Tensor:
     """``gate``/``up`` may be column slices of one [R, 2I] tensor (row stride 2I)."""
@@ -396,6 +440,7 @@ def moe_swiglu_clamp(gate: torch.Tensor, up: torch.Tensor, limit: float, out: Op
     return out
 
 
+@_allocates
 def moe_combine_indexed(Y: torch.Tensor, token_to_perm: torch.Tensor, wts: torch.Tensor,
                         shared_out: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
                         stream=None) -> torch.Tensor:
@@ -421,6 +466,7 @@ def moe_workspace_layout(cfg: MoePrefillConfig, max_rows: int) -> WorkspaceLayou
     return L
 
 
+@_allocates
 def moe_prefill_forward(cfg: MoePrefillConfig, x: torch.Tensor, w_gate_up: ExpertTable, w_down: ExpertTable,
                         ws: torch.Tensor, w_router: Optional[torch.Tensor] = None,
                         logits: Optional[torch.Tensor] = None, router_bias: Optional[torch.Tensor] = None,
@@ -454,6 +500,7 @@ def moe_shared_expert_workspace_bytes(T: int, H: int, I: int) -> int:
     return int(lib().moe_shared_expert_workspace_bytes(T, H, I))
 
 
+@_allocates
 def moe_shared_expert_forward(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, w_down: torch.Tensor,
                               limit: float = 7.0, ws: Optional[torch.Tensor] = None,
                               out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
@@ -464,7 +511,6 @@ def moe_shared_expert_forward(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch
     I = w_gate.shape[0]
     if ws is None:
         ws = torch.empty(max(moe_shared_expert_workspace_bytes(T, H, I), 1), dtype=torch.uint8, device=x.device)
-        _used_on(ws, stream)
     if out is None:
         out = torch.empty(T, H, dtype=torch.bfloat16, device=x.device)
     _check(lib().moe_shared_expert_forward(_ptr(x), T, H, I, _ptr(w_gate), _ptr(w_up), _ptr(w_down), limit, _ptr(ws),
@@ -500,25 +546,46 @@ def _fp8():
     return _FP8
 
 
+class _OnStream:
+    """The FP8 calls' module with its allocations on a stream."""
+
+    def __init__(self, stream):
+        self.stream = stream
+
+    def __getattr__(self, name):
+        call = getattr(_FP8 or _fp8(), name)
+
+        def run(*args):
+            with _on(self.stream):
+                r = call(*args)
+            return _result(r, self.stream)
+
+        return run
+
+
+def _calls(stream):
+    return (_FP8 or _fp8()) if stream is None else _OnStream(stream)
+
+
 def moe_fp8_quantize_rows(x: torch.Tensor, out: Optional[torch.Tensor] = None, scales: Optional[torch.Tensor] = None,
                           stream=None):
     """Rows [R, K] (BF16 or FP32, any row stride) -> (E4M3 [R, K], FP32 [R, ceil(K/128)]): one scale
     for each 128 columns of a row.  New outputs have rows whole 16-byte pieces apart and scales stored
     group by group, the layouts the products read fastest."""
-    return (_FP8 or _fp8()).quantize(x, out, scales, stream, False)
+    return _calls(stream).quantize(x, out, scales, stream, False)
 
 
 def moe_fp8_quantize_blocks(w: torch.Tensor, out: Optional[torch.Tensor] = None, scales: Optional[torch.Tensor] = None,
                             stream=None):
     """Weight [N, K] (BF16 or FP32, any row stride) -> (E4M3 [N, K], FP32 [ceil(N/128), ceil(K/128)]): one
     scale for each 128 x 128 block."""
-    return (_FP8 or _fp8()).quantize(w, out, scales, stream, True)
+    return _calls(stream).quantize(w, out, scales, stream, True)
 
 
 def moe_fp8_gemm(A: torch.Tensor, a_scales: torch.Tensor, W: torch.Tensor, w_scales: torch.Tensor,
                  out: Optional[torch.Tensor] = None, c_dtype: torch.dtype = torch.bfloat16, stream=None) -> torch.Tensor:
     """Quantised rows A [R, K] times a quantised weight W [N, K] transposed: BF16 or FP32 [R, N]."""
-    return (_FP8 or _fp8()).gemm(A, a_scales, W, w_scales, out, c_dtype, stream)
+    return _calls(stream).gemm(A, a_scales, W, w_scales, out, c_dtype, stream)
 
 
 def moe_fp8_grouped_gemm(A: torch.Tensor, a_scales: torch.Tensor, W: torch.Tensor, w_scales: torch.Tensor,
@@ -528,7 +595,7 @@ def moe_fp8_grouped_gemm(A: torch.Tensor, a_scales: torch.Tensor, W: torch.Tenso
     """Expert-sorted rows times their expert's weight, W [experts, N, K]: BF16 or FP32 [R, N].  Sorted row p
     is row ``gather_ids[p]`` of A (row p without).  W holds the experts from ``first`` on; the others' rows
     are zeros."""
-    return (_FP8 or _fp8()).grouped(A, a_scales, W, w_scales, expert_offsets, R, gather_ids, first, out, c_dtype, stream)
+    return _calls(stream).grouped(A, a_scales, W, w_scales, expert_offsets, R, gather_ids, first, out, c_dtype, stream)
 
 
 def moe_fp8_grouped_gemm_swiglu(A: torch.Tensor, a_scales: torch.Tensor, W: torch.Tensor, w_scales: torch.Tensor,
@@ -537,8 +604,8 @@ def moe_fp8_grouped_gemm_swiglu(A: torch.Tensor, a_scales: torch.Tensor, W: torc
                                 out: Optional[torch.Tensor] = None, scales: Optional[torch.Tensor] = None, stream=None):
     """Gate/up product over W [experts, 2I, K], clamped SwiGLU, and the row quantiser on its result:
     (E4M3 [R, I], FP32 [R, I/128]), the operands of the down product."""
-    return (_FP8 or _fp8()).grouped_swiglu(A, a_scales, W, w_scales, expert_offsets, R, limit, gather_ids, first, out,
-                                           scales, stream)
+    return _calls(stream).grouped_swiglu(A, a_scales, W, w_scales, expert_offsets, R, limit, gather_ids, first, out,
+                                         scales, stream)
 
 
 def moe_fp8_add_rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Tensor] = None,
@@ -548,7 +615,7 @@ def moe_fp8_add_rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: Option
     (E4M3 [R, K], FP32 [R, ceil(K/128)], h or None without a residual, BF16 y or None).  x, residual and weight
     are BF16 or FP32 each, of any row stride; h has the residual's type, in ``residual_out`` (which may be the
     residual itself) or a new tensor.  ``normed``: True for y, or the tensor it goes to."""
-    return (_FP8 or _fp8()).add_rms_norm(x, weight, residual, eps, normed, residual_out, out, scales, stream)
+    return _calls(stream).add_rms_norm(x, weight, residual, eps, normed, residual_out, out, scales, stream)
 
 
 # ------------------------------------------------------------------------------------------ few tokens
@@ -556,12 +623,6 @@ def moe_fp8_add_rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: Option
 
 def moe_few_workspace_bytes(cfg: MoePrefillConfig, T: int, fp8: bool, shared_intermediate: int = 0) -> int:
     return int(lib().moe_few_workspace_bytes(ctypes.byref(cfg), int(fp8), shared_intermediate, T))
-
-
-def _few_ws(cfg: MoePrefillConfig, T: int, fp8: bool, shared_intermediate: int, device, stream) -> torch.Tensor:
-    ws = torch.empty(max(moe_few_workspace_bytes(cfg, T, fp8, shared_intermediate), 1), dtype=torch.uint8, device=device)
-    _used_on(ws, stream)
-    return ws
 
 
 def moe_fp8_few_forward(x: Optional[torch.Tensor], w_gate_up: torch.Tensor, s_gate_up: torch.Tensor, w_down: torch.Tensor,
@@ -576,13 +637,9 @@ def moe_fp8_few_forward(x: Optional[torch.Tensor], w_gate_up: torch.Tensor, s_ga
     ``rows``: the tokens' codes and scales where they are quantised already; x is then only the router's (None
     with ``logits``).  ``shared``: (gate_up, its scales, down, its scales) of a shared expert, clamped at
     ``shared_limit`` (default: limit).  ``ws``: a workspace of this call's own, of any contents."""
-    if ws is None and stream is not None and w_down.dim() == 3:
-        t = x if x is not None else rows[0]
-        cfg = MoePrefillConfig(t.shape[1], w_down.shape[2], num_experts or w_down.shape[0], top_k)
-        ws = _few_ws(cfg, t.shape[0], True, shared[2].shape[1] if shared is not None else 0, t.device, stream)
-    return (_FP8 or _fp8()).few_fp8(x, w_gate_up, s_gate_up, w_down, s_down, top_k, w_router, logits, router_bias, limit,
-                                    renormalize, routed_scale, num_experts, first, shared,
-                                    limit if shared_limit is None else shared_limit, rows, ws, out, stream)
+    return _calls(stream).few_fp8(x, w_gate_up, s_gate_up, w_down, s_down, top_k, w_router, logits, router_bias, limit,
+                                  renormalize, routed_scale, num_experts, first, shared,
+                                  limit if shared_limit is None else shared_limit, rows, ws, out, stream)
 
 
 def moe_w4a16_few_forward(cfg: MoePrefillConfig, x: torch.Tensor, w_gate_up: ExpertTable, w_down: ExpertTable,
@@ -591,10 +648,8 @@ def moe_w4a16_few_forward(cfg: MoePrefillConfig, x: torch.Tensor, w_gate_up: Exp
                           ws: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """A whole layer of NVFP4 experts for up to ``MOE_FEW_MAX_TOKENS`` tokens x BF16 [T, H]: BF16 [T, H], plus
     ``shared_out`` BF16 [T, H].  ``ws``: a workspace of this call's own, of any contents."""
-    if ws is None and stream is not None:
-        ws = _few_ws(cfg, x.shape[0], False, 0, x.device, stream)
-    return (_FP8 or _fp8()).few_w4(cfg, x, w_gate_up.handle, w_down.handle, w_router, logits, router_bias, shared_out, ws, out,
-                                   stream)
+    return _calls(stream).few_w4(cfg, x, w_gate_up.handle, w_down.handle, w_router, logits, router_bias, shared_out, ws, out,
+                                 stream)
 
 
 def moe_get_device_error(stream=None) -> int:
@@ -615,6 +670,7 @@ def moe_debug_set_wait_limit_ns(ns: int) -> int:
     return int(lib().moe_debug_set_wait_limit_ns(int(ns)))
 
 
+@_allocates
 def moe_debug_grouped_gemm_after(A: torch.Tensor, W: ExpertTable, expert_offsets: torch.Tensor, R: int,
                                  ready: torch.Tensor, ready_need: int, gather_ids: Optional[torch.Tensor] = None,
                                  out: Optional[torch.Tensor] = None, c_dtype: torch.dtype = torch.float32,

@@ -14,30 +14,14 @@ prints their times and distances from the same experts in FP32.
 
 from __future__ import annotations
 
-import contextlib
 from typing import Optional
 
 import torch
 
 from . import _lib as moe
+from ._lib import _on, _result
 
 __all__ = ["Fp8Weight", "Fp8SharedExpert", "Fp8Experts"]
-
-
-def _on(stream):
-    """Context in which torch's own operations and allocations belong to `stream` too, as the calls that are
-    given it do: what a forward drops on return is then handed out again behind its last use."""
-    if stream is None:
-        return contextlib.nullcontext()
-    return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream)
-                             else torch.cuda.ExternalStream(stream.cuda_stream))
-
-
-def _result(t: torch.Tensor, stream) -> torch.Tensor:
-    """A result allocated on `stream`, for the current stream to use (and to drop) once it has waited for it."""
-    if stream is not None:
-        t.record_stream(torch.cuda.current_stream())
-    return t
 
 
 class Fp8Weight:
