@@ -89,6 +89,9 @@ class Fp8Experts:
         waits for it before it uses the result elsewhere."""
         if (w_router is None) == (logits is None):
             raise ValueError("forward: exactly one of w_router and logits")
+        # (the gathers and the combine go by x's tokens: rows of fewer tokens would be read past their end)
+        if rows is not None and (len(rows) != 2 or rows[0].shape != x.shape or rows[1].shape[0] != x.shape[0]):
+            raise ValueError(f"rows: need codes {tuple(x.shape)} and their scales, got {[tuple(t.shape) for t in rows]}")
         with _on(stream):
             if logits is None:
                 logits = moe.moe_router_logits(x, w_router, stream=stream)
