@@ -716,6 +716,9 @@ __global__ void __launch_bounds__(THREADS, PER_SM) few_kernel(const __grid_const
     r.tokens[e] = 0;
     r.held[e] = F::held(a, e);
   }
+  // (A CTA whose tensor memory another kernel's CTA on its SM still has would keep what it has drawn until that one is
+  // gone, and all others waiting: it draws once it can work.  The grid before this one hides the barrier.)
+  __syncthreads();
   griddep_wait();
   griddep_launch_dependents();
   // (the first draws' answers come while the tokens are routed)
