@@ -170,10 +170,13 @@ __global__ void __maxnreg__(C == 1 ? 64 : 128) ring_kernel(RmsNormArgs a, int de
     return p / 8 * G + p % 8 * 8 + half * 64;
   };
   int slot = 0, parity = 0, part = 0;
+  bool live = true;  // no wait has run out
   for (int64_t row = blockIdx.x; row < a.R; row += n_rows) {
     const void *xs = x + row * x_pitch, *rs = r + row * r_pitch;
     if (depth > 0) {
-      mbar_wait_warp(smem_u32(&full[slot]), parity, &s_abort, a.err);  // (a row whose wait ran out has wrong values, and the error is set)
+      // (a row whose wait ran out has wrong values, and the error is set; no row is fetched from then on, as its slot may
+      // be one that is still waited for)
+      live &= mbar_wait_warp(smem_u32(&full[slot]), parity, &s_abort, a.err);
       xs = ring + slot * (x_bytes + r_bytes);
       rs = ring + slot * (x_bytes + r_bytes) + x_bytes;
     }
@@ -201,7 +204,7 @@ __global__ void __maxnreg__(C == 1 ? 64 : 128) ring_kernel(RmsNormArgs a, int de
     if (lane == 0) s_part[part][tid >> 5] = sum;
     __syncthreads();  // (the row's sums are there, its shared memory is read, and the parts of the row before it)
     if (depth > 0) {
-      if (tid == 0 && row + depth * n_rows < a.R) fetch(row + depth * n_rows, slot);
+      if (tid == 0 && live && row + depth * n_rows < a.R) fetch(row + depth * n_rows, slot);
       if (++slot == depth) {
         slot = 0;
         parity ^= 1;
@@ -242,7 +245,7 @@ __global__ void __maxnreg__(C == 1 ? 64 : 128) ring_kernel(RmsNormArgs a, int de
       }
     }
   }
-  if (tid == 0 && s_abort)
+  if (tid == 0 && !live)
     for (int i = 0; i < depth; ++i) {  // no copy may still be on its way into a CTA that is gone
       mbar_wait_drain(smem_u32(&full[i]), 0);
       mbar_wait_drain(smem_u32(&full[i]), 1);
