@@ -85,7 +85,7 @@ struct Smem {
   alignas(16) float scales[NF][F_SLOT];
   uint32_t tmem;
   int routed, rows, most, abort;     // picked experts, their rows, tokens of one at most
-  volatile int issued;               // k blocks whose weights were loaded, -1 before the end
+  int weights_issued, rows_issued;   // k blocks whose weights and whose rows were loaded, once their loaders have ended
   float wts[MAX_SLOTS];
   short pos[MAX_SLOTS];              // row of slot (t, s), -1: of an expert held elsewhere
   uint8_t token[MAX_SLOTS + MAX_T];  // of row p
@@ -395,10 +395,7 @@ MOE_DEV void load_weights(const FewArgs& a, const typename F::Maps& maps, Smem& 
     if (!load(u1)) break;
     u1 = draw(a.counters);
   }
-  // (after a wait that ran out: no copy may still be on its way into a CTA that is gone)
-  if (lane == 0) s.issued = i;
-  if (*(volatile int*)&s.abort && lane == 0)
-    for (int j = max(0, i - NS); j < i; ++j) mbar_wait_drain(smem_u32(&s.full[j % NS]), j / NS & 1);
+  if (lane == 0) s.weights_issued = i;
 }
 
 // Loads the activation rows and all scales of the same k blocks, once they are there.
@@ -431,19 +428,7 @@ MOE_DEV void load_rows(const FewArgs& a, const typename F::Maps& maps, Smem& s, 
   }
   cp_async_commit();
   cp_async_wait<0>();
-  // (after a wait that ran out: the arrivals that stages are still short of, this warp's or the weights', so that what is
-  // on its way to them can be waited for)
-  if (*(volatile int*)&s.abort) {
-    const uint64_t t0 = globaltimer_ns();
-    while (s.issued < 0 && globaltimer_ns() - t0 < kWaitLimitNs) __nanosleep(100);
-    const int issued = s.issued;
-    for (int j = i; j < issued; ++j) F::Rows::arrive(smem_u32(&s.full[j % NS]));
-    if (issued >= 0 && lane == 0)
-      for (int j = issued; j < i; ++j) {
-        for (int n = 0; n < F::WEIGHT_ARRIVALS; ++n) mbar_arrive(smem_u32(&s.full[j % NS]));
-        mbar_wait_drain(smem_u32(&s.full[j % NS]), j / NS & 1);
-      }
-  }
+  if (lane == 0) s.rows_issued = i;
 }
 
 // Issues the MMAs of every stage, with an accumulator to each k block.
@@ -477,13 +462,6 @@ MOE_DEV void multiply(const FewArgs& a, Smem& s, uint32_t stages) {
         turn ^= 1;
       }
     }
-  }
-  if (!ok) {
-    if (elect_one()) {
-      mma_commit(smem_u32(&s.drain));
-      mbar_wait_drain(smem_u32(&s.drain), 0);
-    }
-    __syncwarp();
   }
 }
 
@@ -679,6 +657,28 @@ MOE_DEV void finish(const FewArgs& a, Smem& s, int drawn) {
   }
 }
 
+// After a wait that ran out, whichever, and with all roles ended: waits for the copies and MMAs that are on their way, as
+// none may be in a CTA that is gone.  One loader may have ended ahead of the other, or both after others gave up: the
+// arrivals that a stage is short of are made here.
+template <class F>
+MOE_DEV void drain(Smem& s) {
+  if (threadIdx.x >> 5 == 1) {  // (the elected lane is the one that has issued the MMAs)
+    if (elect_one()) {
+      mma_commit(smem_u32(&s.drain));
+      mbar_wait_drain(smem_u32(&s.drain), 0);
+    }
+    __syncwarp();
+  } else if (threadIdx.x == 0) {
+    const int weights = s.weights_issued, rows = s.rows_issued, end = max(weights, rows);
+    for (int j = max(0, end - NS); j < end; ++j) {
+      const uint32_t full = smem_u32(&s.full[j % NS]);
+      const int missing = (j >= weights ? F::WEIGHT_ARRIVALS : 0) + (j >= rows ? F::FULL_ARRIVALS - F::WEIGHT_ARRIVALS : 0);
+      for (int n = 0; n < missing; ++n) mbar_arrive(full);
+      mbar_wait_drain(full, j / NS & 1);
+    }
+  }
+}
+
 template <class F>
 __global__ void __launch_bounds__(THREADS, PER_SM) few_kernel(const __grid_constant__ FewArgs a,
                                                                const __grid_constant__ typename F::Maps maps) {
@@ -702,7 +702,7 @@ __global__ void __launch_bounds__(THREADS, PER_SM) few_kernel(const __grid_const
       mbar_init(smem_u32(&s.stored[i]), 4);
     }
     mbar_init(smem_u32(&s.drain), 1);
-    s.issued = -1;
+    s.weights_issued = s.rows_issued = 0;
     s.abort = 0;
     s.most = shared_entries(a) ? a.T : 0;  // (from here on raised by atomics alone, of every warp that has picked experts)
     fence_barrier_init();
@@ -748,12 +748,13 @@ __global__ void __launch_bounds__(THREADS, PER_SM) few_kernel(const __grid_const
   } else if (warp == 7) {
     publish<F>(a, s);
   }
-  __syncwarp();
-  if (s.routed + shared_entries(a) > 0 && !*(volatile int*)&s.abort)
+  // (the whole warp or none of it)
+  if (s.routed + shared_entries(a) > 0 && !__any_sync(0xffffffffu, *(volatile int*)&s.abort))
     finish<F>(a, s, warp >= 8 ? u0 : draw(a.counters + 32));
   __syncwarp();
   tc_fence_before();
   __syncthreads();
+  if (s.abort) drain<F>(s);
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(s.tmem, F::TMEM_COLS);

@@ -108,9 +108,8 @@ struct Fp8 {
       }
       if (lane < NT + 2) cp_async4(smem_u32(scales + lane), sc);
       sc += step;
-      arrive(full);
+      cp_async_arrive(full);
     }
-    MOE_DEV static void arrive(uint32_t full) { cp_async_arrive(full); }
   };
 
   MOE_DEV static void multiply(uint32_t tmem, int db, uint32_t at, int, int) {

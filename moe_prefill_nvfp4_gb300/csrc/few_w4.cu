@@ -255,9 +255,6 @@ struct W4 {
       if (lane == 0) mbar_arrive_expect_tx(full, un.m * PIECES * RB);
       if (kb + 1 < un.kb1) fetch(s, un, kb + 1);
     }
-    MOE_DEV static void arrive(uint32_t full) {
-      if (lane_id() == 0) mbar_arrive(full);
-    }
   };
 
   MOE_DEV static void multiply(uint32_t tmem, int db, uint32_t at, int m, int most) {
