@@ -563,8 +563,9 @@ int moe_workspace_layout(const moe_prefill_config* cfg, int max_rows, moe_worksp
  * points return MOE_ERR_UNSUPPORTED_SHAPE for the others.  Returns MOE_ERR_INVALID_ARG for
  * another value.
  *
- * moe_debug_set_wait_limit_ns: the bound of every pipeline wait of the CTA-pair kernel
- * (default and maximum 2 s; 0 restores the default).  After the bound a waiting kernel records
+ * moe_debug_set_wait_limit_ns: the bound of every pipeline wait of the CTA-pair kernel, the shared
+ * expert's products, the FP8 products, the norm and the few-token layers (default and maximum 2 s;
+ * 0 restores the default; the single-CTA kernel keeps the default).  After the bound a waiting kernel records
  * MOE_DEVERR_TIMEOUT, drains its copies and MMAs and returns.  Returns the previous bound.
  */
 #define MOE_GEMM_KERNEL_AUTO 0

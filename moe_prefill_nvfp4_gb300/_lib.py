@@ -666,7 +666,7 @@ def moe_debug_set_gemm_kernel(which: int) -> None:
 
 
 def moe_debug_set_wait_limit_ns(ns: int) -> int:
-    """Bound of the CTA-pair GEMM's pipeline waits (0 restores 2 s); returns the previous bound."""
+    """Bound of the pipeline waits of all kernels but the single-CTA GEMM (0 restores 2 s); returns the previous bound."""
     return int(lib().moe_debug_set_wait_limit_ns(int(ns)))
 
 

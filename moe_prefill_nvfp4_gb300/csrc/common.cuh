@@ -102,18 +102,20 @@ MOE_DEV bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, 
   }
 }
 
-// A whole warp's wait, with one outcome for all its lanes.  The timer is looked at once in a while only: reading it
-// takes longer than most waits for a copy that was issued early.
-MOE_DEV bool mbar_wait_warp(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* err) {
+// A whole warp's wait, with one outcome for all its lanes.  The timer is looked at once in a while only, as reading it
+// takes longer than most waits for a copy that was issued early -- but after every poll where the limit is shorter than
+// 64 of them take.
+constexpr uint64_t kShortLimitNs = 1000000ull;
+MOE_DEV bool mbar_wait_warp(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* err, uint64_t limit) {
   bool ok = mbar_try_wait(bar, parity);
   if (!__all_sync(0xffffffffu, ok)) {
     uint64_t t0 = 0;
     for (int n = 0; !ok; ++n) {
       ok = mbar_try_wait_sleep(bar, parity, kSleepHintNs);
       if (ok || *abort_flag) break;
-      if (n % 64 == 63) {
+      if (n % 64 == 63 || limit < kShortLimitNs) {
         if (t0 == 0) t0 = globaltimer_ns();
-        if (globaltimer_ns() - t0 > kWaitLimitNs) {
+        if (globaltimer_ns() - t0 > limit) {
           *abort_flag = 1;
           set_error(err, MOE_DEVERR_TIMEOUT);
         }

@@ -26,7 +26,7 @@
 // the down products, 5 from the last sums to the result.
 //
 // Units and tasks are drawn behind all that they need, so whichever CTAs are running make progress, also beside another
-// call's kernel that holds a part of the SMs.  Every wait is bounded (MOE_DEVERR_TIMEOUT).
+// call's kernel that holds a part of the SMs.  Every wait is bounded (FewArgs::wait_ns, MOE_DEVERR_TIMEOUT).
 //
 // What differs between the weights' formats is in a class F:
 //   KB                       columns of a k block (of the weights' 128 bytes, one swizzle row)
@@ -112,10 +112,12 @@ MOE_DEV uint64_t streaming_policy() {
 
 MOE_DEV uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
 
-MOE_DEV bool warp_wait(uint64_t& bar, uint32_t parity, Smem& s, int* err) { return mbar_wait_warp(smem_u32(&bar), parity, &s.abort, err); }
+MOE_DEV bool warp_wait(uint64_t& bar, uint32_t parity, Smem& s, const FewArgs& a) {
+  return mbar_wait_warp(smem_u32(&bar), parity, &s.abort, a.err, a.wait_ns);
+}
 
 // Waits for a count of what other warps have stored and published (a poll is a round trip to L2).
-MOE_DEV bool wait_count(const int* count, int need, Smem& s, int* err) {
+MOE_DEV bool wait_count(const int* count, int need, Smem& s, const FewArgs& a) {
   int ok = 1;
   if (lane_id() == 0) {
     uint64_t t0 = 0;
@@ -125,11 +127,11 @@ MOE_DEV bool wait_count(const int* count, int need, Smem& s, int* err) {
       if (v >= need) break;
       ok = !*(volatile int*)&s.abort;
       if (!ok) break;
-      if (n % 64 == 0) {
+      if (n % 64 == 0 || a.wait_ns < kShortLimitNs) {
         if (t0 == 0) t0 = globaltimer_ns();
-        if (globaltimer_ns() - t0 > kWaitLimitNs) {
-          s.abort = 1;
-          set_error(err, MOE_DEVERR_TIMEOUT);
+        if (globaltimer_ns() - t0 > a.wait_ns) {
+          *(volatile int*)&s.abort = 1;
+          set_error(a.err, MOE_DEVERR_TIMEOUT);
         }
       }
       __nanosleep(50);
@@ -370,7 +372,7 @@ MOE_DEV void load_weights(const FewArgs& a, const typename F::Maps& maps, Smem& 
   int i = 0, n = 0;
   auto load = [&](int drawn) {  // false: there is nothing left, or a wait ran out
     const int u = __shfl_sync(0xffffffffu, drawn, 0), slot = n % DRAWN;
-    if (!warp_wait(s.spent[slot], (n / DRAWN & 1) ^ 1, s, a.err)) return false;
+    if (!warp_wait(s.spent[slot], (n / DRAWN & 1) ^ 1, s, a)) return false;
     Unit un = {};
     un.flags = END;
     if (u < us.total) un = unit_at<F>(a, s, us, u);
@@ -383,7 +385,7 @@ MOE_DEV void load_weights(const FewArgs& a, const typename F::Maps& maps, Smem& 
     typename F::Weights weights(a, maps, un);
     for (int kb = un.kb0; kb < un.kb1; ++kb, ++i) {
       const int st = i % NS;
-      if (!warp_wait(s.empty[st], (i / NS & 1) ^ 1, s, a.err)) return false;
+      if (!warp_wait(s.empty[st], (i / NS & 1) ^ 1, s, a)) return false;
       weights.load(kb, stages + st * F::STAGE, smem_u32(&s.full[st]));
     }
     return true;
@@ -405,20 +407,20 @@ MOE_DEV void load_rows(const FewArgs& a, const typename F::Maps& maps, Smem& s, 
   int i = 0, seen = -1;
   for (int n = 0;; ++n) {
     const int slot = n % DRAWN;
-    if (!warp_wait(s.drawn[slot], n / DRAWN & 1, s, a.err)) break;
+    if (!warp_wait(s.drawn[slot], n / DRAWN & 1, s, a)) break;
     const Unit un = s.unit[slot];
     if (un.flags & END) break;
     typename F::Rows rows(a, maps, un);
     bool ok = true;
     if (un.flags & DOWN && un.entry != seen) {
-      ok = wait_count(a.ready + un.entry, un.m * ((un.flags & SHARED ? a.Is : a.I) / F::KB), s, a.err);
+      ok = wait_count(a.ready + un.entry, un.m * ((un.flags & SHARED ? a.Is : a.I) / F::KB), s, a);
       seen = un.entry;
     }
     if (!ok) break;
     rows.start(s, un);
     for (int kb = un.kb0; kb < un.kb1; ++kb, ++i) {
       const int st = i % NS;
-      ok = warp_wait(s.empty[st], (i / NS & 1) ^ 1, s, a.err);
+      ok = warp_wait(s.empty[st], (i / NS & 1) ^ 1, s, a);
       if (!ok) break;
       rows.load(s, un, kb, stages + st * F::STAGE, s.scales[i % NF], smem_u32(&s.full[st]));
     }
@@ -439,7 +441,7 @@ MOE_DEV void multiply(const FewArgs& a, Smem& s, uint32_t stages) {
   bool ok = true;
   for (int n = 0; ok; ++n) {
     const int slot = n % DRAWN;
-    ok = warp_wait(s.drawn[slot], n / DRAWN & 1, s, a.err);
+    ok = warp_wait(s.drawn[slot], n / DRAWN & 1, s, a);
     if (!ok) break;
     const int flags = s.unit[slot].flags, blocks = s.unit[slot].kb1 - s.unit[slot].kb0, m = s.unit[slot].m;
     __syncwarp();
@@ -447,7 +449,7 @@ MOE_DEV void multiply(const FewArgs& a, Smem& s, uint32_t stages) {
     if (lane_id() == 0) mbar_arrive(smem_u32(&s.spent[slot]));
     for (int j = 0; j < blocks; ++j, ++i) {
       const int st = i % NS;
-      ok = warp_wait(s.full[st], i / NS & 1, s, a.err) && warp_wait(s.d_empty[db], turn ^ 1, s, a.err);
+      ok = warp_wait(s.full[st], i / NS & 1, s, a) && warp_wait(s.d_empty[db], turn ^ 1, s, a);
       if (!ok) break;
       fence_proxy_async_shared();  // (the rows came through the generic proxy)
       tc_fence_after();
@@ -474,7 +476,7 @@ MOE_DEV void epilogue(const FewArgs& a, Smem& s) {
   int i = 0, db = 0, turn = 0;
   for (int n = 0;; ++n) {
     const int slot = n % DRAWN;
-    if (!warp_wait(s.drawn[slot], n / DRAWN & 1, s, a.err)) return;
+    if (!warp_wait(s.drawn[slot], n / DRAWN & 1, s, a)) return;
     const Unit un = s.unit[slot];
     __syncwarp();
     if (un.flags & END) return;
@@ -483,7 +485,7 @@ MOE_DEV void epilogue(const FewArgs& a, Smem& s) {
 #pragma unroll
     for (int j = 0; j < NT / 2; ++j) acc[0][j] = acc[1][j] = 0;
     for (int kb = un.kb0; kb < un.kb1; ++kb, ++i) {
-      if (!warp_wait(s.d_full[db], turn, s, a.err)) return;
+      if (!warp_wait(s.d_full[db], turn, s, a)) return;
       tc_fence_after();
       F::add(acc, lane_base, db, s.scales[i % NF], un.m, s.most, smem_u32(&s.d_empty[db]));
       if (++db == nd) {
@@ -519,10 +521,10 @@ template <class F>
 MOE_DEV void publish(const FewArgs& a, Smem& s) {
   for (int n = 0;; ++n) {
     const int slot = n % DRAWN;
-    if (!warp_wait(s.drawn[slot], n / DRAWN & 1, s, a.err)) return;
+    if (!warp_wait(s.drawn[slot], n / DRAWN & 1, s, a)) return;
     const int flags = s.unit[slot].flags, entry = s.unit[slot].entry, place = s.unit[slot].place;
     if (flags & END) return;
-    if (!warp_wait(s.stored[slot], n / DRAWN & 1, s, a.err)) return;
+    if (!warp_wait(s.stored[slot], n / DRAWN & 1, s, a)) return;
     __syncwarp();
     if (lane_id() == 0) {
       mbar_arrive(smem_u32(&s.spent[slot]));
@@ -640,7 +642,7 @@ MOE_DEV void finish(const FewArgs& a, Smem& s, int drawn) {
     drawn = draw(a.counters + 32);
     if (u >= blocks) {
       const int t = (u - blocks) / places, place = u - blocks - t * places;
-      if (!wait_count(a.columns_done + place * 32 / 256, entries * a.slices[1], s, a.err)) return;
+      if (!wait_count(a.columns_done + place * 32 / 256, entries * a.slices[1], s, a)) return;
       finish_columns(a, s, place, t);
     } else {
       int v = u, e = 0, m = a.T;
@@ -651,7 +653,7 @@ MOE_DEV void finish(const FewArgs& a, Smem& s, int drawn) {
         v -= s.entry[e].first * per_row;
       }
       const int kb = v / m;
-      if (!wait_count(a.block_done + e * a.blocks_max + kb, a.slices[0] * F::KB / 128, s, a.err)) return;
+      if (!wait_count(a.block_done + e * a.blocks_max + kb, a.slices[0] * F::KB / 128, s, a)) return;
       finish_block<F>(a, s, e, kb, v - kb * m);
     }
   }

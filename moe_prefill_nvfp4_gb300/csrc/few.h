@@ -36,6 +36,7 @@ struct FewArgs {
   const uint16_t* shared_out;  // NULL, or BF16 [T, H] to add
   uint16_t* out;               // BF16 [T, H]
   int* err;
+  uint64_t wait_ns;            // bound of every wait
   // workspace
   int *counters, *ready, *block_done, *columns_done;
   int n_counters, blocks_max;

@@ -48,6 +48,7 @@ int common(const moe_prefill_config* c, const uint16_t* x, int T, const uint16_t
   a.routed_scale = c->routed_scale;
   a.limit = c->swiglu_limit;
   a.out = out;
+  a.wait_ns = gemm_wait_limit_ns();
   l = fp8 ? few_fp8_layout(T, a.H, a.I, a.Is, a.E, a.k) : few_w4_layout(T, a.H, a.I, a.Is, a.E, a.k);
   return ws_bytes < l.total ? MOE_ERR_WORKSPACE_TOO_SMALL : MOE_OK;
 }

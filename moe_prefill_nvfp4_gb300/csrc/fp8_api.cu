@@ -119,6 +119,7 @@ int moe_fp8_add_rms_norm(const void* x, int x_dtype, int64_t ld_x, const void* r
   if (rc != MOE_OK || R == 0) return rc;
   RmsNormArgs a = {};
   a.err = device_error_word();
+  a.wait_ns = gemm_wait_limit_ns();
   a.x = x;
   a.r = r;
   a.w = w;

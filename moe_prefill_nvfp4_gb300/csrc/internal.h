@@ -185,6 +185,7 @@ struct RmsNormArgs {
   float eps;
   bool x_bf16, r_bf16, w_bf16;
   int* err;
+  uint64_t wait_ns;
 };
 int rms_norm_launch(const RmsNormArgs& a, cudaStream_t st);
 

@@ -176,7 +176,7 @@ __global__ void __maxnreg__(C == 1 ? 64 : 128) ring_kernel(RmsNormArgs a, int de
     if (depth > 0) {
       // (a row whose wait ran out has wrong values, and the error is set; no row is fetched from then on, as its slot may
       // be one that is still waited for)
-      live &= mbar_wait_warp(smem_u32(&full[slot]), parity, &s_abort, a.err);
+      live &= mbar_wait_warp(smem_u32(&full[slot]), parity, &s_abort, a.err, a.wait_ns);
       xs = ring + slot * (x_bytes + r_bytes);
       rs = ring + slot * (x_bytes + r_bytes) + x_bytes;
     }
