@@ -792,12 +792,16 @@ int launch(const FewArgs& a, const typename F::Maps& maps, cudaStream_t st) {
   return launch_pdl(few_kernel<F>, dim3(nsm * PER_SM), dim3(THREADS), smem, st, a, maps);
 }
 
+// The SMs of a whole GB300, whatever the device at hand: the slices of k are the order of the sums and the size of the
+// workspace, which is asked for without a device, and neither may change with a part of a GPU.
+constexpr int SLICED_FOR_SMS = 152;
+
 // K blocks of a slice over `blocks` of them, of a phase of `units` units a slice: 8 (256 KB to a unit), and half of that,
 // or down to `least`, where it would leave the CTAs fewer than two units each (four each: 16 tokens at 24 experts 102 us
 // in FP8 instead of 100; one token with at least 2 k blocks in FP8 46 us, with 4 45, in NVFP4 with 1 45, with 2 41).
 inline int slice_blocks(int blocks, int64_t units, int least) {
   int want = 8;
-  while (want > least && units * ((blocks + want - 1) / want) < 2 * 152 * PER_SM) want /= 2;
+  while (want > least && units * ((blocks + want - 1) / want) < 2 * SLICED_FOR_SMS * PER_SM) want /= 2;
   const int slices = (blocks + want - 1) / want;
   return (blocks + slices - 1) / slices;
 }
