@@ -113,11 +113,15 @@ MOE_DEV float finish(float (&h)[N], const float (&w)[N], float inv, uint32_t (&c
   float scale;
   // in pairs, where nothing overflows or is rounded to a subnormal, and y's floor of 2^-100 is not the scale's
   if (most > 0x1p-60f && most < 0x1p100f && amax > __uint_as_float(kFp8AmaxFloorBits) && amax < 0x1p100f) {
+    // 448 / most = b + bl to 2^-44, a quotient of double length: the remainder of an approximate one, exact in an FMA, by
+    // the reciprocal again (Dekker, A floating-point technique for extending the available precision, 1971)
     float r;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(most));
-    const float b = 448.f * r, bl = __fmaf_rn(-b, most, 448.f) * r;  // 448 / most = b + bl, to 2^-44
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(most));  // (to 2^-23)
+    const float b = 448.f * r, bl = __fmaf_rn(-b, most, 448.f) * r;
 #pragma unroll
     for (int i = 0; i < N; ++i) v[i] = __fmaf_rn(h[i], b, __fmaf_rn(h[i], bl, lo[i] * b));
+    // amax / 448, the quotient by the rounded reciprocal corrected with its remainder (Markstein, Computation of elementary
+    // functions on the IBM RISC System/6000 processor, 1990): the nearest number for every amax here
     const float s = amax * (1.f / 448.f);
     scale = __fmaf_rn(__fmaf_rn(-448.f, s, amax), 1.f / 448.f, s);
   } else {
