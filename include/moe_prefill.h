@@ -430,12 +430,12 @@ typedef struct {
  *
  * cfg: hidden, moe_intermediate, num_experts (<= MOE_FEW_MAX_EXPERTS), top_k (<= 32), swiglu_limit (> 0, infinity
  * clamps nothing), renormalize, routed_scale; flags 0 or MOE_FWD_NO_MULTICAST (there is none to leave out).
- *   x          device BF16 [T, H], 1 <= T <= MOE_FEW_MAX_TOKENS
- *   w_router   device BF16 [E, H] or NULL; logits device FP32 [T, E] or NULL (exactly one of them);
+ *   x          device BF16 [T, H], 1 <= T <= MOE_FEW_MAX_TOKENS, on a 16-byte boundary
+ *   w_router   device BF16 [E, H], on a 16-byte boundary, or NULL; logits device FP32 [T, E] or NULL (exactly one of them);
  *   router_bias device FP32 [E] or NULL (selection only)
  *   ws         device workspace of moe_few_workspace_bytes, 256-byte aligned; its contents need not be kept or
  *              cleared between calls, and calls that can overlap need one each
- *   out        device BF16 [T, H]
+ *   out        device BF16 [T, H]; may be x itself
  * No host round trip: capturable.  A call that shares the GPU with another kernel waits for no CTA that is not
  * running.
  *
