@@ -20,8 +20,8 @@
 // and brings them into the operand's form; another such task adds up slices and experts of 32 columns of the result.
 // No sum depends on who was last.
 //
-// Kernel time (160 experts, top-8, 5120 x 1536, in graphs of calls with other tokens): one token 45 us in FP8 and 39 in
-// NVFP4, 16 tokens 317 and 201; the picked weights' bytes take 28 and 16, 311 and 175 us.  What is above that is latency:
+// Kernel time (160 experts, top-8, 5120 x 1536, in graphs of calls with other tokens): one token 46 us in FP8 and 40 in
+// NVFP4, 16 tokens 316 and 202; the picked weights' bytes take 28 and 16, 311 and 175 us.  What is above that is latency:
 // 4 us of logits, 4 of routing, 5 to the first stages (their code comes from L2 too), 4 between the last gate/up sums and
 // the down products, 5 from the last sums to the result.
 //

@@ -16,8 +16,9 @@
 //   any   4 columns to a thread, 32 apart, a warp to a group: element loads and stores that still coalesce
 // 8192 rows of 5120 columns, all in BF16, take 64 us, 5.9 TB/s (a CTA to a row without the ring 76, three or four CTAs of
 // 64 or 48 registers 64 and 65, five of 40 registers 107; three rows ahead instead of two 69).  2048 rows without a
-// residual, whose 21 MB come from L2, take 13.4 us: there it is bound by its instructions (11.3 with codes from y in
-// single FP32 numbers, whose error against FP64 was 1.1 to 1.5 times as large).
+// residual, whose 21 MB come from L2, take 13.4 us, and 6.0 more for every 1024: three CTAs need 2.6 us to a row each, for
+// its chain from the copy to the codes and for their instructions, half of an SM's issue slots (2048 rows 11.3 us with
+// codes from y in single FP32 numbers, whose error against FP64 was 1.1 to 1.5 times as large).
 
 #include <algorithm>
 #include <atomic>
